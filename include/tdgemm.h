@@ -411,6 +411,104 @@ int64_t tdg_mfma_probe_sink_floats(void);
 int tdg_lds_probe(int mode, int64_t iters, uint32_t *out, void *stream);
 int64_t tdg_lds_probe_bytes(int mode, int64_t iters);
 
+/* ---- Rows that pick their own weights: rows sorted by expert and back, the
+ * experts' products, and low-rank adapters beside a shared projection.  The
+ * rules above hold here too: device pointers owned by the caller, nothing
+ * allocated or synchronised, work enqueued on `stream`, argument errors before
+ * any HIP call, TDG_ERR_NO_DEVICE off gfx950, thread-safe.  Outputs (and a
+ * workspace) may not overlap each other or an input; sizes are 0 .. 2^31 -
+ * 2^16; leading dimensions and strides are in elements; every array is aligned
+ * to its element.  Shapes past one launch's grid (over 16 million rows, or
+ * rows past 65535 workgroups) are TDG_ERR_UNSUPPORTED.  Results are the same
+ * from run to run.  Ids, slots and offsets are read on the device and never
+ * lead a read or write outside the arrays as described here, whatever they
+ * hold. */
+
+/* Element of the rows that tdg_rows_* move. */
+typedef enum { TDG_ELEM_F16 = 0, TDG_ELEM_F32 = 1 } tdg_elem;
+
+/* The plan of a routed layer.  Each of `tokens` tokens names top_k experts:
+ * ids[t * ld_ids + j], entry e = t * top_k + j.  Entries whose id lies outside
+ * [0, experts) (say -1, a padding token's) are dropped.  The kept ones are
+ * sorted by expert, in entry order within an expert (the same expert twice is
+ * two entries):
+ *   offsets[g]  kept entries with an id below g, g = 0 .. experts: expert g's
+ *               rows are offsets[g] .. offsets[g + 1] - 1 of the sorted rows;
+ *   slots[e]    the entry's sorted row, -1 when dropped;
+ *   order[i]    the entry of sorted row i, -1 from offsets[experts] on.
+ * offsets holds experts + 1 values, slots and order tokens * top_k, dense.
+ * 1 <= experts <= 1024, top_k >= 1, tokens * top_k <= 2^30.  The workspace
+ * (tdg_route_workspace: 0 up to 4096 entries, then the counts of each
+ * workgroup; at most 1 MiB) is 4-byte aligned; its contents on return are
+ * unspecified. */
+int tdg_route_workspace(int64_t tokens, int64_t top_k, int64_t experts, size_t *bytes);
+int tdg_route_plan(int64_t tokens, int64_t top_k, int64_t experts, const int32_t *ids, int64_t ld_ids,
+                   int32_t *offsets, int32_t *order, int32_t *slots, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/* Rows by slot: tokens x cols token rows on one side, rows x cols sorted rows
+ * on the other, slots (dense tokens x top_k) as tdg_route_plan writes them:
+ * distinct where they are not -1.  A slot outside [0, rows) has no row: it is
+ * neither read nor written.  Sorted rows that no slot names are left as they
+ * were.
+ *   dispatch       out[slot(t, j)] = x[t], bit for bit;
+ *   combine        y[t] = sum over j of w[t][j] * z[slot(t, j)], summed in
+ *                  FP32 in the order of j and rounded once (0 for a token
+ *                  with no row); weights NULL means 1, which makes it the
+ *                  dispatch's gradient;
+ *   combine_grad   dz[slot(t, j)] = w[t][j] * dy[t] (rounded once) and
+ *                  dweights[t][j] = sum over columns of dy[t] * z[slot(t, j)]
+ *                  in FP32 (0 for an entry with no row).
+ * row_elem is the sorted rows' element, token_elem the token rows'; weights
+ * and dweights are FP32 with leading dimensions ld_weights, ld_dweights.
+ * tokens * top_k <= 2^30. */
+int tdg_rows_dispatch(int elem, int64_t tokens, int64_t top_k, int64_t cols, const void *x, int64_t ldx,
+                      const int32_t *slots, int64_t rows, void *out, int64_t ldo, void *stream);
+int tdg_rows_combine(int row_elem, int token_elem, int64_t tokens, int64_t top_k, int64_t cols, const void *z,
+                     int64_t ldz, int64_t rows, const int32_t *slots, const float *weights, int64_t ld_weights,
+                     void *y, int64_t ldy, void *stream);
+int tdg_rows_combine_grad(int row_elem, int token_elem, int64_t tokens, int64_t top_k, int64_t cols,
+                          const void *dy, int64_t ldy, const void *z, int64_t ldz, int64_t rows,
+                          const int32_t *slots, const float *weights, int64_t ld_weights, void *dz, int64_t lddz,
+                          float *dweights, int64_t ld_dweights, void *stream);
+
+/* The experts' products, FP16 -> FP32.  Group g holds rows offsets[g] ..
+ * offsets[g + 1] - 1 (offsets: groups + 1 ascending device values, as
+ * tdg_route_plan writes them; clamped to the row count), 0 <= groups <= 1024:
+ *   grouped      C[i] = A[i] . B_g     A: M x K, B_g: K x N, C: M x N;
+ *   grouped_nt   C[i] = A[i] . B_g^T   A: M x K, B_g: N x K, C: M x N: the
+ *                gradient of `grouped`'s A, from C's gradient and the same B;
+ *   grouped_tn   C_g = A[g]^T . B[g]   A: rows x M, B: rows x N, C_g: M x N:
+ *                the gradient of its B; zeros for a group without rows.
+ * B_g is at B + g * stride_b, C_g at C + g * stride_c.  Rows of C that belong
+ * to no group are left as they were. */
+int gemm_f16f32_grouped(int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, const uint16_t *A,
+                        int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b, float *C, int64_t ldc,
+                        void *stream);
+int gemm_f16f32_grouped_nt(int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K,
+                           const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b,
+                           float *C, int64_t ldc, void *stream);
+int gemm_f16f32_grouped_tn(int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N,
+                           const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, float *C, int64_t ldc,
+                           int64_t stride_c, void *stream);
+
+/* A shared projection with low-rank adapters of many requests beside it,
+ * FP16 -> FP32: C[t] = A[t] . B + scale[a] * (A[t] . down[a]) . up[a] with
+ * a = adapter[t]; a row whose a lies outside [0, adapters) (say -1) gets the
+ * shared product alone, and no row is touched by another's adapter.
+ * down[a] is K x rank at down + a * stride_down, up[a] rank x N at
+ * up + a * stride_up; scale may be NULL (1 for all); A . down is kept to at
+ * least 21 bits.  0 <= rank <= TDG_LORA_MAX_RANK.  The workspace
+ * (tdg_lora_workspace) is 16-byte aligned; its contents on return are
+ * unspecified. */
+#define TDG_LORA_MAX_RANK 256
+int tdg_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank, size_t *bytes);
+int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda, const uint16_t *B,
+                     int64_t ldb, int64_t adapters, int64_t rank, const uint16_t *down, int64_t ld_down,
+                     int64_t stride_down, const uint16_t *up, int64_t ld_up, int64_t stride_up,
+                     const int32_t *adapter, const float *scale, float *C, int64_t ldc, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

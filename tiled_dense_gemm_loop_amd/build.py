@@ -1,7 +1,8 @@
 """Build libtdgemm.so, the gfx950 GEMM library, in-tree with hipcc.
 
 The kernel tables for the three dtypes are separate translation units and are
-compiled in parallel with the host API and the copy/transpose ladder.  All
+compiled in parallel with the host API, the copy/transpose ladder and the
+products whose rows pick their own weights.  All
 HIP code is compiled for gfx950 only, with packed-FP32 instruction selection
 turned off.
 """
@@ -34,6 +35,9 @@ UNITS = [
     ("tdg_probe.hip", [], "tdg_probe.o"),
     ("tdg_reduce.hip", [], "tdg_reduce.o"),
     ("tdg_noalloc.hip", [], "tdg_noalloc.o"),
+    ("tdg_route.hip", [], "tdg_route.o"),
+    ("tdg_grouped.hip", [], "tdg_grouped.o"),
+    ("tdg_lora.hip", [], "tdg_lora.o"),
 ]
 
 

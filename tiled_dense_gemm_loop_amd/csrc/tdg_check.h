@@ -1,0 +1,51 @@
+// tdg_check.h -- argument checks shared by the operators whose rows pick
+// their weights (routed rows, grouped products, adapters).  Host code only;
+// nothing here calls HIP.
+#pragma once
+
+#include <stdint.h>
+
+namespace tdg {
+
+// Largest rows, columns or k: the kernels form (tile start + tile extent) on
+// 32-bit indices, so every size keeps a margin of 2^16 below 2^31.
+constexpr int64_t kMaxSize = ((int64_t)1 << 31) - ((int64_t)1 << 16);
+
+inline bool size_ok(int64_t n) { return n >= 0 && n <= kMaxSize; }
+
+// A row-major rows x cols matrix of `es`-byte elements: leading dimension at
+// least max(1, cols), a pointer unless it is empty, its bytes within int64.
+inline bool matrix_ok(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+    if (ld < (cols > 1 ? cols : 1)) return false;
+    if (rows > 0 && ld > INT64_MAX / es / rows) return false;
+    return p || rows == 0 || cols == 0;
+}
+
+// `count` such matrices, `stride` elements apart (rows * ld fits: checked
+// before).  Matrices that share memory are refused when `apart` (outputs).
+inline bool stack_ok(const void *p, int64_t count, int64_t stride, int64_t rows, int64_t cols, int64_t ld,
+                     int64_t es, bool apart) {
+    if (!matrix_ok(count > 0 ? p : (const void *)1, rows, cols, ld, es)) return false;
+    if (count <= 1) return true;
+    if (stride < 0 || stride > INT64_MAX / es / 2 / count) return false;
+    return !apart || rows == 0 || cols == 0 || stride >= (rows - 1) * ld + cols;
+}
+
+// Bytes from a matrix's (or a stack's) first element through its last.
+inline uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t es, int64_t count = 1,
+                           int64_t stride = 0) {
+    if (rows <= 0 || cols <= 0 || count <= 0) return 0;
+    return (uint64_t)((count - 1) * stride + (rows - 1) * ld + cols) * (uint64_t)es;
+}
+
+inline bool overlaps(const void *a, uint64_t alen, const void *b, uint64_t blen) {
+    if (!a || !b || !alen || !blen) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + blen && y < x + alen;
+}
+
+inline bool aligned_to(const void *p, uintptr_t bytes) { return (uintptr_t)p % bytes == 0; }
+
+inline int64_t ceil_quot(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace tdg
