@@ -20,6 +20,7 @@ namespace tdg {
 
 // TDG_DEBUG_* bits passed to every GEMM launch (tdg_set_debug_flags).
 static std::atomic<int> debug_flags{0};
+int debug_flags_now() { return debug_flags.load(std::memory_order_relaxed); }
 
 // The three dtype tables, concatenated once.
 const KernelEntry *kernel_table(int *count) {

@@ -1,6 +1,7 @@
 // tdg_grouped.hip -- host side of the products whose rows pick their weights:
 // gemm_f16f32_grouped, _nt and _tn.
 #include "tdg_grouped.hpp"
+#include <stdlib.h>
 
 #include "tdg_check.h"
 #include "tdg_internal.h"
@@ -45,6 +46,39 @@ int grouped_args_ok(int lay, int64_t groups, const int32_t *offsets, int64_t row
     return TDG_OK;
 }
 
+struct Variant {
+    const void *fn;
+    int bm, bn, threads;
+};
+
+#define TDG_BY_LAYOUT(KERNEL, ...)                                              \
+    (lay == tdg::LAY_NN   ? (const void *)&tdg::KERNEL<tdg::LAY_NN, __VA_ARGS__> \
+     : lay == tdg::LAY_NT ? (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__> \
+                          : (const void *)&tdg::KERNEL<tdg::LAY_TN, __VA_ARGS__>)
+
+Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+    const bool tn = lay == tdg::LAY_TN;
+    // The DMA copies whole 16-byte chunks of a row: the row lengths that it
+    // cuts into chunks have to be multiples of 8.  Its lanes reach a tile's
+    // rows with 32-bit byte offsets.
+    const bool chunks = (tn ? M : K) % 8 == 0 && (lay == tdg::LAY_NT ? K : N) % 8 == 0;
+    const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
+    if (!chunks || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256};
+    const int64_t tall = tn ? M : rows / groups;  // rows of C in a group, on average
+    static const char *force = getenv("TDG_FORCE");
+    int f = force ? atoi(force) : 0;
+    if (!f) f = tn ? 1 : tall <= 48 ? 3 : tall < 192 ? 2 : 1;
+    if (f == 1) return {TDG_BY_LAYOUT(tdg_grouped_ring, 256, 256, 2, 4, 2), 256, 256, 512};
+    if (f == 2) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 3), 128, 128, 256};
+    if (f == 4) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256};
+    if (f == 5) return {TDG_BY_LAYOUT(tdg_grouped_ring, 256, 128, 2, 2, 2), 256, 128, 256};
+    if (f == 6 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 64, 1, 2, 6), 32, 64, 128};
+    if (f == 7 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 128, 2, 2, 4), 64, 128, 256};
+    if (f == 8 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 128, 1, 4, 3), 32, 128, 256};
+    if (f == 9 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 64, 1, 2, 4), 32, 64, 128};
+    return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 128, 1, 4, 6), 32, 128, 256};
+}
+
 int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, int64_t K,
                 const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b, void *C, int64_t ldc,
                 int64_t stride_c, void *stream) {
@@ -52,27 +86,25 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     if (rc != TDG_OK) return rc;
     if (groups == 0 || N == 0 || (lay == tdg::LAY_TN ? M == 0 : rows == 0)) return TDG_OK;
 
-    constexpr int BM = 128, BN = 128, NT = 256;
-    const void *fn = lay == tdg::LAY_NN   ? (const void *)&tdg::tdg_grouped_any<tdg::LAY_NN, BM, BN, 2, 2>
-                     : lay == tdg::LAY_NT ? (const void *)&tdg::tdg_grouped_any<tdg::LAY_NT, BM, BN, 2, 2>
-                                          : (const void *)&tdg::tdg_grouped_any<tdg::LAY_TN, BM, BN, 2, 2>;
+    const Variant v = choose(lay, groups, rows, M, N, K, lda, ldb);
     GroupedArgs a;
     a.A = (const unsigned char *)A, a.B = (const unsigned char *)B, a.C = (unsigned char *)C;
     a.lda = lda * 2, a.ldb = ldb * 2, a.ldc = ldc * 4;
     a.stride_b = stride_b * 2, a.stride_c = stride_c * 4;
     a.offsets = offsets;
     a.groups = (int)groups, a.rows = (int)rows, a.M = (int)M, a.N = (int)N, a.K = (int)K;
-    a.tiles_m = (int)tdg::ceil_quot(M, BM), a.tiles_n = (int)tdg::ceil_quot(N, BN);
+    a.tiles_m = (int)tdg::ceil_quot(M, v.bm), a.tiles_n = (int)tdg::ceil_quot(N, v.bn);
+    a.flags = tdg::debug_flags_now();
     // Most tiles: every group can end inside a tile, and needs a row for it.
     const int64_t row_tiles = lay == tdg::LAY_TN ? groups * a.tiles_m
-                                                 : rows / BM + (groups < rows ? groups : rows);
+                                                 : rows / v.bm + (groups < rows ? groups : rows);
     if (row_tiles > INT32_MAX / a.tiles_n) return TDG_ERR_UNSUPPORTED;
     const int64_t grid = tdg::ceil_quot(row_tiles * a.tiles_n, 8) * 8;
-    if (grid > (int64_t)UINT32_MAX / NT) return TDG_ERR_UNSUPPORTED;
+    if (grid > (int64_t)UINT32_MAX / v.threads) return TDG_ERR_UNSUPPORTED;
     rc = tdg::device_check();
     if (rc != TDG_OK) return rc;
     void *kargs[] = {&a};
-    if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(NT), kargs, 0, (hipStream_t)stream) != hipSuccess)
+    if (hipLaunchKernel(v.fn, dim3((unsigned)grid), dim3((unsigned)v.threads), kargs, 0, (hipStream_t)stream) != hipSuccess)
         return TDG_ERR_LAUNCH;
     if (hipGetLastError() != hipSuccess) return TDG_ERR_LAUNCH;
     return TDG_OK;

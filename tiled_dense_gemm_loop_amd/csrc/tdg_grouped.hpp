@@ -36,6 +36,7 @@ struct GroupedArgs {
     int M, N, K;   // M: TN only (columns of A); K: NN and NT only
     int tiles_m;   // TN only: ceil(M / BM)
     int tiles_n;   // ceil(N / BN)
+    int flags;     // TDG_DEBUG_* bits
 };
 
 // One operand's LDS image: BX rows (or columns) of the product, 64 k.
@@ -181,82 +182,73 @@ __device__ static __forceinline__ void store_tile(unsigned char *C, int64_t ldc,
         }
 }
 
+// One operand chunk of eight elements, any size, stride and alignment: whole
+// chunks are one 16-byte load, a chunk that a row's end cuts is read element
+// by element, so no byte outside an operand's rows is ever read; what lies
+// outside [.., row_end) x [.., col_end) is zero.
+__device__ static __forceinline__ u32x4 load_chunk(const unsigned char *P, int64_t ld, int row, int row_end, int col,
+                                                   int col_end) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (row < row_end && col < col_end) {
+        const unsigned char *p = P + (int64_t)row * ld + (int64_t)col * 2;
+        const int left = col_end - col;
+        if (left >= 8) {
+            v = load16_global(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; e++)
+                if (e < left) {
+                    const uint32_t b = *(const TDG_GLOBAL uint16_t *)(p + 2 * e);
+                    v[e / 2] |= b << (16 * (e & 1));
+                }
+        }
+    }
+    return v;
+}
+
 // Any sizes, strides and alignments: tiles go through registers, tile t+1
-// loading while tile t is computed, two LDS buffers.  A 16-byte chunk that a
-// row's end cuts is read element by element, so no byte outside an operand's
-// rows is ever read; what lies outside is zero in LDS.
+// loading while tile t is computed, two LDS buffers.
 template <int LAY, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a) {
+struct GroupedAny {
     typedef Image<LAY != LAY_TN, BM> IA;
     typedef Image<LAY == LAY_NT, BN> IB;
-    constexpr int NT = WM * WN * 64;
-    constexpr int CA = IA::CHUNKS / NT, CB = IB::CHUNKS / NT;
+    static constexpr int NT = WM * WN * 64;
+    static constexpr int CA = IA::CHUNKS / NT, CB = IB::CHUNKS / NT;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, MI = WTM / 32, NI = WTN / 32;
+    static constexpr int STAGE = IA::BYTES + IB::BYTES, SMEM = 2 * STAGE;
     static_assert(IA::CHUNKS % NT == 0 && IB::CHUNKS % NT == 0, "tile must split evenly over threads");
-    constexpr int WTM = BM / WM, WTN = BN / WN, MI = WTM / 32, NI = WTN / 32;
-    constexpr int STAGE = IA::BYTES + IB::BYTES;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * STAGE];
 
-    const GroupedTile t = find_tile<LAY, BM>(a);
-    if (!t.ok) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % WM, wn = wave / WM;
-    // The product's rows are x in [x0, x_end) of A, its columns y in [y0, N)
-    // of B, its k in [k_lo, k_hi).
-    const int x0 = LAY == LAY_TN ? t.tm * BM : t.lo + t.tm * BM, x_end = LAY == LAY_TN ? a.M : t.hi;
-    const int y0 = t.tn * BN, y_end = a.N;
-    const int k_lo = LAY == LAY_TN ? t.lo : 0, k_hi = LAY == LAY_TN ? t.hi : a.K;
-    const unsigned char *A = a.A, *B = a.B + (LAY == LAY_TN ? 0 : (int64_t)t.g * a.stride_b);
-    const int nt = (k_hi - k_lo + 63) / 64;
-
-    auto load = [&](const unsigned char *P, int64_t ld, bool kc, int q, int cpr, int swz, int x, int x_hi,
-                    int k0) -> u32x4 {
-        const int r = q / cpr, c = ((q % cpr) ^ swz) * 8;
-        const int row = kc ? x + r : k0 + r, row_hi = kc ? x_hi : k_hi;
-        const int col = kc ? k0 + c : x + c, col_hi = kc ? k_hi : x_hi;
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (row < row_hi && col < col_hi) {
-            const unsigned char *p = P + (int64_t)row * ld + (int64_t)col * 2;
-            const int left = col_hi - col;
-            if (left >= 8) {
-                v = load16_global(p);
-            } else {
+    // acc += the tile's product over k in [k_lo, k_hi).  Rows (TN: columns) of
+    // A from x0 to x_end, columns (NT: rows) of B from y0 to y_end.
+    __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, const unsigned char *B,
+                                               int64_t ldb, int x0, int x_end, int y0, int y_end, int k_lo,
+                                               int k_hi, unsigned char *smem, f32x16 (&acc)[MI][NI]) {
+        const int nt = (k_hi - k_lo + 63) >> 6;
+        if (nt <= 0) return;
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave % WM, wn = wave / WM;
+        u32x4 ra[CA], rb[CB];
+        auto load_tile = [&](int kt) {
+            const int k0 = k_lo + kt * 64;
 #pragma unroll
-                for (int e = 0; e < 7; e++)
-                    if (e < left) {
-                        const uint32_t b = *(const TDG_GLOBAL uint16_t *)(p + 2 * e);
-                        v[e / 2] |= b << (16 * (e & 1));
-                    }
+            for (int i = 0; i < CA; i++) {
+                const int q = i * NT + tid, r = q / IA::CPR, c = ((q % IA::CPR) ^ IA::swz(r)) * 8;
+                ra[i] = LAY != LAY_TN ? load_chunk(A, lda, x0 + r, x_end, k0 + c, k_hi)
+                                      : load_chunk(A, lda, k0 + r, k_hi, x0 + c, x_end);
             }
-        }
-        return v;
-    };
-    u32x4 ra[CA], rb[CB];
-    auto load_tile = [&](int kt) {
-        const int k0 = k_lo + kt * 64;
 #pragma unroll
-        for (int i = 0; i < CA; i++) {
-            const int q = i * NT + tid;
-            ra[i] = load(A, a.lda, LAY != LAY_TN, q, IA::CPR, IA::swz(q / IA::CPR), x0, x_end, k0);
-        }
+            for (int i = 0; i < CB; i++) {
+                const int q = i * NT + tid, r = q / IB::CPR, c = ((q % IB::CPR) ^ IB::swz(r)) * 8;
+                rb[i] = LAY == LAY_NT ? load_chunk(B, ldb, y0 + r, y_end, k0 + c, k_hi)
+                                      : load_chunk(B, ldb, k0 + r, k_hi, y0 + c, y_end);
+            }
+        };
+        auto store_lds = [&](unsigned char *st) {
 #pragma unroll
-        for (int i = 0; i < CB; i++) {
-            const int q = i * NT + tid;
-            rb[i] = load(B, a.ldb, LAY == LAY_NT, q, IB::CPR, IB::swz(q / IB::CPR), y0, y_end, k0);
-        }
-    };
-    auto store_lds = [&](unsigned char *st) {
+            for (int i = 0; i < CA; i++) lds_write16(st + (i * NT + tid) * 16, ra[i]);
 #pragma unroll
-        for (int i = 0; i < CA; i++) lds_write16(st + (i * NT + tid) * 16, ra[i]);
-#pragma unroll
-        for (int i = 0; i < CB; i++) lds_write16(st + IA::BYTES + (i * NT + tid) * 16, rb[i]);
-    };
-
-    f32x16 acc[MI][NI];
-#pragma unroll
-    for (int mi = 0; mi < MI; mi++)
-#pragma unroll
-        for (int ni = 0; ni < NI; ni++) acc[mi][ni] = f32x16{};
-    if (nt > 0) {
+            for (int i = 0; i < CB; i++) lds_write16(st + IA::BYTES + (i * NT + tid) * 16, rb[i]);
+        };
         load_tile(0);
         store_lds(smem);
         __syncthreads();
@@ -282,8 +274,236 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a)
             }
         }
     }
-    unsigned char *C = a.C + (LAY == LAY_TN ? (int64_t)t.g * a.stride_c : 0);
-    store_tile<MI, NI>(C, a.ldc, x0 + wm * WTM, x_end, y0 + wn * WTN, y_end, acc);
+};
+
+// Rows whose length is a whole number of 16-byte chunks: global-to-LDS DMA
+// (global_load_lds_dwordx4, from any byte address), a ring of STAGES buffers
+// with STAGES - 1 tiles in flight, fragments read three k steps ahead and the
+// copies of a later tile spread over the MFMAs of two steps: the schedule of
+// the plain product's direct loop.  Edges cost no test in the loop: a lane
+// whose row or column lies past the tile's end copies the last one instead
+// (it only feeds C elements that are not stored), and only the tile that the
+// end of k cuts takes its chunks past that end from a block of zeros.
+template <int LAY, int BM, int BN, int WM, int WN, int STAGES>
+struct GroupedRing {
+    typedef Image<LAY != LAY_TN, BM> IA;
+    typedef Image<LAY == LAY_NT, BN> IB;
+    static constexpr int NT = WM * WN * 64;
+    static constexpr int CA = IA::CHUNKS / NT, CB = IB::CHUNKS / NT, ND = CA + CB;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, MI = WTM / 32, NI = WTN / 32;
+    static constexpr int STAGE = IA::BYTES + IB::BYTES, SMEM = STAGES * STAGE;
+    static constexpr int A_STEP = NT / IA::CPR, B_STEP = NT / IB::CPR;  // image rows per chunk index
+    static constexpr int AHEAD = STAGES - 1;
+    static_assert(IA::CHUNKS % NT == 0 && IB::CHUNKS % NT == 0, "tile must split evenly over threads");
+    static_assert(A_STEP % 16 == 0 || (LAY == LAY_TN && A_STEP % 4 == 0), "A swizzle must repeat");
+    static_assert(B_STEP % 16 == 0 || (LAY != LAY_NT && B_STEP % 4 == 0), "B swizzle must repeat");
+    static_assert(STAGES >= 2 && AHEAD * ND <= 63 && SMEM <= 160 * 1024, "ring");
+
+    // acc += the tile's product over k in [k_lo, k_hi).  Rows of A from x0 to
+    // x_end, columns (NT: rows) of B from y0 to y_end; P, ld as they sit in
+    // memory.
+    __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, const unsigned char *B,
+                                               int64_t ldb, int x0, int x_end, int y0, int y_end, int k_lo,
+                                               int k_hi, unsigned char *smem, f32x16 (&acc)[MI][NI]) {
+        const int nt = (k_hi - k_lo + 63) >> 6;
+        if (nt <= 0) return;
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave % WM, wn = wave / WM;
+        const uint32_t smem_addr = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)smem;
+        constexpr bool AKC = LAY != LAY_TN, BKC = LAY == LAY_NT;
+
+        // Per-lane byte offsets of the thread's chunks from the tile's first
+        // row and k.  KC: one per chunk (the rows are clamped); RC: one for
+        // all (the k rows advance with the wave-uniform base).
+        const int a_r = tid / IA::CPR, a_c = (tid % IA::CPR) ^ IA::swz(a_r);
+        const int b_r = tid / IB::CPR, b_c = (tid % IB::CPR) ^ IB::swz(b_r);
+        uint32_t a_off[AKC ? CA : 1], b_off[BKC ? CB : 1];
+#pragma unroll
+        for (int i = 0; i < (AKC ? CA : 1); i++)
+            a_off[i] = AKC ? (uint32_t)(min(i * A_STEP + a_r, x_end - 1 - x0) * lda + a_c * 16)
+                           : (uint32_t)(a_r * lda + min(a_c * 8, x_end - 8 - x0) * 2);
+#pragma unroll
+        for (int i = 0; i < (BKC ? CB : 1); i++)
+            b_off[i] = BKC ? (uint32_t)(min(i * B_STEP + b_r, y_end - 1 - y0) * ldb + b_c * 16)
+                           : (uint32_t)(b_r * ldb + min(b_c * 8, y_end - 8 - y0) * 2);
+        const unsigned char *a_base =
+            A + (AKC ? (int64_t)x0 * lda + (int64_t)k_lo * 2 : (int64_t)k_lo * lda + (int64_t)x0 * 2);
+        const unsigned char *b_base =
+            B + (BKC ? (int64_t)y0 * ldb + (int64_t)k_lo * 2 : (int64_t)k_lo * ldb + (int64_t)y0 * 2);
+        const uint64_t zero_addr = (uint64_t)(uintptr_t)tdg_zero16;
+        auto issue = [&](uint32_t st, int kt, int d, auto checked) __attribute__((always_inline)) {
+            const bool is_a = d < CA;
+            const int i = is_a ? d : d - CA;
+            const uint32_t m0 = smem_addr + st + (uint32_t)wave * 1024u +
+                                (uint32_t)((is_a ? 0 : IA::BYTES) + i * NT * 16);
+            kt = __builtin_amdgcn_readfirstlane(kt);
+            const unsigned char *base =
+                is_a ? a_base + (AKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * A_STEP) * lda)
+                     : b_base + (BKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * B_STEP) * ldb);
+            const uint32_t off = is_a ? a_off[AKC ? i : 0] : b_off[BKC ? i : 0];
+            if constexpr (decltype(checked)::value) {
+                // first k of the chunk, counted from the tile's
+                const int k = is_a ? (AKC ? a_c * 8 : i * A_STEP + a_r) : (BKC ? b_c * 8 : i * B_STEP + b_r);
+                const uint64_t p = (uint64_t)(uintptr_t)(base + off);
+                const uint64_t src = k < k_hi - k_lo - kt * 64 ? p : zero_addr;
+                asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+            } else {
+                asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
+            }
+        };
+
+        // Fragment reads: KC one offset per step, RC one per 32-wide block
+        // (the swizzle of a k row repeats every four rows).
+        uint32_t fa_off[AKC ? 4 : MI], fb_off[BKC ? 4 : NI];
+#pragma unroll
+        for (int i = 0; i < (AKC ? 4 : MI); i++)
+            fa_off[i] = AKC ? IA::frag(lane, wm * WTM, i, 0) : IA::frag(lane, wm * WTM + i * 32, 0, 0);
+#pragma unroll
+        for (int i = 0; i < (BKC ? 4 : NI); i++)
+            fb_off[i] = IA::BYTES + (BKC ? IB::frag(lane, wn * WTN, i, 0) : IB::frag(lane, wn * WTN + i * 32, 0, 0));
+        auto read_a = [&](const unsigned char *st, int s, int mi) __attribute__((always_inline)) -> u32x4 {
+            if constexpr (AKC) return lds_read16(st + fa_off[s] + mi * 32 * 128);
+            else return Mfma<DT_F16>::read_b(st + fa_off[mi] + (s * 16) * IA::ROWB,
+                                             st + fa_off[mi] + (s * 16 + 4) * IA::ROWB);
+        };
+        auto read_b = [&](const unsigned char *st, int s, int ni) __attribute__((always_inline)) -> u32x4 {
+            if constexpr (BKC) return lds_read16(st + fb_off[s] + ni * 32 * 128);
+            else return Mfma<DT_F16>::read_b(st + fb_off[ni] + (s * 16) * IB::ROWB,
+                                             st + fb_off[ni] + (s * 16 + 4) * IB::ROWB);
+        };
+        constexpr int FD = 3;
+        u32x4 fa[4][MI], fb[4][NI];
+
+        // One k step's MFMAs, with the fragment reads of step rs (of buffer
+        // rst) and copies [lo, hi) of tile dma_kt spread between them.
+        auto step = [&](int s, const unsigned char *rst, int rs, uint32_t dma_st, int dma_kt, int lo, int hi,
+                        auto checked) __attribute__((always_inline)) {
+            constexpr int NM = MI * NI, NR = MI + NI;
+#pragma unroll
+            for (int m = 0; m < NM; m++) {
+                acc[m / NI][m % NI] = Mfma<DT_F16>::mac_sub(fa[s][m / NI], fb[s][m % NI], acc[m / NI][m % NI], 0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = (m * NR + NM - 1) / NM; u < ((m + 1) * NR + NM - 1) / NM; u++) {
+                    if (u < MI) fa[rs][u] = read_a(rst, rs, u);
+                    else fb[rs][u - MI] = read_b(rst, rs, u - MI);
+                }
+                const int nd = hi - lo;
+#pragma unroll
+                for (int d = (m * nd + NM - 1) / NM; d < ((m + 1) * nd + NM - 1) / NM; d++)
+                    issue(dma_st, dma_kt, lo + d, checked);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto stage = [&](int t) { return (uint32_t)((t % STAGES) * STAGE); };
+
+        // Tiles from t_chk on may copy the tile that the end of k cuts.
+        const bool cut = ((k_hi - k_lo) & 63) != 0;
+        const int chk = cut ? nt - 1 : nt;
+        // Prologue: every buffer is free.  Past the last tile, the last one
+        // is copied again (into a buffer that is not read any more), so the
+        // copies in flight at each wait are a constant.
+#pragma unroll
+        for (int p = 0; p <= AHEAD; p++) {
+            const int kt = min(p, nt - 1);
+            if (kt >= chk) {
+#pragma unroll
+                for (int d = 0; d < ND; d++) issue(stage(p), kt, d, std::true_type{});
+            } else {
+#pragma unroll
+                for (int d = 0; d < ND; d++) issue(stage(p), kt, d, std::false_type{});
+            }
+        }
+        wait_vmcnt<AHEAD * ND>();
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < FD; s++) {
+#pragma unroll
+            for (int mi = 0; mi < MI; mi++) fa[s][mi] = read_a(smem, s, mi);
+#pragma unroll
+            for (int ni = 0; ni < NI; ni++) fb[s][ni] = read_b(smem, s, ni);
+        }
+        auto tiles = [&](int t0, int t1, auto checked) __attribute__((always_inline)) {
+            for (int t = t0; t < t1; t++) {
+                const unsigned char *cur = smem + stage(t), *next = cur;
+                uint32_t dma_st = 0;
+                int dma_kt = 0;
+#pragma unroll
+                for (int s = 0; s < 4; s++) {
+                    const int r = s + FD;
+                    if (r == 4) {
+                        // tile t+1 has landed and every wave is done with t-1
+                        if (t + 1 < nt) {
+                            wait_vmcnt<(AHEAD - 1) * ND>();
+                            __syncthreads();
+                        }
+                        next = smem + stage(t + 1);
+                        dma_kt = min(t + 1 + AHEAD, nt - 1);
+                        dma_st = stage(t + STAGES);
+                        if (t + 1 >= nt) dma_st = stage(t - 1 + STAGES);
+                    }
+                    const int part = r >= 4 && r < 6 ? r - 4 : -1;
+                    step(s, r < 4 ? cur : next, r & 3, dma_st, dma_kt, part < 0 ? 0 : part * ND / 2,
+                         part < 0 ? 0 : (part + 1) * ND / 2, checked);
+                }
+            }
+        };
+        const int t_chk = chk >= nt ? nt : max(0, chk - 1 - AHEAD);
+        tiles(0, t_chk, std::false_type{});
+        tiles(t_chk, nt, std::true_type{});
+        // No copy may land in LDS after the workgroup's end (or in what the
+        // caller does next with it).
+        wait_vmcnt<0>();
+    }
+};
+
+template <int MI, int NI>
+__device__ static __forceinline__ void clear_acc(f32x16 (&acc)[MI][NI]) {
+#pragma unroll
+    for (int mi = 0; mi < MI; mi++)
+#pragma unroll
+        for (int ni = 0; ni < NI; ni++) acc[mi][ni] = f32x16{};
+}
+
+// The race screen of TDG_DEBUG_POISON_LDS: LDS full of NaN before the first
+// tile is asked for.
+template <int BYTES, int NT>
+__device__ static __forceinline__ void poison_lds(int flags, unsigned char *smem) {
+    if (flags & TDG_DEBUG_POISON_LDS) {
+        for (int o = threadIdx.x * 16; o < BYTES; o += NT * 16) lds_write16(smem + o, u32x4{~0u, ~0u, ~0u, ~0u});
+        __syncthreads();
+    }
+}
+
+// One tile of a grouped product per workgroup; E is GroupedAny or GroupedRing.
+template <class E, int LAY, int BM, int BN, int WM, int WN>
+__device__ static __forceinline__ void grouped_tile(const GroupedArgs &a, unsigned char *smem) {
+    constexpr bool TN = LAY == LAY_TN;
+    const GroupedTile t = find_tile<LAY, BM>(a);
+    if (!t.ok) return;
+    poison_lds<E::SMEM, E::NT>(a.flags, smem);
+    const int x0 = TN ? t.tm * BM : t.lo + t.tm * BM, x_end = TN ? a.M : t.hi, y0 = t.tn * BN;
+    f32x16 acc[E::MI][E::NI];
+    clear_acc(acc);
+    E::run(a.A, a.lda, a.B + (TN ? 0 : (int64_t)t.g * a.stride_b), a.ldb, x0, x_end, y0, a.N, TN ? t.lo : 0,
+           TN ? t.hi : a.K, smem, acc);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    store_tile<E::MI, E::NI>(a.C + (TN ? (int64_t)t.g * a.stride_c : 0), a.ldc, x0 + (wave % WM) * E::WTM, x_end,
+                             y0 + (wave / WM) * E::WTN, a.N, acc);
+}
+
+template <int LAY, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a) {
+    typedef GroupedAny<LAY, BM, BN, WM, WN> E;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
+    grouped_tile<E, LAY, BM, BN, WM, WN>(a, smem);
+}
+
+template <int LAY, int BM, int BN, int WM, int WN, int STAGES>
+__global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_ring(GroupedArgs a) {
+    typedef GroupedRing<LAY, BM, BN, WM, WN, STAGES> E;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
+    grouped_tile<E, LAY, BM, BN, WM, WN>(a, smem);
 }
 
 }  // namespace tdg

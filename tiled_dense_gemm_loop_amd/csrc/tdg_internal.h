@@ -29,6 +29,9 @@ const KernelEntry *kernel_table(int *count);
 // TDG_OK when the current device is gfx950, else TDG_ERR_NO_DEVICE.
 int device_check();
 
+// The TDG_DEBUG_* bits that launches take at this moment.
+int debug_flags_now();
+
 // Split-K second pass: C (M x N, ldc) = sum over `parts` dense M x N partial
 // products at ws, in part order.  FP32 for the FP16 / FP32 dtypes, INT32 for
 // INT8.  Enqueued on `stream`.
