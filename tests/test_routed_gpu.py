@@ -47,6 +47,17 @@ def wider(t, pad, skip=0):
     return v
 
 
+def at_page_end(t):
+    """t (a matrix, or a stack) on the device, its last byte the last of a
+    4 KiB page; NaN behind it."""
+    bytes_ = t.numel() * t.element_size()
+    buf = torch.full(((bytes_ + 8192) // t.element_size(),), float("nan"), dtype=t.dtype, device="cuda")
+    skip = (-(buf.data_ptr() + bytes_)) % 4096 // t.element_size()
+    v = buf[skip:skip + t.numel()].view(t.shape)
+    assert (v.data_ptr() + bytes_) % 4096 == 0
+    return v.copy_(t)
+
+
 def near(got, want, tol):
     got = got.cpu().double()
     bad = ~((got - want).abs() <= tol)
@@ -338,6 +349,33 @@ def test_grouped_tn(lib, rows, M, N, pad, skip, gap, kind):
     near(got, want, tol)
 
 
+@pytest.mark.parametrize("rows,K,N", [([40, 0, 70], 65, 67), ([1], 1, 1), ([300, 20], 96, 129), ([5], 129, 96),
+                                      ([2, 260], 1001, 7)])
+def test_grouped_operands_at_a_page_end(lib, rows, K, N):
+    """Operands with nothing mapped to count on behind them."""
+    r = rng(20, K, N)
+    off, R = groups_of(rows, 0, 0)
+    a, b, dy = whole(r, R, K), whole(r, len(rows), K, N), whole(r, R, N)
+    o, zero = off.cuda(), lambda t: torch.zeros_like(t)
+    want, _ = grouped64(a, b, off)
+    near(lib.gemm_f16f32_grouped(at_page_end(a), at_page_end(b), o), want, zero(want))
+    bt = b.transpose(1, 2).contiguous()
+    near(lib.gemm_f16f32_grouped_nt(at_page_end(a), at_page_end(bt), o), want, zero(want))
+    want = torch.stack([a[int(off[g]):int(off[g + 1])].double().t() @ dy[int(off[g]):int(off[g + 1])].double()
+                        for g in range(len(rows))])
+    near(lib.gemm_f16f32_grouped_tn(at_page_end(a), at_page_end(dy), o), want, zero(want))
+
+
+@pytest.mark.parametrize("M,K,N,rank", [(3, 65, 67, 9), (70, 129, 130, 33), (300, 97, 255, 5)])
+def test_lora_operands_at_a_page_end(lib, M, K, N, rank):
+    r = rng(21, M)
+    a, b, down, up = whole(r, M, K, most=2), whole(r, K, N), whole(r, 3, K, rank, most=1), whole(r, 3, rank, N, most=2)
+    pick = torch.from_numpy(r.integers(-1, 3, M)).to(torch.int32)
+    want, _, _ = lora64(a, b, down, up, pick, None)
+    got = lib.gemm_f16f32_lora(at_page_end(a), at_page_end(b), at_page_end(down), at_page_end(up), pick.cuda())
+    near(got, want, torch.zeros_like(want))
+
+
 @pytest.mark.parametrize("K,N", [(128, 128), (72, 100), (65, 67)])
 def test_groups_do_not_touch_each_other(lib, K, N):
     """Infinities and NaN in one group's rows and weights stay in that group."""
@@ -570,6 +608,30 @@ def test_expert_layer_in_a_graph_on_its_own_stream(lib):
         for g, t in zip(got, w):
             assert torch.equal(g, t)
         layer_on(lib, *s)  # eager work between the replays
+
+
+def test_no_tile_is_read_before_it_lands(lib):
+    """With LDS full of NaN at the start (the library's race screen), every
+    product is what it is without."""
+    r = rng(22)
+    off, R = groups_of([300, 40, 0, 513], 0, 0)
+    o = off.cuda()
+    calls = []
+    for K, N in ((256, 264), (200, 65), (40, 40)):
+        a, b, dy = normal(r, R, K).cuda(), normal(r, 4, K, N).cuda(), normal(r, R, N).cuda()
+        down, up = normal(r, 4, K, 16).cuda(), normal(r, 4, 16, N).cuda()
+        pick = torch.from_numpy(r.integers(-1, 4, R)).to(torch.int32).cuda()
+        calls += [lambda a=a, b=b: lib.gemm_f16f32_grouped(a, b, o), lambda dy=dy, b=b: lib.gemm_f16f32_grouped_nt(dy, b, o),
+                  lambda a=a, dy=dy: lib.gemm_f16f32_grouped_tn(a, dy, o)]
+        calls += [lambda m=m, a=a, b=b, d=down, u=up, p=pick: lib.gemm_f16f32_lora(a[:m], b[0], d, u, p[:m])
+                  for m in (5, 60, 200, R)]
+    plain = [f().clone() for f in calls]
+    before = lib.tdg_set_debug_flags(lib.TDG_DEBUG_POISON_LDS)
+    try:
+        for f, p in zip(calls, plain):
+            assert torch.equal(f(), p)
+    finally:
+        lib.tdg_set_debug_flags(before)
 
 
 def test_lora_in_a_graph(lib):

@@ -1,7 +1,6 @@
 // tdg_grouped.hip -- host side of the products whose rows pick their weights:
 // gemm_f16f32_grouped, _nt and _tn.
 #include "tdg_grouped.hpp"
-#include <stdlib.h>
 
 #include "tdg_check.h"
 #include "tdg_internal.h"
@@ -56,27 +55,39 @@ struct Variant {
      : lay == tdg::LAY_NT ? (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__> \
                           : (const void *)&tdg::KERNEL<tdg::LAY_TN, __VA_ARGS__>)
 
-Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+               const void *B, int64_t ldb, int64_t stride_b) {
     const bool tn = lay == tdg::LAY_TN;
-    // The DMA copies whole 16-byte chunks of a row: the row lengths that it
-    // cuts into chunks have to be multiples of 8.  Its lanes reach a tile's
-    // rows with 32-bit byte offsets.
-    const bool chunks = (tn ? M : K) % 8 == 0 && (lay == tdg::LAY_NT ? K : N) % 8 == 0;
+    // The DMA copies whole 16-byte chunks, and its lanes reach a tile's rows
+    // with 32-bit byte offsets.
+    const bool chunks = tdg::chunk_stays_in_page(A, rows, tn ? M : K, lda) &&
+                        (tn ? tdg::chunk_stays_in_page(B, rows, N, ldb)
+                            : tdg::chunk_stays_in_page(B, lay == tdg::LAY_NN ? K : N, lay == tdg::LAY_NN ? N : K, ldb,
+                                                       groups, stride_b));
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
     if (!chunks || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256};
-    const int64_t tall = tn ? M : rows / groups;  // rows of C in a group, on average
-    static const char *force = getenv("TDG_FORCE");
-    int f = force ? atoi(force) : 0;
-    if (!f) f = tn ? 1 : tall <= 48 ? 3 : tall < 192 ? 2 : 1;
-    if (f == 1) return {TDG_BY_LAYOUT(tdg_grouped_ring, 256, 256, 2, 4, 2), 256, 256, 512};
-    if (f == 2) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 3), 128, 128, 256};
-    if (f == 4) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256};
-    if (f == 5) return {TDG_BY_LAYOUT(tdg_grouped_ring, 256, 128, 2, 2, 2), 256, 128, 256};
-    if (f == 6 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 64, 1, 2, 6), 32, 64, 128};
-    if (f == 7 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 128, 2, 2, 4), 64, 128, 256};
-    if (f == 8 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 128, 1, 4, 3), 32, 128, 256};
-    if (f == 9 && !tn) return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 64, 1, 2, 4), 32, 64, 128};
-    return {TDG_BY_LAYOUT(tdg_grouped_ring, 32, 128, 1, 4, 6), 32, 128, 256};
+    // Tiles that the product is expected to have: half a row tile more per
+    // group that can have rows than the rows fill, one at the least.
+    const int64_t live = groups < rows ? groups : rows;
+    auto tiles = [&](int64_t b) {
+        int64_t high = rows / b + live / 2;
+        if (high < live) high = live;
+        return (tn ? groups * tdg::ceil_quot(M, b) : high) * tdg::ceil_quot(N, b);
+    };
+    // 256 x 256 needs the fewest bytes per operation, but a workgroup for
+    // every CU, and rows to fill it (us, 256 / 128 / 64 wide): 16384 rows, 16
+    // groups, K = N = 4096: 568 / 653 / 1061; 4096 rows, 32 groups, K = N =
+    // 2048: 111 / 84 / 92.  128 x 128 holds two workgroups per CU with two
+    // buffers, and where there is only one to hold it has four (TN of 16384
+    // rows, 4 groups, 1024 x 1024: 48 / 41).  64 x 64 is for products with few
+    // tiles, the ones of few rows that are bound by reading B among them (8
+    // rows, 64 groups, K = 2048, N = 1408: 24 / 13; 500 rows, 4 groups, K = N
+    // = 1000: 13 / 9).
+    if (tiles(256) >= 256 && (tn || rows >= 192 * live))
+        return {TDG_BY_LAYOUT(tdg_grouped_ring, 256, 256, 2, 4, 2), 256, 256, 512};
+    if (tiles(128) > 256) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256};
+    if (tiles(128) >= 192) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256};
+    return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 64, 2, 2, 4), 64, 64, 256};
 }
 
 int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, int64_t K,
@@ -86,7 +97,7 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     if (rc != TDG_OK) return rc;
     if (groups == 0 || N == 0 || (lay == tdg::LAY_TN ? M == 0 : rows == 0)) return TDG_OK;
 
-    const Variant v = choose(lay, groups, rows, M, N, K, lda, ldb);
+    const Variant v = choose(lay, groups, rows, M, N, K, A, lda, B, ldb, stride_b);
     GroupedArgs a;
     a.A = (const unsigned char *)A, a.B = (const unsigned char *)B, a.C = (unsigned char *)C;
     a.lda = lda * 2, a.ldb = ldb * 2, a.ldc = ldc * 4;
@@ -95,7 +106,8 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     a.groups = (int)groups, a.rows = (int)rows, a.M = (int)M, a.N = (int)N, a.K = (int)K;
     a.tiles_m = (int)tdg::ceil_quot(M, v.bm), a.tiles_n = (int)tdg::ceil_quot(N, v.bn);
     a.flags = tdg::debug_flags_now();
-    // Most tiles: every group can end inside a tile, and needs a row for it.
+    // Most row tiles: every group can end inside a tile, and needs a row for
+    // it.
     const int64_t row_tiles = lay == tdg::LAY_TN ? groups * a.tiles_m
                                                  : rows / v.bm + (groups < rows ? groups : rows);
     if (row_tiles > INT32_MAX / a.tiles_n) return TDG_ERR_UNSUPPORTED;

@@ -72,9 +72,10 @@ struct Image {
     }
 };
 
-// Where a workgroup works: its group, the group's rows [lo, hi) and its tile.
+// Where a workgroup works: its group, the group's rows [lo, hi), the tile's
+// first row (TN: column of A) and its column tile.
 struct GroupedTile {
-    int g, lo, hi, tm, tn;
+    int g, lo, hi, x0, tn;
     bool ok;
 };
 
@@ -93,25 +94,31 @@ __device__ static __forceinline__ void order_tile(int id, int tiles_m, int tiles
     tn = r / gm;
 }
 
-// Workgroup -> tile.  Tiles are numbered group by group; workgroups are dealt
-// round-robin to the 8 XCDs, so workgroup b takes tile (b % 8) * ceil(total / 8)
-// + b / 8: every XCD works on a run of tiles and reads each group's B into its
-// own L2 once.  For NN and NT the tile counts depend on the offsets: every
-// wave sums them itself (64 lanes, a run of groups each), which costs less
-// than a launch that would write them down.  The grid is sized for the most
-// tiles that the rows can make; workgroups past the total end at once.
+// Workgroup b of a run of `total` tiles -> tile: workgroups are dealt round-
+// robin to the 8 XCDs, so b takes tile (b % 8) * ceil(total / 8) + b / 8:
+// every XCD works on a run of tiles and reads a group's B into its own L2 once.
+// -1: none.
+__device__ static __forceinline__ int xcd_tile(int b, int total) {
+    const int per = (total + 7) >> 3, id = (b & 7) * per + (b >> 3);
+    return (b >> 3) < per && id < total ? id : -1;
+}
+
+// Workgroup -> tile.  Tiles are numbered group by group.  For NN and NT the tile counts depend on the offsets:
+// every wave sums them itself (64 lanes, a run of groups each), which costs
+// less than a launch that would write them down.  The grid is sized for the
+// most tiles that the rows can make; workgroups past the total end at once.
 template <int LAY, int BM>
 __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a) {
     GroupedTile t;
     t.ok = false;
-    const int b = blockIdx.x;
     if constexpr (LAY == LAY_TN) {
         const int per_g = a.tiles_m * a.tiles_n;
-        const int total = a.groups * per_g, per = (total + 7) >> 3;
-        const int id = (b & 7) * per + (b >> 3);
-        if ((b >> 3) >= per || id >= total) return t;
+        const int id = xcd_tile(blockIdx.x, a.groups * per_g);
+        if (id < 0) return t;
         t.g = id / per_g;
-        order_tile(id - t.g * per_g, a.tiles_m, a.tiles_n, t.tm, t.tn);
+        int tm;
+        order_tile(id - t.g * per_g, a.tiles_m, a.tiles_n, tm, t.tn);
+        t.x0 = tm * BM;
         t.lo = group_offset(a, t.g);
         t.hi = max(t.lo, group_offset(a, t.g + 1));
         t.ok = true;
@@ -120,42 +127,42 @@ __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a) {
     const int lane = threadIdx.x & 63;
     const int run = (a.groups + 63) >> 6;
     const int g0 = min(a.groups, lane * run), g1 = min(a.groups, g0 + run);
-    int mine = 0;
+    int mine = 0;  // row tiles of the lane's groups
     if (g0 < g1) {
         int lo = group_offset(a, g0);
         for (int g = g0; g < g1; g++) {
-            const int hi = group_offset(a, g + 1);
-            mine += (max(hi - lo, 0) + BM - 1) / BM;
+            const int hi = group_offset(a, g + 1), len = max(hi - lo, 0);
+            mine += (len + BM - 1) / BM;
             lo = hi;
         }
     }
-    int incl = mine;
+    int upto = mine;
     for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(incl, d);
-        if (lane >= d) incl += up;
+        const int up = __shfl_up(upto, d);
+        if (lane >= d) upto += up;
     }
-    const int total = __builtin_amdgcn_readlane(incl, 63) * a.tiles_n, per = (total + 7) >> 3;
-    const int id = (b & 7) * per + (b >> 3);
-    if ((b >> 3) >= per || id >= total) return t;
-    const int row_tile = id / a.tiles_n;  // only to find the group: every group has whole runs of tiles_n
-    const unsigned long long at = __ballot(incl > row_tile);
-    const int owner = __builtin_amdgcn_readfirstlane(__ffsll(at) - 1);
-    int first = __builtin_amdgcn_readlane(incl - mine, owner);  // row tiles before group g
-    int g = min(a.groups, owner * run);
+    const int id = xcd_tile(blockIdx.x, __builtin_amdgcn_readlane(upto, 63) * a.tiles_n);
+    if (id < 0) return t;
+    const int at = id / a.tiles_n;  // the how manieth row tile: finds the group
+    const int owner = __builtin_amdgcn_readfirstlane(__ffsll(__ballot(upto > at)) - 1);
+    int first = __builtin_amdgcn_readlane(upto - mine, owner);  // row tiles before group g
+    int g = min(a.groups - 1, owner * run);
     int lo = group_offset(a, g), hi, tiles;
     for (;; g++) {
         hi = group_offset(a, g + 1);
         tiles = (max(hi - lo, 0) + BM - 1) / BM;
-        if (row_tile < first + tiles || g + 1 >= a.groups) break;
+        if (at < first + tiles || g + 1 >= a.groups) break;
         first += tiles;
         lo = hi;
     }
-    t.g = g, t.lo = lo, t.hi = hi;
     // Offsets that do not ascend break the numbering; such a workgroup ends
     // here rather than work outside [lo, hi).
     const int local = id - first * a.tiles_n;
     if (local < 0 || local >= tiles * a.tiles_n) return t;
-    order_tile(local, tiles, a.tiles_n, t.tm, t.tn);
+    t.g = g, t.lo = lo, t.hi = hi;
+    int tm;
+    order_tile(local, tiles, a.tiles_n, tm, t.tn);
+    t.x0 = lo + tm * BM;
     t.ok = true;
     return t;
 }
@@ -167,30 +174,50 @@ __device__ static __forceinline__ void store_tile(unsigned char *C, int64_t ldc,
                                                   int col_end, const f32x16 (&acc)[MI][NI]) {
     const int lane = threadIdx.x & 63;
     const int rq = (lane >> 5) * 4;
-    const bool inside = row0 + MI * 32 <= row_end && col0 + NI * 32 <= col_end;
+    auto store = [&](auto masked, auto streaming) __attribute__((always_inline)) {
 #pragma unroll
-    for (int mi = 0; mi < MI; mi++)
+        for (int mi = 0; mi < MI; mi++)
 #pragma unroll
-        for (int ni = 0; ni < NI; ni++) {
-            const int col = col0 + ni * 32 + (lane & 31);
+            for (int ni = 0; ni < NI; ni++) {
+                const int col = col0 + ni * 32 + (lane & 31);
 #pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int row = row0 + mi * 32 + (v >> 2) * 8 + rq + (v & 3);
-                if (inside || (row < row_end && col < col_end))
-                    *(float *)(C + (int64_t)row * ldc + (int64_t)col * 4) = acc[mi][ni][v];
+                for (int v = 0; v < 16; v++) {
+                    const int row = row0 + mi * 32 + (v >> 2) * 8 + rq + (v & 3);
+                    if (decltype(masked)::value && (row >= row_end || col >= col_end)) continue;
+                    float *p = (float *)(C + (int64_t)row * ldc + (int64_t)col * 4);
+                    if constexpr (decltype(streaming)::value) __builtin_nontemporal_store(acc[mi][ni][v], p);
+                    else *p = acc[mi][ni][v];
+                }
             }
-        }
+    };
+    const bool inside = row0 + MI * 32 <= row_end && col0 + NI * 32 <= col_end;
+    const bool lines = (((uintptr_t)C | (uint64_t)ldc) & 127) == 0;
+    if (inside && lines) store(std::false_type{}, std::true_type{});
+    else if (inside) store(std::false_type{}, std::false_type{});
+    else store(std::true_type{}, std::false_type{});
 }
 
-// One operand chunk of eight elements, any size, stride and alignment: whole
-// chunks are one 16-byte load, a chunk that a row's end cuts is read element
-// by element, so no byte outside an operand's rows is ever read; what lies
-// outside [.., row_end) x [.., col_end) is zero.
-__device__ static __forceinline__ u32x4 load_chunk(const unsigned char *P, int64_t ld, int row, int row_end, int col,
-                                                   int col_end) {
+// Where A's rows are: row x of the product at `off(x)` bytes from A.  RowsFrom:
+// one after the other, row x0 at A itself; RowsBy: row x is A's row list[x].
+struct RowsFrom {
+    int x0;
+    int64_t ld;
+    __device__ __forceinline__ int64_t off(int x) const { return (int64_t)(x - x0) * ld; }
+};
+struct RowsBy {
+    const int32_t *list;
+    int64_t ld;
+    __device__ __forceinline__ int64_t off(int x) const { return (int64_t)list[x] * ld; }
+};
+
+// One operand chunk of eight elements of the row at `row`, any size, stride
+// and alignment: a whole chunk is one 16-byte load, one that the row's end
+// cuts is read element by element, so no byte outside the rows is ever read;
+// what lies outside is zero.
+__device__ static __forceinline__ u32x4 load_chunk(const unsigned char *row, bool row_ok, int col, int col_end) {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (row < row_end && col < col_end) {
-        const unsigned char *p = P + (int64_t)row * ld + (int64_t)col * 2;
+    if (row_ok && col < col_end) {
+        const unsigned char *p = row + (int64_t)col * 2;
         const int left = col_end - col;
         if (left >= 8) {
             v = load16_global(p);
@@ -219,10 +246,13 @@ struct GroupedAny {
     static_assert(IA::CHUNKS % NT == 0 && IB::CHUNKS % NT == 0, "tile must split evenly over threads");
 
     // acc += the tile's product over k in [k_lo, k_hi).  Rows (TN: columns) of
-    // A from x0 to x_end, columns (NT: rows) of B from y0 to y_end.
-    __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, const unsigned char *B,
-                                               int64_t ldb, int x0, int x_end, int y0, int y_end, int k_lo,
-                                               int k_hi, unsigned char *smem, f32x16 (&acc)[MI][NI]) {
+    // A from x0 to x_end, found by `rows` (TN: not used); columns (NT: rows)
+    // of B from y0 to y_end.
+    template <class Rows>
+    __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, Rows rows,
+                                               const unsigned char *B, int64_t ldb, int x0, int x_end, int y0,
+                                               int y_end, int k_lo, int k_hi, unsigned char *smem,
+                                               f32x16 (&acc)[MI][NI]) {
         const int nt = (k_hi - k_lo + 63) >> 6;
         if (nt <= 0) return;
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -233,14 +263,16 @@ struct GroupedAny {
 #pragma unroll
             for (int i = 0; i < CA; i++) {
                 const int q = i * NT + tid, r = q / IA::CPR, c = ((q % IA::CPR) ^ IA::swz(r)) * 8;
-                ra[i] = LAY != LAY_TN ? load_chunk(A, lda, x0 + r, x_end, k0 + c, k_hi)
-                                      : load_chunk(A, lda, k0 + r, k_hi, x0 + c, x_end);
+                if (LAY == LAY_TN)
+                    ra[i] = load_chunk(A + (int64_t)(k0 + r) * lda, k0 + r < k_hi, x0 + c, x_end);
+                else
+                    ra[i] = load_chunk(A + rows.off(min(x0 + r, x_end - 1)), x0 + r < x_end, k0 + c, k_hi);
             }
 #pragma unroll
             for (int i = 0; i < CB; i++) {
                 const int q = i * NT + tid, r = q / IB::CPR, c = ((q % IB::CPR) ^ IB::swz(r)) * 8;
-                rb[i] = LAY == LAY_NT ? load_chunk(B, ldb, y0 + r, y_end, k0 + c, k_hi)
-                                      : load_chunk(B, ldb, k0 + r, k_hi, y0 + c, y_end);
+                rb[i] = LAY == LAY_NT ? load_chunk(B + (int64_t)(y0 + r) * ldb, y0 + r < y_end, k0 + c, k_hi)
+                                      : load_chunk(B + (int64_t)(k0 + r) * ldb, k0 + r < k_hi, y0 + c, y_end);
             }
         };
         auto store_lds = [&](unsigned char *st) {
@@ -276,14 +308,17 @@ struct GroupedAny {
     }
 };
 
-// Rows whose length is a whole number of 16-byte chunks: global-to-LDS DMA
-// (global_load_lds_dwordx4, from any byte address), a ring of STAGES buffers
-// with STAGES - 1 tiles in flight, fragments read three k steps ahead and the
-// copies of a later tile spread over the MFMAs of two steps: the schedule of
-// the plain product's direct loop.  Edges cost no test in the loop: a lane
-// whose row or column lies past the tile's end copies the last one instead
-// (it only feeds C elements that are not stored), and only the tile that the
-// end of k cuts takes its chunks past that end from a block of zeros.
+// Global-to-LDS DMA (global_load_lds_dwordx4, from any byte address), a ring
+// of STAGES buffers with STAGES - 1 tiles in flight, fragments read three k
+// steps ahead and the copies of a later tile spread over the MFMAs of two
+// steps: the schedule of the plain product's direct loop.  Edges cost no test
+// in the loop: a lane whose row or column lies past the tile's end copies the
+// last one instead (it only feeds C elements that are not stored), and only
+// the tile that the end of k cuts takes its chunks past that end from a block
+// of zeros.  Chunks that start inside a row are copied whole: what they hold
+// past a row's end feeds C elements that are not stored, or, where the row
+// runs along k, is cleared in LDS.  Past an operand's last byte they read only
+// within its 4 KiB page: the host sees to that (chunk_stays_in_page).
 template <int LAY, int BM, int BN, int WM, int WN, int STAGES>
 struct GroupedRing {
     typedef Image<LAY != LAY_TN, BM> IA;
@@ -299,12 +334,12 @@ struct GroupedRing {
     static_assert(B_STEP % 16 == 0 || (LAY != LAY_NT && B_STEP % 4 == 0), "B swizzle must repeat");
     static_assert(STAGES >= 2 && AHEAD * ND <= 63 && SMEM <= 160 * 1024, "ring");
 
-    // acc += the tile's product over k in [k_lo, k_hi).  Rows of A from x0 to
-    // x_end, columns (NT: rows) of B from y0 to y_end; P, ld as they sit in
-    // memory.
-    __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, const unsigned char *B,
-                                               int64_t ldb, int x0, int x_end, int y0, int y_end, int k_lo,
-                                               int k_hi, unsigned char *smem, f32x16 (&acc)[MI][NI]) {
+    // As GroupedAny::run; here `rows` gives offsets below 2^32.
+    template <class Rows>
+    __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, Rows rows,
+                                               const unsigned char *B, int64_t ldb, int x0, int x_end, int y0,
+                                               int y_end, int k_lo, int k_hi, unsigned char *smem,
+                                               f32x16 (&acc)[MI][NI]) {
         const int nt = (k_hi - k_lo + 63) >> 6;
         if (nt <= 0) return;
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -320,14 +355,14 @@ struct GroupedRing {
         uint32_t a_off[AKC ? CA : 1], b_off[BKC ? CB : 1];
 #pragma unroll
         for (int i = 0; i < (AKC ? CA : 1); i++)
-            a_off[i] = AKC ? (uint32_t)(min(i * A_STEP + a_r, x_end - 1 - x0) * lda + a_c * 16)
-                           : (uint32_t)(a_r * lda + min(a_c * 8, x_end - 8 - x0) * 2);
+            a_off[i] = AKC ? (uint32_t)(rows.off(min(x0 + i * A_STEP + a_r, x_end - 1)) + a_c * 16)
+                           : (uint32_t)(a_r * lda + min(a_c * 8, (x_end - 1 - x0) & ~7) * 2);
 #pragma unroll
         for (int i = 0; i < (BKC ? CB : 1); i++)
             b_off[i] = BKC ? (uint32_t)(min(i * B_STEP + b_r, y_end - 1 - y0) * ldb + b_c * 16)
-                           : (uint32_t)(b_r * ldb + min(b_c * 8, y_end - 8 - y0) * 2);
+                           : (uint32_t)(b_r * ldb + min(b_c * 8, (y_end - 1 - y0) & ~7) * 2);
         const unsigned char *a_base =
-            A + (AKC ? (int64_t)x0 * lda + (int64_t)k_lo * 2 : (int64_t)k_lo * lda + (int64_t)x0 * 2);
+            A + (AKC ? (int64_t)k_lo * 2 : (int64_t)k_lo * lda + (int64_t)x0 * 2);
         const unsigned char *b_base =
             B + (BKC ? (int64_t)y0 * ldb + (int64_t)k_lo * 2 : (int64_t)k_lo * ldb + (int64_t)y0 * 2);
         const uint64_t zero_addr = (uint64_t)(uintptr_t)tdg_zero16;
@@ -346,9 +381,19 @@ struct GroupedRing {
                 const int k = is_a ? (AKC ? a_c * 8 : i * A_STEP + a_r) : (BKC ? b_c * 8 : i * B_STEP + b_r);
                 const uint64_t p = (uint64_t)(uintptr_t)(base + off);
                 const uint64_t src = k < k_hi - k_lo - kt * 64 ? p : zero_addr;
-                asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+                asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
             } else {
-                asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(m0) : "memory");
+                // The base may have been written to its scalar registers by a
+                // vector instruction just before (v_readlane, where the
+                // compiler reloads spilled ones).  A vector-memory instruction
+                // may read them five wait states later at the earliest, which
+                // the compiler does not count for inline assembly; a scalar
+                // one may read them at once, and what it writes is safe.
+                uint64_t safe;
+                asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+                             : "=&s"(safe)
+                             : "v"(off), "s"(base), "{m0}"(m0)
+                             : "memory");
             }
         };
 
@@ -397,25 +442,55 @@ struct GroupedRing {
         };
         auto stage = [&](int t) { return (uint32_t)((t % STAGES) * STAGE); };
 
-        // Tiles from t_chk on may copy the tile that the end of k cuts.
+        // The tile that the end of k cuts is copied with the checked form.
         const bool cut = ((k_hi - k_lo) & 63) != 0;
-        const int chk = cut ? nt - 1 : nt;
-        // Prologue: every buffer is free.  Past the last tile, the last one
-        // is copied again (into a buffer that is not read any more), so the
-        // copies in flight at each wait are a constant.
+        // Prologue: every buffer is free.
 #pragma unroll
         for (int p = 0; p <= AHEAD; p++) {
-            const int kt = min(p, nt - 1);
-            if (kt >= chk) {
+            if (p >= nt) break;
+            if (cut && p == nt - 1) {
 #pragma unroll
-                for (int d = 0; d < ND; d++) issue(stage(p), kt, d, std::true_type{});
+                for (int d = 0; d < ND; d++) issue(stage(p), p, d, std::true_type{});
             } else {
 #pragma unroll
-                for (int d = 0; d < ND; d++) issue(stage(p), kt, d, std::false_type{});
+                for (int d = 0; d < ND; d++) issue(stage(p), p, d, std::false_type{});
             }
         }
-        wait_vmcnt<AHEAD * ND>();
+        // Waits until at most the n youngest tiles are still in flight.
+        auto wait_tiles = [&](int n) __attribute__((always_inline)) {
+            if (n >= AHEAD) wait_vmcnt<AHEAD * ND>();
+            else if (AHEAD > 4 && n == 4) wait_vmcnt<4 * ND <= 63 ? 4 * ND : 0>();
+            else if (AHEAD > 3 && n == 3) wait_vmcnt<3 * ND <= 63 ? 3 * ND : 0>();
+            else if (AHEAD > 2 && n == 2) wait_vmcnt<2 * ND <= 63 ? 2 * ND : 0>();
+            else if (AHEAD > 1 && n == 1) wait_vmcnt<ND <= 63 ? ND : 0>();
+            else wait_vmcnt<0>();
+        };
+        // Rows along k whose end splits a chunk: its elements from that end on
+        // are cleared once the last tile has landed, one thread per row.
+        const int split = AKC || BKC ? (k_hi - k_lo) & 7 : 0;
+        auto clear_split = [&](int t) __attribute__((always_inline)) {
+            if (split == 0 || t != nt - 1) return;
+            const int c = ((k_hi - k_lo) & 63) >> 3;
+            auto clear = [&](unsigned char *p) __attribute__((always_inline)) {
+                const u32x4 v = lds_read16(p);
+                u32x4 w;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int left = split - 2 * j;  // elements of word j that stay
+                    w[j] = v[j] & (left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u);
+                }
+                lds_write16(p, w);
+            };
+            unsigned char *st = smem + stage(t);
+            if (AKC)
+                for (int r = tid; r < BM; r += NT) clear(st + r * 128 + ((c ^ IA::swz(r)) << 4));
+            if (BKC)
+                for (int r = tid; r < BN; r += NT) clear(st + IA::BYTES + r * 128 + ((c ^ IB::swz(r)) << 4));
+            __syncthreads();
+        };
+        wait_tiles(min(AHEAD, nt - 1));
         __syncthreads();
+        clear_split(0);
 #pragma unroll
         for (int s = 0; s < FD; s++) {
 #pragma unroll
@@ -423,37 +498,36 @@ struct GroupedRing {
 #pragma unroll
             for (int ni = 0; ni < NI; ni++) fb[s][ni] = read_b(smem, s, ni);
         }
-        auto tiles = [&](int t0, int t1, auto checked) __attribute__((always_inline)) {
+        // Tiles t0 .. t1 - 1.  `copies`: tile t + STAGES is copied meanwhile,
+        // into tile t's buffer; it exists (and only it can be the cut one).
+        auto tiles = [&](int t0, int t1, auto copies, auto checked) __attribute__((always_inline)) {
             for (int t = t0; t < t1; t++) {
                 const unsigned char *cur = smem + stage(t), *next = cur;
-                uint32_t dma_st = 0;
-                int dma_kt = 0;
 #pragma unroll
                 for (int s = 0; s < 4; s++) {
                     const int r = s + FD;
                     if (r == 4) {
-                        // tile t+1 has landed and every wave is done with t-1
-                        if (t + 1 < nt) {
+                        // tile t+1 has landed, and every wave has read tile t
+                        if constexpr (decltype(copies)::value) {
                             wait_vmcnt<(AHEAD - 1) * ND>();
                             __syncthreads();
+                        } else if (t + 1 < nt) {
+                            wait_tiles(nt - 2 - t);
+                            __syncthreads();
+                            clear_split(t + 1);
                         }
                         next = smem + stage(t + 1);
-                        dma_kt = min(t + 1 + AHEAD, nt - 1);
-                        dma_st = stage(t + STAGES);
-                        if (t + 1 >= nt) dma_st = stage(t - 1 + STAGES);
                     }
-                    const int part = r >= 4 && r < 6 ? r - 4 : -1;
-                    step(s, r < 4 ? cur : next, r & 3, dma_st, dma_kt, part < 0 ? 0 : part * ND / 2,
+                    const int part = decltype(copies)::value && r >= 4 && r < 6 ? r - 4 : -1;
+                    step(s, r < 4 ? cur : next, r & 3, stage(t), t + STAGES, part < 0 ? 0 : part * ND / 2,
                          part < 0 ? 0 : (part + 1) * ND / 2, checked);
                 }
             }
         };
-        const int t_chk = chk >= nt ? nt : max(0, chk - 1 - AHEAD);
-        tiles(0, t_chk, std::false_type{});
-        tiles(t_chk, nt, std::true_type{});
-        // No copy may land in LDS after the workgroup's end (or in what the
-        // caller does next with it).
-        wait_vmcnt<0>();
+        const int full = max(0, nt - STAGES);  // tiles with a later one to copy
+        tiles(0, cut ? max(0, full - 1) : full, std::true_type{}, std::false_type{});
+        if (cut) tiles(max(0, full - 1), full, std::true_type{}, std::true_type{});
+        tiles(full, nt, std::false_type{}, std::false_type{});
     }
 };
 
@@ -477,18 +551,19 @@ __device__ static __forceinline__ void poison_lds(int flags, unsigned char *smem
 
 // One tile of a grouped product per workgroup; E is GroupedAny or GroupedRing.
 template <class E, int LAY, int BM, int BN, int WM, int WN>
-__device__ static __forceinline__ void grouped_tile(const GroupedArgs &a, unsigned char *smem) {
+__device__ static __forceinline__ void grouped_product(const GroupedArgs &a, unsigned char *smem) {
     constexpr bool TN = LAY == LAY_TN;
     const GroupedTile t = find_tile<LAY, BM>(a);
     if (!t.ok) return;
     poison_lds<E::SMEM, E::NT>(a.flags, smem);
-    const int x0 = TN ? t.tm * BM : t.lo + t.tm * BM, x_end = TN ? a.M : t.hi, y0 = t.tn * BN;
+    const int x_end = TN ? a.M : t.hi, y0 = t.tn * BN;
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
-    E::run(a.A, a.lda, a.B + (TN ? 0 : (int64_t)t.g * a.stride_b), a.ldb, x0, x_end, y0, a.N, TN ? t.lo : 0,
-           TN ? t.hi : a.K, smem, acc);
+    E::run(a.A + (TN ? 0 : (int64_t)t.x0 * a.lda), a.lda, RowsFrom{t.x0, a.lda},
+           a.B + (TN ? 0 : (int64_t)t.g * a.stride_b), a.ldb, t.x0, x_end, y0, a.N, TN ? t.lo : 0, TN ? t.hi : a.K,
+           smem, acc);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    store_tile<E::MI, E::NI>(a.C + (TN ? (int64_t)t.g * a.stride_c : 0), a.ldc, x0 + (wave % WM) * E::WTM, x_end,
+    store_tile<E::MI, E::NI>(a.C + (TN ? (int64_t)t.g * a.stride_c : 0), a.ldc, t.x0 + (wave % WM) * E::WTM, x_end,
                              y0 + (wave / WM) * E::WTN, a.N, acc);
 }
 
@@ -496,14 +571,14 @@ template <int LAY, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a) {
     typedef GroupedAny<LAY, BM, BN, WM, WN> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    grouped_tile<E, LAY, BM, BN, WM, WN>(a, smem);
+    grouped_product<E, LAY, BM, BN, WM, WN>(a, smem);
 }
 
 template <int LAY, int BM, int BN, int WM, int WN, int STAGES>
 __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_ring(GroupedArgs a) {
     typedef GroupedRing<LAY, BM, BN, WM, WN, STAGES> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    grouped_tile<E, LAY, BM, BN, WM, WN>(a, smem);
+    grouped_product<E, LAY, BM, BN, WM, WN>(a, smem);
 }
 
 }  // namespace tdg

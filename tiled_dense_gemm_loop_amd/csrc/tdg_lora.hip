@@ -3,19 +3,22 @@
 // a = adapter[t], and the second term is left out where a is not in
 // [0, adapters).
 //
-// Two launches.  The first makes low[t] = A[t] . down[a], a thin product that
-// K is cut for so that it fills the chip; its parts are summed where they are
-// read.  The second makes C:
-//   * many rows (k_lora_main): the shared product's tiles, and on each wave's
-//     32-row blocks low . up on the matrix cores, one pass per distinct
-//     adapter of the block, added to the accumulators of that adapter's rows
-//     alone: C is written once, and no row sees another's adapter;
-//   * few rows: the shared product is bound by reading B, and has too few
-//     tiles to do it at full rate.  Its parts over K are made in the first
-//     launch beside low's, and the second (k_lora_join) sums them and adds
-//     low . up in FP32.
-// On the matrix cores low goes in as two FP16 parts, high and rest, of the row
-// scaled by a power of two to just under 2^14: 21 bits or more at any size.
+// low[t] = A[t] . down[a] is a thin product that K is cut for so that it fills
+// the chip (k_lora_parts_*): a workgroup takes a tile of rows and, one after
+// the other, the distinct adapters among them.  Rows are sorted by adapter
+// first, so that there are few.
+//   * Many rows: k_lora_sort sorts each 4096 rows; k_lora_parts_* makes low;
+//     k_lora_split sums its parts and cuts each row into two FP16 rows, high
+//     and rest, scaled by a power of two to just under 2^14: 21 bits or more
+//     at any size.  k_lora_main_* then makes the shared product's tiles over
+//     the sorted rows, and on each wave's 32-row blocks low . up on the matrix
+//     cores, one pass per distinct adapter of the block, added to the
+//     accumulators of that adapter's rows alone: C is written once, and no row
+//     sees another's adapter.
+//   * Few rows: the shared product is bound by reading B, and has too few
+//     tiles to do it at full rate.  Its parts over K are made in the same
+//     launch as low's, and a second (k_lora_join) sums them and adds low . up
+//     in FP32.  The rows are sorted in each workgroup.
 #include "tdg_grouped.hpp"
 
 #include "tdg_check.h"
@@ -32,15 +35,22 @@ struct LoraArgs {
     float *C;
     float *part;  // parts x M x N: the shared product over slices of K (few rows)
     float *low;   // low_parts x M x rank
+    _Float16 *cut;  // M rows of low's high part and rest, rank16 each (many rows)
+    int32_t *ex;    // M: their rows' power of two
+    int rank16;     // the rank, rounded up to 16
+    int32_t *order; // M: the rows, sorted by adapter (many rows)
     int64_t lda, ldb, ldc, ld_down, stride_down, ld_up, stride_up;  // bytes
     int M, N, K, adapters, rank;
     int row_tiles, col_tiles;           // of the shared product
     int parts, k_per_part;              // K tiles of each slice
     int low_parts, low_k_per_part;
     int low_cols, low_lanes;            // blocks of the rank; workgroups that share a row tile's adapters
-    int shared_wgs;                     // workgroups on the shared product
+    int low_wgs;                        // workgroups on low, the first ones
     int flags;
 };
+
+// At most this many rows are "few": the key of sort_few holds them in 8 bits.
+constexpr int kFewRows = 256;
 
 // Which adapter a row has, -1 for none.
 __device__ __forceinline__ int adapter_of(const LoraArgs &p, int row) {
@@ -48,140 +58,251 @@ __device__ __forceinline__ int adapter_of(const LoraArgs &p, int row) {
     return (unsigned)a < (unsigned)p.adapters ? a : -1;
 }
 
-// The first launch: tiles of the shared product over a slice of K (few rows
-// only), and of low.  A tile of low belongs to BM <= 64 rows; its workgroups
-// take the distinct adapters among those rows in turn, each a whole product of
-// which the adapter's own rows are kept.
-template <class E, int BM, int BN, int WM, int WN>
+// Each SORT_ROWS rows sorted by adapter (by its remainder, where there are
+// more adapters than counters: rows that share a counter may mix), those with
+// none last.  Equal keys come out in any order: where a row is worked on does
+// not change its values.
+constexpr int SORT_ROWS = 4096, SORT_THREADS = 1024;
+
+// Adds 1 to count[key] for every active lane; returns what was there before.
+// One request's rows follow each other, so a wave's keys are often all the
+// same, and one addition for all of them spares 64 in turn.
+__device__ __forceinline__ int take(int *count, int key, int lane) {
+    const unsigned long long on = __ballot(1);
+    const int first = __builtin_amdgcn_readfirstlane(key);
+    if (__ballot(key == first) == on) {
+        int at = 0;
+        const int leader = __ffsll(on) - 1;
+        if (lane == leader) at = atomicAdd(&count[first], __popcll(on));
+        return __builtin_amdgcn_readlane(at, leader) + __popcll(on & ((1ull << lane) - 1));
+    }
+    return atomicAdd(&count[key], 1);
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) k_lora_sort(LoraArgs p) {
+    __shared__ int count[SORT_THREADS], wave_sum[SORT_THREADS / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int base = blockIdx.x * SORT_ROWS;
+    count[tid] = 0;
+    __syncthreads();
+    int key[SORT_ROWS / SORT_THREADS];
+#pragma unroll
+    for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++) {
+        const int row = base + i * SORT_THREADS + tid;
+        const int a = adapter_of(p, row);
+        key[i] = row >= p.M ? -1 : a < 0 ? SORT_THREADS - 1 : a % (SORT_THREADS - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++)
+        if (key[i] >= 0) take(count, key[i], lane);
+    __syncthreads();
+    const int mine = count[tid];
+    int incl = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(incl, d);
+        if (lane >= d) incl += up;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    int start = incl - mine;
+    for (int w = 0; w < wave; w++) start += wave_sum[w];
+    count[tid] = start;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++)
+        if (key[i] >= 0) p.order[base + take(count, key[i], lane)] = base + i * SORT_THREADS + tid;
+}
+
+// Few rows, more than one tile of them: every workgroup sorts them all for
+// itself, by counting the smaller keys; list[i] is the i-th row.
+__device__ __forceinline__ void sort_few(const LoraArgs &p, int32_t *key, int32_t *list) {
+    for (int row = threadIdx.x; row < kFewRows; row += blockDim.x) {
+        const int a = adapter_of(p, row);
+        key[row] = row >= p.M ? INT32_MAX : (a < 0 ? 1 << 22 : a & ((1 << 22) - 1)) << 8 | row;
+    }
+    __syncthreads();
+    for (int row = threadIdx.x; row < p.M; row += blockDim.x) {
+        const int mine = key[row];
+        int before = 0;
+#pragma unroll 4
+        for (int i = 0; i < kFewRows; i += 4) {
+            const i32x4 k = *(const i32x4 *)(key + i);
+            before += (k[0] < mine) + (k[1] < mine) + (k[2] < mine) + (k[3] < mine);
+        }
+        list[before] = row;
+    }
+    __syncthreads();
+}
+
+// Tiles of the shared product over a slice of K (few rows only), and of low.
+// A tile of low belongs to 64 rows of the sorted order; its workgroups take
+// the distinct adapters among them in turn, each a whole product of which the
+// adapter's own rows are kept.
+constexpr int PART_TILE = 64;
+
+template <class E>
 __device__ __forceinline__ void lora_parts(const LoraArgs &p, unsigned char *smem) {
+    constexpr int BM = PART_TILE, BN = PART_TILE, WM = 2;
+    __shared__ __attribute__((aligned(16))) int32_t key[kFewRows], list[kFewRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
     poison_lds<E::SMEM, E::NT>(p.flags, smem);
     f32x16 acc[E::MI][E::NI];
-    int b = blockIdx.x;
-    if (b < p.shared_wgs) {
+    int b = (int)blockIdx.x - p.low_wgs;
+    if (b >= 0) {
         // XCD b % 8 takes a run of tiles, rows first: B's tile is read once
         // into its L2 for all row tiles.
-        const int per = (p.shared_wgs + 7) >> 3;
+        const int per = ((int)gridDim.x - p.low_wgs) >> 3;
         b = (b & 7) * per + (b >> 3);
         if (b >= p.row_tiles * p.col_tiles * p.parts) return;
         const int tm = b % p.row_tiles, rest = b / p.row_tiles;
         const int tn = rest % p.col_tiles, part = rest / p.col_tiles;
         const int k_lo = part * p.k_per_part * 64, k_hi = min(p.K, k_lo + p.k_per_part * 64);
         clear_acc(acc);
-        E::run(p.A, p.lda, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, k_lo, k_hi, smem, acc);
+        E::run(p.A + (int64_t)(tm * BM) * p.lda, p.lda, RowsFrom{tm * BM, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN,
+               p.N, k_lo, k_hi, smem, acc);
         store_tile<E::MI, E::NI>((unsigned char *)(p.part + (int64_t)part * p.M * p.N), (int64_t)p.N * 4,
                                  tm * BM + wm * E::WTM, p.M, tn * BN + wn * E::WTN, p.N, acc);
         return;
     }
-    b -= p.shared_wgs;
+    b = blockIdx.x;
     const int turn = b % p.low_lanes;
     b /= p.low_lanes;
     const int tc = b % p.low_cols;
     b /= p.low_cols;
     const int part = b % p.low_parts, row0 = b / p.low_parts * BM;
+    if (row0 >= p.M) return;
     const int k_lo = part * p.low_k_per_part * 64, k_hi = min(p.K, k_lo + p.low_k_per_part * 64);
     float *low = p.low + (int64_t)part * p.M * p.rank;
-    const int id = adapter_of(p, lane < BM ? row0 + lane : p.M);
+    if (!p.order && p.M > BM) sort_few(p, key, list);
+    const int rows = min(BM, p.M - row0);
+    int row = -1;
+    if (lane < rows) row = p.order ? p.order[row0 + lane] : p.M > BM ? list[row0 + lane] : lane;
+    const int id = row >= 0 ? adapter_of(p, row) : -1;
     unsigned long long left = __ballot(id >= 0);
-    bool first = true;
     for (int n = 0; left; n++) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffsll(left) - 1));
         const unsigned long long mine = __ballot(id == a);
         left &= ~mine;
         if (n % p.low_lanes != turn) continue;
-        if (!first) __syncthreads();  // every wave is done with the LDS of the product before
-        first = false;
+        // every wave is done with the LDS of the product before; the rows of
+        // this tile are in its first words
+        if (threadIdx.x < BM) key[threadIdx.x] = max(row, 0);
+        __syncthreads();
         clear_acc(acc);
-        E::run(p.A, p.lda, p.down + (int64_t)a * p.stride_down, p.ld_down, row0, p.M, tc * BN, p.rank, k_lo, k_hi,
-               smem, acc);
+        E::run(p.A, p.lda, RowsBy{key, p.lda}, p.down + (int64_t)a * p.stride_down, p.ld_down, 0, rows, tc * BN,
+               p.rank, k_lo, k_hi, smem, acc);
 #pragma unroll
         for (int mi = 0; mi < E::MI; mi++)
 #pragma unroll
-            for (int ni = 0; ni < E::NI; ni++) {
-                const int c = tc * BN + wn * E::WTN + ni * 32 + (lane & 31);
+            for (int v = 0; v < 16; v++) {
+                const int r = wm * E::WTM + mi * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+                const int at = __shfl(row, r);
+                if (!((mine >> r) & 1)) continue;
 #pragma unroll
-                for (int v = 0; v < 16; v++) {
-                    const int r = wm * E::WTM + mi * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-                    if ((mine >> r) & 1 && c < p.rank) low[(int64_t)(row0 + r) * p.rank + c] = acc[mi][ni][v];
+                for (int ni = 0; ni < E::NI; ni++) {
+                    const int c = tc * BN + wn * E::WTN + ni * 32 + (lane & 31);
+                    if (c < p.rank) low[(int64_t)at * p.rank + c] = acc[mi][ni][v];
                 }
             }
     }
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
-__global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_parts_ring(LoraArgs p) {
-    typedef GroupedRing<LAY_NN, BM, BN, WM, WN, STAGES> E;
+__global__ void __launch_bounds__(256, 1) k_lora_parts_ring(LoraArgs p) {
+    typedef GroupedRing<LAY_NN, PART_TILE, PART_TILE, 2, 2, 4> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    lora_parts<E, BM, BN, WM, WN>(p, smem);
+    lora_parts<E>(p, smem);
 }
-template <int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_parts_any(LoraArgs p) {
-    typedef GroupedAny<LAY_NN, BM, BN, WM, WN> E;
+__global__ void __launch_bounds__(256, 1) k_lora_parts_any(LoraArgs p) {
+    typedef GroupedAny<LAY_NN, PART_TILE, PART_TILE, 2, 2> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    lora_parts<E, BM, BN, WM, WN>(p, smem);
+    lora_parts<E>(p, smem);
 }
 
-// low[row][c .. c + 7], summed over its parts; zero past the rank.
-__device__ __forceinline__ void load_low(const LoraArgs &p, int row, int c, float (&v)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[e] = 0.0f;
+// Between the launches for many rows: a wave per row sums low's parts, finds
+// the row's largest finite magnitude and writes the row as two FP16 rows,
+// x 2^-ex = high + rest, |x 2^-ex| < 2^14.  A value that is not finite goes
+// into the high part alone.
+constexpr int SPLIT_THREADS = 256;
+__global__ void __launch_bounds__(SPLIT_THREADS) k_lora_split(LoraArgs p) {
+    const int row = blockIdx.x * (SPLIT_THREADS / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (row >= p.M || adapter_of(p, row) < 0) return;
+    constexpr int PER = TDG_LORA_MAX_RANK / 64;
+    float x[PER] = {};
     for (int i = 0; i < p.low_parts; i++) {
-        const float *q = p.low + ((int64_t)i * p.M + row) * p.rank + c;
-        if (c + 8 <= p.rank) {
-            typedef float f32x4_ua __attribute__((ext_vector_type(4), aligned(4)));
-            const f32x4_ua x = *(const f32x4_ua *)q, y = *(const f32x4_ua *)(q + 4);
+        const float *low = p.low + ((int64_t)i * p.M + row) * p.rank;
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] += x[e], v[4 + e] += y[e];
-        } else {
+        for (int q = 0; q < PER; q++)
+            if (q * 64 + lane < p.rank) x[q] += low[q * 64 + lane];
+    }
+    float most = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                if (c + e < p.rank) v[e] += q[e];
-        }
+    for (int q = 0; q < PER; q++) {
+        const float m = fabsf(x[q]);
+        most = m <= 3.402823466e38f ? fmaxf(most, m) : most;
+    }
+    for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+    const int ex = most > 0.0f ? ilogbf(most) - 13 : 0;
+    if (lane == 0) p.ex[row] = ex;
+    _Float16 *hi = p.cut + (int64_t)row * 2 * p.rank16, *rest = hi + p.rank16;
+#pragma unroll
+    for (int q = 0; q < PER; q++) {
+        const int c = q * 64 + lane;
+        if (c >= p.rank16) break;
+        const float v = ldexpf(x[q], -ex);
+        const _Float16 h = (_Float16)v;
+        hi[c] = h;
+        rest[c] = fabsf(v) <= 65504.0f ? (_Float16)(v - (float)h) : (_Float16)0.0f;
     }
 }
 
-// acc += scale * low . up for the wave's rows from row0 and columns from col0.
-// The columns of up[a] that the wave needs are staged in its own part of LDS
-// (no barrier), 64 of the rank at a time.
-template <int MI, int NI>
-__device__ __forceinline__ void add_adapters(const LoraArgs &p, int row0, int col0, unsigned char *lds,
+// acc += scale * low . up for the wave's sorted rows from x0 and columns from
+// col0.  The columns of up[a] that the wave needs are staged in its own part
+// of LDS (no barrier), 64 of the rank at a time.  WHOLE: chunks of up
+// may be read whole (as the DMA reads those of B).
+template <int MI, int NI, bool WHOLE>
+__device__ __forceinline__ void add_adapters(const LoraArgs &p, int x0, int col0, unsigned char *lds,
                                              f32x16 (&acc)[MI][NI]) {
     typedef Image<false, NI * 32> IU;  // 64 of the rank by the wave's columns
     const int lane = threadIdx.x & 63;
     int staged = -1, staged_c = 0;
 #pragma unroll
     for (int mi = 0; mi < MI; mi++) {
-        const int row = row0 + mi * 32 + (lane & 31);
-        const int id = adapter_of(p, row);
+        const int x = x0 + mi * 32 + (lane & 31);
+        const int row = p.order[min(x, p.M - 1)];
+        const int id = x < p.M ? adapter_of(p, row) : -1;
+        const int ex = id >= 0 ? p.ex[row] : 0;
+        // rows without an adapter read what is there: their sums are not used
+        const _Float16 *cut = p.cut + (int64_t)row * 2 * p.rank16 + (lane >> 5) * 8;
         uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
         while (left) {
             const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
             const uint32_t mine = (uint32_t)__ballot(id == a);
             left &= ~mine;
-            // the row's power of two: its largest finite |low| below 2^14
-            float most = 0.0f;
-            for (int c = (lane >> 5) * 8; c < p.rank; c += 16) {
-                float v[8];
-                load_low(p, min(row, p.M - 1), c, v);
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const float m = fabsf(v[e]);
-                    most = m <= 3.402823466e38f ? fmaxf(most, m) : most;
-                }
-            }
-            most = fmaxf(most, __shfl_xor(most, 32));
-            const int ex = most > 0.0f ? ilogbf(most) - 13 : 0;
             f32x16 sum[NI];
 #pragma unroll
             for (int ni = 0; ni < NI; ni++) sum[ni] = f32x16{};
             for (int c0 = 0; c0 < p.rank; c0 += 64) {
                 if (staged != a || staged_c != c0) {
-                    const unsigned char *up = p.up + (int64_t)a * p.stride_up;
+                    const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col0 * 2;
+                    // rows of the rank that are there, in steps of the MFMA's 16
+                    const int need = min(64, p.rank16 - c0) * IU::CPR;
+                    for (int q0 = 0; q0 < need; q0 += 256) {
+                        u32x4 v[4];
 #pragma unroll
-                    for (int i = 0; i < IU::CHUNKS / 64; i++) {
-                        const int q = i * 64 + lane, r = q / IU::CPR, c = ((q % IU::CPR) ^ IU::swz(r)) * 8;
-                        lds_write16(lds + q * 16, load_chunk(up, p.ld_up, c0 + r, p.rank, col0 + c, p.N));
+                        for (int i = 0; i < 4; i++) {
+                            const int q = q0 + i * 64 + lane, r = q / IU::CPR;
+                            const int c = ((q % IU::CPR) ^ IU::swz(r)) * 8;
+                            const unsigned char *src = up + (int64_t)(c0 + r) * p.ld_up;
+                            if (WHOLE) {
+                                const bool ok = c0 + r < p.rank && col0 + c < p.N;
+                                v[i] = load16_global(ok ? src + c * 2 : (const unsigned char *)tdg_zero16);
+                            } else {
+                                v[i] = load_chunk(src, c0 + r < p.rank, c, p.N - col0);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; i++) lds_write16(lds + (q0 + i * 64 + lane) * 16, v[i]);
                     }
                     staged = a, staged_c = c0;
                     __builtin_amdgcn_wave_barrier();
@@ -189,21 +310,13 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, int row0, int co
 #pragma unroll
                 for (int s = 0; s < 4; s++) {
                     if (c0 + s * 16 >= p.rank) break;
-                    float v[8];
-                    load_low(p, min(row, p.M - 1), c0 + s * 16 + (lane >> 5) * 8, v);
-                    f16x8 hi, rest;
-#pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        const float x = ldexpf(v[e], -ex);
-                        hi[e] = (_Float16)x;
-                        const float d = x - (float)hi[e];
-                        rest[e] = fabsf(x) <= 65504.0f ? (_Float16)d : (_Float16)0.0f;  // not finite: all in hi
-                    }
+                    const u32x4 hi = *(const u32x4 *)(cut + c0 + s * 16);
+                    const u32x4 rest = *(const u32x4 *)(cut + p.rank16 + c0 + s * 16);
 #pragma unroll
                     for (int ni = 0; ni < NI; ni++) {
                         const u32x4 u = IU::read(lds, lane, ni * 32, s);
-                        sum[ni] = Mfma<DT_F16>::mac_sub(__builtin_bit_cast(u32x4, hi), u, sum[ni], 0);
-                        sum[ni] = Mfma<DT_F16>::mac_sub(__builtin_bit_cast(u32x4, rest), u, sum[ni], 0);
+                        sum[ni] = Mfma<DT_F16>::mac_sub(hi, u, sum[ni], 0);
+                        sum[ni] = Mfma<DT_F16>::mac_sub(rest, u, sum[ni], 0);
                     }
                 }
                 __builtin_amdgcn_wave_barrier();
@@ -222,9 +335,9 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, int row0, int co
     }
 }
 
-// The second launch for many rows: the shared product's tiles with the
-// adapters added to the accumulators.
-template <class E, int BM, int BN, int WM, int WN>
+// The shared product's tiles for many rows, with the adapters added to the
+// accumulators.  Tile row x is row order[x] of A and C.
+template <class E, int BM, int BN, int WM, int WN, bool WHOLE>
 __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem) {
     static_assert(E::SMEM >= WM * WN * Image<false, E::NI * 32>::BYTES, "LDS for up");
     const int total = p.row_tiles * p.col_tiles, per = (total + 7) >> 3;
@@ -235,84 +348,115 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     poison_lds<E::SMEM, E::NT>(p.flags, smem);
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
-    E::run(p.A, p.lda, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, 0, p.K, smem, acc);
+    E::run(p.A, p.lda, RowsBy{p.order, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, 0, p.K, smem, acc);
     __syncthreads();  // every wave is done with the tiles in LDS
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row0 = tm * BM + (wave % WM) * E::WTM, col0 = tn * BN + (wave / WM) * E::WTN;
-    add_adapters<E::MI, E::NI>(p, row0, col0, smem + wave * Image<false, E::NI * 32>::BYTES, acc);
-    store_tile<E::MI, E::NI>((unsigned char *)p.C, p.ldc, row0, p.M, col0, p.N, acc);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int x0 = tm * BM + (wave % WM) * E::WTM, col0 = tn * BN + (wave / WM) * E::WTN;
+    if (x0 >= p.M || col0 >= p.N) return;
+    add_adapters<E::MI, E::NI, WHOLE>(p, x0, col0, smem + wave * Image<false, E::NI * 32>::BYTES, acc);
+#pragma unroll
+    for (int mi = 0; mi < E::MI; mi++) {
+        const int at = p.order[min(x0 + mi * 32 + (lane & 31), p.M - 1)];
+#pragma unroll
+        for (int v = 0; v < 16; v++) {
+            const int r = (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+            float *dst = (float *)((unsigned char *)p.C + (int64_t)__shfl(at, r) * p.ldc) + col0 + (lane & 31);
+            if (x0 + mi * 32 + r >= p.M) continue;
+#pragma unroll
+            for (int ni = 0; ni < E::NI; ni++)
+                if (col0 + ni * 32 + (lane & 31) < p.N) dst[ni * 32] = acc[mi][ni][v];
+        }
+    }
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
 __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_ring(LoraArgs p) {
     typedef GroupedRing<LAY_NN, BM, BN, WM, WN, STAGES> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    lora_main<E, BM, BN, WM, WN>(p, smem);
+    lora_main<E, BM, BN, WM, WN, true>(p, smem);
 }
 template <int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_any(LoraArgs p) {
     typedef GroupedAny<LAY_NN, BM, BN, WM, WN> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    lora_main<E, BM, BN, WM, WN>(p, smem);
+    lora_main<E, BM, BN, WM, WN, false>(p, smem);
 }
 
 // The second launch for few rows: C[t][n] = the shared product's parts, in
-// order, and scale * sum_c low[t][c] * up[c][n].  A thread owns V columns of
-// JOIN_ROWS rows; neighbouring rows with the same adapter share up's loads.
-constexpr int JOIN_THREADS = 256, JOIN_ROWS = 4;
+// order, plus scale * sum_c low[t][c] * up[c][n].  A thread owns V columns of
+// ROWS rows; neighbouring rows with the same adapter share up's loads.  Bound
+// by latency: up's loads go out eight at a time, and the parts' before them.
+constexpr int JOIN_THREADS = 256, MAX_PARTS = 8;
 
-template <int V>
+template <int V, int ROWS>
 __global__ void __launch_bounds__(JOIN_THREADS) k_lora_join(LoraArgs p) {
-    __shared__ float low[JOIN_ROWS][TDG_LORA_MAX_RANK];
-    const int t0 = blockIdx.x * JOIN_ROWS, tid = threadIdx.x;
+    typedef float fv __attribute__((ext_vector_type(V)));
+    typedef _Float16 hv __attribute__((ext_vector_type(V)));
+    typedef fv fv_ua __attribute__((aligned(4)));
+    typedef hv hv_ua __attribute__((aligned(2)));
+    __shared__ float low[ROWS][TDG_LORA_MAX_RANK];
+    const int t0 = blockIdx.x * ROWS, tid = threadIdx.x;
     const int64_t n = ((int64_t)blockIdx.y * JOIN_THREADS + tid) * V;
-    int id[JOIN_ROWS];
+    const bool on = n < p.N;
+    fv sum[ROWS];
 #pragma unroll
-    for (int j = 0; j < JOIN_ROWS; j++) {
-        id[j] = __builtin_amdgcn_readfirstlane(adapter_of(p, t0 + j));
-        if (id[j] >= 0)
-            for (int c = tid; c < p.rank; c += JOIN_THREADS) {
-                float s = 0.0f;
-                for (int i = 0; i < p.low_parts; i++) s += p.low[((int64_t)i * p.M + t0 + j) * p.rank + c];
-                low[j][c] = s;
-            }
+    for (int j = 0; j < ROWS; j++) {
+        fv v[MAX_PARTS];
+#pragma unroll
+        for (int i = 0; i < MAX_PARTS; i++)
+            v[i] = on && i < p.parts && t0 + j < p.M ? *(const fv_ua *)(p.part + ((int64_t)i * p.M + t0 + j) * p.N + n)
+                                                     : fv{};
+        sum[j] = v[0];
+#pragma unroll
+        for (int i = 1; i < MAX_PARTS; i++) sum[j] += v[i];
+    }
+    int id[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; j++) id[j] = __builtin_amdgcn_readfirstlane(adapter_of(p, t0 + j));
+#pragma unroll
+    for (int j = 0; j < ROWS; j++) {
+        if (id[j] < 0 || tid >= p.rank) continue;
+        float v[MAX_PARTS];
+#pragma unroll
+        for (int i = 0; i < MAX_PARTS; i++)
+            v[i] = i < p.low_parts ? p.low[((int64_t)i * p.M + t0 + j) * p.rank + tid] : 0.0f;
+        float s = v[0];
+#pragma unroll
+        for (int i = 1; i < MAX_PARTS; i++) s += v[i];
+        low[j][tid] = s;
     }
     __syncthreads();
-    if (n >= p.N) return;
-    typedef float fv __attribute__((ext_vector_type(V), aligned(4)));
-    typedef _Float16 hv __attribute__((ext_vector_type(V), aligned(2)));
-    fv sum[JOIN_ROWS];
+    if (!on) return;
+    fv side[ROWS] = {};
+    for (int c0 = 0; c0 < p.rank; c0 += 8) {
+        hv u[8];
 #pragma unroll
-    for (int j = 0; j < JOIN_ROWS; j++) {
-        fv s = {};
-        if (t0 + j < p.M)
-            for (int i = 0; i < p.parts; i++) s += *(const fv *)(p.part + ((int64_t)i * p.M + t0 + j) * p.N + n);
-        sum[j] = s;
-    }
-    fv side[JOIN_ROWS] = {};
-    for (int c = 0; c < p.rank; c++) {
-        fv u = {};
-#pragma unroll
-        for (int j = 0; j < JOIN_ROWS; j++) {
+        for (int j = 0; j < ROWS; j++) {
             if (id[j] < 0) continue;
             if (j == 0 || id[j] != id[j - 1]) {
-                const hv h = *(const hv *)(p.up + (int64_t)id[j] * p.stride_up + (int64_t)c * p.ld_up + n * 2);
+                const unsigned char *up = p.up + (int64_t)id[j] * p.stride_up + n * 2;
 #pragma unroll
-                for (int q = 0; q < V; q++) u[q] = (float)h[q];
+                for (int e = 0; e < 8; e++)
+                    if (c0 + e < p.rank) u[e] = *(const hv_ua *)(up + (int64_t)(c0 + e) * p.ld_up);
             }
 #pragma unroll
-            for (int q = 0; q < V; q++) side[j][q] = fmaf(low[j][c], u[q], side[j][q]);
+            for (int e = 0; e < 8; e++)
+                if (c0 + e < p.rank) {
+                    const float l = low[j][c0 + e];
+#pragma unroll
+                    for (int q = 0; q < V; q++) side[j][q] = fmaf(l, (float)u[e][q], side[j][q]);
+                }
         }
     }
 #pragma unroll
-    for (int j = 0; j < JOIN_ROWS; j++) {
+    for (int j = 0; j < ROWS; j++) {
         if (t0 + j >= p.M) continue;
         if (id[j] >= 0) {
             const float scale = p.scale ? p.scale[id[j]] : 1.0f;
 #pragma unroll
             for (int q = 0; q < V; q++) sum[j][q] = fmaf(scale, side[j][q], sum[j][q]);
         }
-        *(fv *)((unsigned char *)p.C + (int64_t)(t0 + j) * p.ldc + n * 4) = sum[j];
+        *(fv_ua *)((unsigned char *)p.C + (int64_t)(t0 + j) * p.ldc + n * 4) = sum[j];
     }
 }
 
@@ -333,22 +477,18 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank) {
 // How the work is cut; a function of the sizes alone, as the workspace is.
 struct Plan {
     bool few;             // few rows: parts of the shared product and a join
-    int bm;               // row tile of the first launch
     int64_t parts, k_per_part, low_parts, low_k_per_part;
-    uint64_t low_at, bytes;  // workspace: parts, then low
+    uint64_t low_at, cut_at, ex_at, order_at, bytes;  // workspace: parts, low, its FP16 rows, their powers, the order
 };
-
-constexpr int64_t kFewRows = 256;
 
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t rank) {
     Plan p = {};
     const int64_t kt = ceil_quot(K, 64);
     p.few = M <= kFewRows;
-    p.bm = M <= 32 ? 32 : 64;
-    const int64_t row_tiles = ceil_quot(M, p.bm);
+    const int64_t row_tiles = ceil_quot(M, PART_TILE);
     auto cut = [&](int64_t tiles, int64_t want, int64_t *parts, int64_t *per) {
         int64_t n = ceil_quot(want, tiles > 0 ? tiles : 1);
-        n = n > 8 ? 8 : n;                       // the parts are read again
+        n = n > MAX_PARTS ? MAX_PARTS : n;       // the parts are read again
         n = n * 4 > kt ? (kt + 3) / 4 : n;       // a slice is four K tiles or more
         n = n < 1 ? 1 : n;
         *per = ceil_quot(kt, n);
@@ -356,9 +496,12 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t rank) {
     };
     if (p.few) cut(row_tiles * ceil_quot(N, 64), 512, &p.parts, &p.k_per_part);
     cut(row_tiles * ceil_quot(rank, 64), 256, &p.low_parts, &p.low_k_per_part);
-    p.low_at = p.few ? (uint64_t)p.parts * M * N * 4 : 0;
-    p.low_at = (p.low_at + 15) / 16 * 16;
-    p.bytes = p.low_at + (uint64_t)p.low_parts * M * rank * 4;
+    auto up16 = [](uint64_t n) { return (n + 15) / 16 * 16; };
+    p.low_at = p.few ? up16((uint64_t)p.parts * M * N * 4) : 0;
+    p.cut_at = p.low_at + up16((uint64_t)p.low_parts * M * rank * 4);
+    p.ex_at = p.cut_at + (p.few ? 0 : (uint64_t)M * 2 * up16(rank) * 2);
+    p.order_at = p.ex_at + (p.few ? 0 : up16((uint64_t)M * 4));
+    p.bytes = p.order_at + (p.few ? 0 : up16((uint64_t)M * 4));
     return p;
 }
 
@@ -410,6 +553,10 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     p.down = (const unsigned char *)down, p.up = (const unsigned char *)up;
     p.adapter = adapter, p.scale = scale, p.C = C;
     p.part = (float *)workspace, p.low = (float *)((unsigned char *)workspace + plan.low_at);
+    p.cut = (_Float16 *)((unsigned char *)workspace + plan.cut_at);
+    p.ex = (int32_t *)((unsigned char *)workspace + plan.ex_at);
+    p.order = plan.few ? nullptr : (int32_t *)((unsigned char *)workspace + plan.order_at);
+    p.rank16 = (int)((rank + 15) / 16 * 16);
     p.lda = lda * 2, p.ldb = ldb * 2, p.ldc = ldc * 4;
     p.ld_down = ld_down * 2, p.stride_down = stride_down * 2, p.ld_up = ld_up * 2, p.stride_up = stride_up * 2;
     p.M = (int)M, p.N = (int)N, p.K = (int)K, p.adapters = (int)adapters, p.rank = (int)rank;
@@ -419,43 +566,63 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     // The DMA copies whole 16-byte chunks and reaches a tile's rows with
     // 32-bit byte offsets.
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
-    const bool near = lda <= far && ldb <= far && ld_down <= far;
-    const bool ring = near && K % 8 == 0 && N % 8 == 0 && rank % 8 == 0;
-    const bool ring_main = near && K % 8 == 0 && N % 8 == 0;
+    const bool near = lda <= far && ldb <= far && ld_down <= far && M * lda <= (int64_t)UINT32_MAX / 2;
+    const bool ring_main = near && chunk_stays_in_page(A, M, K, lda) && chunk_stays_in_page(B, K, N, ldb);
+    const bool ring = ring_main && chunk_stays_in_page(down, K, rank, ld_down, adapters, stride_down);
 
-    const int64_t low_tiles = ceil_quot(M, plan.bm);
+    const int64_t low_tiles = ceil_quot(M, PART_TILE);
     p.low_cols = (int)ceil_quot(rank, 64);
-    p.low_lanes = low_tiles >= 64 ? 4 : plan.bm;
+    // Workgroups that share a row tile's distinct adapters: as many as fill the
+    // chip a few times over (one without work costs about 3 us of a slot).
+    const int64_t lanes = 1024 / (low_tiles * plan.low_parts * p.low_cols);
+    p.low_lanes = (int)(lanes < 1 ? 1 : lanes > PART_TILE ? PART_TILE : lanes);
     p.row_tiles = (int)low_tiles, p.col_tiles = (int)ceil_quot(N, 64);
     const int64_t shared = plan.few ? ceil_quot(low_tiles * p.col_tiles * plan.parts, 8) * 8 : 0;
-    const int64_t wgs = shared + low_tiles * plan.low_parts * p.low_cols * p.low_lanes;
+    const int64_t low_wgs = ceil_quot(low_tiles * plan.low_parts * p.low_cols * p.low_lanes, 8) * 8;
+    const int64_t wgs = low_wgs + shared;
     if (wgs > (int64_t)UINT32_MAX / 256 || ceil_quot(M, 64) > INT32_MAX / 8 / ceil_quot(N, 64) ||
         ceil_quot(N, JOIN_THREADS) > 65535)
         return TDG_ERR_UNSUPPORTED;
-    p.shared_wgs = (int)shared;
+    p.low_wgs = (int)low_wgs;
     rc = device_check();
     if (rc != TDG_OK) return rc;
     const void *fn;
-    if (plan.bm == 32)
-        fn = ring ? (const void *)&k_lora_parts_ring<32, 64, 1, 2, 4> : (const void *)&k_lora_parts_any<32, 64, 1, 2>;
-    else
-        fn = ring ? (const void *)&k_lora_parts_ring<64, 64, 2, 2, 4> : (const void *)&k_lora_parts_any<64, 64, 2, 2>;
-    rc = launch(fn, dim3((unsigned)wgs), plan.bm == 32 ? 128 : 256, &p, stream);
+    if (!plan.few) {
+        rc = launch((const void *)&k_lora_sort, dim3((unsigned)ceil_quot(M, SORT_ROWS)), SORT_THREADS, &p, stream);
+        if (rc != TDG_OK) return rc;
+    }
+    fn = ring ? (const void *)&k_lora_parts_ring : (const void *)&k_lora_parts_any;
+    rc = launch(fn, dim3((unsigned)wgs), 256, &p, stream);
     if (rc != TDG_OK) return rc;
     if (plan.few) {
-        const bool v4 = N % 4 == 0;
-        fn = v4 ? (const void *)&k_lora_join<4> : (const void *)&k_lora_join<1>;
-        return launch(fn, dim3((unsigned)ceil_quot(M, JOIN_ROWS), (unsigned)ceil_quot(N, JOIN_THREADS * (v4 ? 4 : 1))),
-                      JOIN_THREADS, &p, stream);
+        const int v = N % 4 == 0 ? (M <= 64 ? 2 : 4) : 1, rows = 1;
+        fn = v == 4   ? (const void *)&k_lora_join<4, 1>
+             : v == 2 ? (const void *)&k_lora_join<2, 1> : (const void *)&k_lora_join<1, 1>;
+        return launch(fn, dim3((unsigned)ceil_quot(M, rows), (unsigned)ceil_quot(N, JOIN_THREADS * v)), JOIN_THREADS,
+                      &p, stream);
     }
-    const bool big = ring_main && ceil_quot(M, 256) * ceil_quot(N, 256) >= 128;
-    const int bt = big ? 256 : 128;
-    p.row_tiles = (int)ceil_quot(M, bt), p.col_tiles = (int)ceil_quot(N, bt);
+    rc = launch((const void *)&k_lora_split, dim3((unsigned)ceil_quot(M, SPLIT_THREADS / 64)), SPLIT_THREADS, &p, stream);
+    if (rc != TDG_OK) return rc;
+    const bool ring_up = ring_main && chunk_stays_in_page(up, rank, N, ld_up, adapters, stride_up);
+    // The largest tile that gives most CUs a workgroup (M x 4096 x 4096 with 8
+    // adapters of rank 64, us, 256 / 128 / 128 x 64 wide tiles: M = 4096 172 /
+    // 221 / 274, M = 1024 121 / 77 / 91, M = 512 131 / 72 / 59).
+    auto tiles = [&](int bm, int bn) { return ceil_quot(M, bm) * ceil_quot(N, bn); };
+    int bm = 128, bn = 128, threads = 256;
+    if (!ring_up) {
+        fn = (const void *)&k_lora_main_any<128, 128, 2, 2>;
+    } else if (tiles(256, 256) >= 128) {
+        fn = (const void *)&k_lora_main_ring<256, 256, 2, 4, 2>;
+        bm = bn = 256, threads = 512;
+    } else if (tiles(128, 128) >= 192) {
+        fn = (const void *)&k_lora_main_ring<128, 128, 2, 2, 4>;
+    } else {
+        fn = (const void *)&k_lora_main_ring<128, 64, 4, 1, 4>;
+        bn = 64;
+    }
+    p.row_tiles = (int)ceil_quot(M, bm), p.col_tiles = (int)ceil_quot(N, bn);
     const int64_t grid = ceil_quot((int64_t)p.row_tiles * p.col_tiles, 8) * 8;
-    fn = big         ? (const void *)&k_lora_main_ring<256, 256, 2, 4, 2>
-         : ring_main ? (const void *)&k_lora_main_ring<128, 128, 2, 2, 2>
-                     : (const void *)&k_lora_main_any<128, 128, 2, 2>;
-    return launch(fn, dim3((unsigned)grid), big ? 512 : 256, &p, stream);
+    return launch(fn, dim3((unsigned)grid), threads, &p, stream);
 }
 
 }  // extern "C"
