@@ -273,6 +273,9 @@ GROUPED = [  # rows of each group, K, N
     ([127, 128, 129], 128, 136), ([300, 1, 0, 257], 200, 264), ([31, 32, 33, 64, 65], 65, 67),
     ([5, 70], 1000, 33), ([7, 2, 9], 7, 300), ([40] * 70, 40, 16), ([600], 520, 512), ([260, 20, 500], 264, 250),
     ([2, 30, 1, 4], 2048, 96), ([64, 64], 0, 16), ([513, 255], 96, 320),
+    # enough tiles for the larger ones, and for several of them per workgroup
+    ([300, 200], 72, 6400), ([300, 200], 72, 9001), ([1100, 947], 72, 8200), ([20, 31], 1000, 1600),
+    ([20, 31], 1000, 2400), ([3, 0, 70, 1] * 66, 264, 250),
 ]
 
 

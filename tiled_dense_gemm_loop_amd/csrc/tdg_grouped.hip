@@ -48,12 +48,17 @@ int grouped_args_ok(int lay, int64_t groups, const int32_t *offsets, int64_t row
 struct Variant {
     const void *fn;
     int bm, bn, threads;
+    int most_wgs;  // workgroups that are launched at most (they take several tiles)
 };
 
 #define TDG_BY_LAYOUT(KERNEL, ...)                                              \
     (lay == tdg::LAY_NN   ? (const void *)&tdg::KERNEL<tdg::LAY_NN, __VA_ARGS__> \
      : lay == tdg::LAY_NT ? (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__> \
                           : (const void *)&tdg::KERNEL<tdg::LAY_TN, __VA_ARGS__>)
+
+#define TDG_ROWS(KERNEL, ...)                                                   \
+    (lay == tdg::LAY_NN ? (const void *)&tdg::KERNEL<tdg::LAY_NN, __VA_ARGS__> \
+                        : (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__>)
 
 Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
                const void *B, int64_t ldb, int64_t stride_b) {
@@ -65,7 +70,7 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
                             : tdg::chunk_stays_in_page(B, lay == tdg::LAY_NN ? K : N, lay == tdg::LAY_NN ? N : K, ldb,
                                                        groups, stride_b));
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
-    if (!chunks || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256};
+    if (!chunks || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256, INT32_MAX};
     // Tiles that the product is expected to have: half a row tile more per
     // group that can have rows than the rows fill, one at the least.
     const int64_t live = groups < rows ? groups : rows;
@@ -84,10 +89,11 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
     // rows, 64 groups, K = 2048, N = 1408: 24 / 13; 500 rows, 4 groups, K = N
     // = 1000: 13 / 9).
     if (tiles(256) >= 256 && (tn || rows >= 192 * live))
-        return {TDG_BY_LAYOUT(tdg_grouped_ring, 256, 256, 2, 4, 2), 256, 256, 512};
-    if (tiles(128) > 256) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256};
-    if (tiles(128) >= 192) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256};
-    return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 64, 2, 2, 4), 64, 64, 256};
+        return tn ? Variant{(const void *)&tdg::tdg_grouped_tn_loop<256, 256, 2, 4, 2>, 256, 256, 512, 256}
+                  : Variant{TDG_ROWS(tdg_grouped_ring, 256, 256, 2, 4, 2), 256, 256, 512, INT32_MAX};
+    if (tiles(128) > 256) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256, INT32_MAX};
+    if (tiles(128) >= 192) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256, INT32_MAX};
+    return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 64, 2, 2, 4), 64, 64, 256, INT32_MAX};
 }
 
 int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, int64_t M, int64_t N, int64_t K,
@@ -105,13 +111,19 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     a.offsets = offsets;
     a.groups = (int)groups, a.rows = (int)rows, a.M = (int)M, a.N = (int)N, a.K = (int)K;
     a.tiles_m = (int)tdg::ceil_quot(M, v.bm), a.tiles_n = (int)tdg::ceil_quot(N, v.bn);
+    // A and B fit in half of the 256 MB memory-side cache, and C is much larger.
+    const uint64_t in_bytes = (uint64_t)rows * (uint64_t)(M + N) * 2, out_bytes = (uint64_t)groups * M * N * 4;
+    a.warm = in_bytes <= (128u << 20) && out_bytes / 4 >= in_bytes;
     a.flags = tdg::debug_flags_now();
     // Most row tiles: every group can end inside a tile, and needs a row for
     // it.
     const int64_t row_tiles = lay == tdg::LAY_TN ? groups * a.tiles_m
                                                  : rows / v.bm + (groups < rows ? groups : rows);
     if (row_tiles > INT32_MAX / a.tiles_n) return TDG_ERR_UNSUPPORTED;
-    const int64_t grid = tdg::ceil_quot(row_tiles * a.tiles_n, 8) * 8;
+    int64_t grid = tdg::ceil_quot(row_tiles * a.tiles_n, 8) * 8;
+    if (grid > INT32_MAX - 65536) return TDG_ERR_UNSUPPORTED;
+    a.tiles_most = (int)grid;
+    if (grid > v.most_wgs) grid = v.most_wgs;
     if (grid > (int64_t)UINT32_MAX / v.threads) return TDG_ERR_UNSUPPORTED;
     rc = tdg::device_check();
     if (rc != TDG_OK) return rc;

@@ -36,7 +36,9 @@ struct GroupedArgs {
     int M, N, K;   // M: TN only (columns of A); K: NN and NT only
     int tiles_m;   // TN only: ceil(M / BM)
     int tiles_n;   // ceil(N / BN)
-    int flags;     // TDG_DEBUG_* bits
+    int tiles_most;  // no tile has this number or a higher one
+    int warm;        // read A and B once at the start (tdg_grouped_tn_loop)
+    int flags;       // TDG_DEBUG_* bits
 };
 
 // One operand's LDS image: BX rows (or columns) of the product, 64 k.
@@ -72,6 +74,14 @@ struct Image {
     }
 };
 
+// threadIdx.x as a value of its own: in a loop over tiles, what is computed
+// from it is computed again for each tile rather than kept in registers.
+__device__ static __forceinline__ int thread_again() {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    return tid;
+}
+
 // Where a workgroup works: its group, the group's rows [lo, hi), the tile's
 // first row (TN: column of A) and its column tile.
 struct GroupedTile {
@@ -80,7 +90,9 @@ struct GroupedTile {
 };
 
 __device__ static __forceinline__ int group_offset(const GroupedArgs &a, int g) {
-    return min(max(a.offsets[g], 0), a.rows);
+    // through the scalar cache: it does not touch the count of copies in flight
+    typedef const int32_t __attribute__((address_space(4))) * Table;
+    return min(max(((Table)(uintptr_t)a.offsets)[g], 0), a.rows);
 }
 
 // Tile order inside a tiles_m x tiles_n block: groups of four tile rows, so
@@ -108,12 +120,12 @@ __device__ static __forceinline__ int xcd_tile(int b, int total) {
 // less than a launch that would write them down.  The grid is sized for the
 // most tiles that the rows can make; workgroups past the total end at once.
 template <int LAY, int BM>
-__device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a) {
+__device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a, int b) {
     GroupedTile t;
     t.ok = false;
     if constexpr (LAY == LAY_TN) {
         const int per_g = a.tiles_m * a.tiles_n;
-        const int id = xcd_tile(blockIdx.x, a.groups * per_g);
+        const int id = xcd_tile(b, a.groups * per_g);
         if (id < 0) return t;
         t.g = id / per_g;
         int tm;
@@ -124,7 +136,7 @@ __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a) {
         t.ok = true;
         return t;
     }
-    const int lane = threadIdx.x & 63;
+    const int lane = thread_again() & 63;
     const int run = (a.groups + 63) >> 6;
     const int g0 = min(a.groups, lane * run), g1 = min(a.groups, g0 + run);
     int mine = 0;  // row tiles of the lane's groups
@@ -141,7 +153,7 @@ __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a) {
         const int up = __shfl_up(upto, d);
         if (lane >= d) upto += up;
     }
-    const int id = xcd_tile(blockIdx.x, __builtin_amdgcn_readlane(upto, 63) * a.tiles_n);
+    const int id = xcd_tile(b, __builtin_amdgcn_readlane(upto, 63) * a.tiles_n);
     if (id < 0) return t;
     const int at = id / a.tiles_n;  // the how manieth row tile: finds the group
     const int owner = __builtin_amdgcn_readfirstlane(__ffsll(__ballot(upto > at)) - 1);
@@ -167,12 +179,12 @@ __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a) {
     return t;
 }
 
-// Accumulators -> C: lane l of a 32x32 block holds column l % 32 of rows
+// Accumulators -> C (returns whether the tile was stored whole): lane l of a 32x32 block holds column l % 32 of rows
 // 8 (v / 4) + 4 (l / 32) + v % 4.
 template <int MI, int NI>
-__device__ static __forceinline__ void store_tile(unsigned char *C, int64_t ldc, int row0, int row_end, int col0,
+__device__ static __forceinline__ bool store_tile(unsigned char *C, int64_t ldc, int row0, int row_end, int col0,
                                                   int col_end, const f32x16 (&acc)[MI][NI]) {
-    const int lane = threadIdx.x & 63;
+    const int lane = thread_again() & 63;
     const int rq = (lane >> 5) * 4;
     auto store = [&](auto masked, auto streaming) __attribute__((always_inline)) {
 #pragma unroll
@@ -195,6 +207,7 @@ __device__ static __forceinline__ void store_tile(unsigned char *C, int64_t ldc,
     if (inside && lines) store(std::false_type{}, std::true_type{});
     else if (inside) store(std::false_type{}, std::false_type{});
     else store(std::true_type{}, std::false_type{});
+    return inside;
 }
 
 // Where A's rows are: row x of the product at `off(x)` bytes from A.  RowsFrom:
@@ -334,25 +347,44 @@ struct GroupedRing {
     static_assert(B_STEP % 16 == 0 || (LAY != LAY_NT && B_STEP % 4 == 0), "B swizzle must repeat");
     static_assert(STAGES >= 2 && AHEAD * ND <= 63 && SMEM <= 160 * 1024, "ring");
 
+    static constexpr bool AKC = LAY != LAY_TN, BKC = LAY == LAY_NT;
+    static constexpr int FD = 3;                   // k steps that fragments are read ahead
+    static constexpr int STORES = MI * NI * 16;    // store instructions of a whole tile, per wave
+
+    // A tile's copies: per-lane byte offsets of the thread's chunks from the
+    // tile's first row and k.  KC: one per chunk (the rows are clamped); RC:
+    // one for all (the k rows advance with the wave-uniform base).
+    uint32_t a_off[AKC ? CA : 1], b_off[BKC ? CB : 1];
+    const unsigned char *a_base, *b_base;
+    int64_t lda, ldb;
+    int len, nt;       // k of the tile, and its K tiles
+    uint32_t lds_at;   // where the wave's first chunks go in the first buffer
+
     // As GroupedAny::run; here `rows` gives offsets below 2^32.
     template <class Rows>
     __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, Rows rows,
                                                const unsigned char *B, int64_t ldb, int x0, int x_end, int y0,
                                                int y_end, int k_lo, int k_hi, unsigned char *smem,
                                                f32x16 (&acc)[MI][NI]) {
-        const int nt = (k_hi - k_lo + 63) >> 6;
-        if (nt <= 0) return;
-        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int wm = wave % WM, wn = wave / WM;
-        const uint32_t smem_addr = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)smem;
-        constexpr bool AKC = LAY != LAY_TN, BKC = LAY == LAY_NT;
+        GroupedRing r;
+        r.aim(A, lda, rows, B, ldb, x0, x_end, y0, y_end, k_lo, k_hi, smem);
+        r.start();
+        r.finish(smem, acc, false);
+    }
 
-        // Per-lane byte offsets of the thread's chunks from the tile's first
-        // row and k.  KC: one per chunk (the rows are clamped); RC: one for
-        // all (the k rows advance with the wave-uniform base).
+    template <class Rows>
+    __device__ __forceinline__ void aim(const unsigned char *A, int64_t lda_, Rows rows, const unsigned char *B,
+                                        int64_t ldb_, int x0, int x_end, int y0, int y_end, int k_lo, int k_hi,
+                                        unsigned char *smem) {
+        lds_at = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)smem +
+                 (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
+        lda = lda_, ldb = ldb_;
+        len = k_hi - k_lo;
+        nt = (len + 63) >> 6;
+        if (nt <= 0) return;
+        const int tid = thread_again();
         const int a_r = tid / IA::CPR, a_c = (tid % IA::CPR) ^ IA::swz(a_r);
         const int b_r = tid / IB::CPR, b_c = (tid % IB::CPR) ^ IB::swz(b_r);
-        uint32_t a_off[AKC ? CA : 1], b_off[BKC ? CB : 1];
 #pragma unroll
         for (int i = 0; i < (AKC ? CA : 1); i++)
             a_off[i] = AKC ? (uint32_t)(rows.off(min(x0 + i * A_STEP + a_r, x_end - 1)) + a_c * 16)
@@ -361,42 +393,104 @@ struct GroupedRing {
         for (int i = 0; i < (BKC ? CB : 1); i++)
             b_off[i] = BKC ? (uint32_t)(min(i * B_STEP + b_r, y_end - 1 - y0) * ldb + b_c * 16)
                            : (uint32_t)(b_r * ldb + min(b_c * 8, (y_end - 1 - y0) & ~7) * 2);
-        const unsigned char *a_base =
-            A + (AKC ? (int64_t)k_lo * 2 : (int64_t)k_lo * lda + (int64_t)x0 * 2);
-        const unsigned char *b_base =
-            B + (BKC ? (int64_t)y0 * ldb + (int64_t)k_lo * 2 : (int64_t)k_lo * ldb + (int64_t)y0 * 2);
-        const uint64_t zero_addr = (uint64_t)(uintptr_t)tdg_zero16;
-        auto issue = [&](uint32_t st, int kt, int d, auto checked) __attribute__((always_inline)) {
-            const bool is_a = d < CA;
-            const int i = is_a ? d : d - CA;
-            const uint32_t m0 = smem_addr + st + (uint32_t)wave * 1024u +
-                                (uint32_t)((is_a ? 0 : IA::BYTES) + i * NT * 16);
-            kt = __builtin_amdgcn_readfirstlane(kt);
-            const unsigned char *base =
-                is_a ? a_base + (AKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * A_STEP) * lda)
-                     : b_base + (BKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * B_STEP) * ldb);
-            const uint32_t off = is_a ? a_off[AKC ? i : 0] : b_off[BKC ? i : 0];
-            if constexpr (decltype(checked)::value) {
-                // first k of the chunk, counted from the tile's
-                const int k = is_a ? (AKC ? a_c * 8 : i * A_STEP + a_r) : (BKC ? b_c * 8 : i * B_STEP + b_r);
-                const uint64_t p = (uint64_t)(uintptr_t)(base + off);
-                const uint64_t src = k < k_hi - k_lo - kt * 64 ? p : zero_addr;
-                asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
-            } else {
-                // The base may have been written to its scalar registers by a
-                // vector instruction just before (v_readlane, where the
-                // compiler reloads spilled ones).  A vector-memory instruction
-                // may read them five wait states later at the earliest, which
-                // the compiler does not count for inline assembly; a scalar
-                // one may read them at once, and what it writes is safe.
-                uint64_t safe;
-                asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
-                             : "=&s"(safe)
-                             : "v"(off), "s"(base), "{m0}"(m0)
-                             : "memory");
-            }
-        };
+        a_base = A + (AKC ? (int64_t)k_lo * 2 : (int64_t)k_lo * lda + (int64_t)x0 * 2);
+        b_base = B + (BKC ? (int64_t)y0 * ldb + (int64_t)k_lo * 2 : (int64_t)k_lo * ldb + (int64_t)y0 * 2);
+    }
 
+    __device__ static __forceinline__ uint32_t stage(int t) { return (uint32_t)((t % STAGES) * STAGE); }
+
+    // Copies chunk set d (A's first, then B's) of K tile kt into its buffer.
+    template <bool CHECKED>
+    __device__ __forceinline__ void issue(int kt, int d) const {
+        const bool is_a = d < CA;
+        const int i = is_a ? d : d - CA;
+        const uint32_t m0 = lds_at + stage(kt) + (uint32_t)((is_a ? 0 : IA::BYTES) + i * NT * 16);
+        kt = __builtin_amdgcn_readfirstlane(kt);
+        const unsigned char *base = is_a ? a_base + (AKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * A_STEP) * lda)
+                                         : b_base + (BKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * B_STEP) * ldb);
+        const uint32_t off = is_a ? a_off[AKC ? i : 0] : b_off[BKC ? i : 0];
+        if constexpr (CHECKED) {
+            // first k of the chunk, counted from the tile's
+            const int tid = thread_again();
+            const int a_r = tid / IA::CPR, a_c = (tid % IA::CPR) ^ IA::swz(a_r);
+            const int b_r = tid / IB::CPR, b_c = (tid % IB::CPR) ^ IB::swz(b_r);
+            const int k = is_a ? (AKC ? a_c * 8 : i * A_STEP + a_r) : (BKC ? b_c * 8 : i * B_STEP + b_r);
+            const uint64_t p = (uint64_t)(uintptr_t)(base + off);
+            const uint64_t src = k < len - kt * 64 ? p : (uint64_t)(uintptr_t)tdg_zero16;
+            asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+        } else {
+            // The base may have been written to its scalar registers by a
+            // vector instruction just before (v_readlane, where the compiler
+            // reloads spilled ones).  A vector-memory instruction may read
+            // them five wait states later at the earliest, which the compiler
+            // does not count for inline assembly; a scalar one may read them
+            // at once, and what it writes is safe.
+            uint64_t safe;
+            asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+                         : "=&s"(safe)
+                         : "v"(off), "s"(base), "{m0}"(m0)
+                         : "memory");
+        }
+    }
+
+    // The first tiles into the buffers, all of which are free.
+    __device__ __forceinline__ void start() const {
+#pragma unroll
+        for (int p = 0; p < STAGES; p++) {
+            if (p >= nt) break;
+            if ((len & 63) != 0 && p == nt - 1) {  // the tile that the end of k cuts
+#pragma unroll
+                for (int d = 0; d < ND; d++) issue<true>(p, d);
+            } else {
+#pragma unroll
+                for (int d = 0; d < ND; d++) issue<false>(p, d);
+            }
+        }
+    }
+
+    // Waits until at most the n youngest tiles are still in flight.
+    __device__ static __forceinline__ void wait_tiles(int n) {
+        if (n >= AHEAD) wait_vmcnt<AHEAD * ND>();
+        else if (AHEAD > 4 && n == 4) wait_vmcnt<4 * ND <= 63 ? 4 * ND : 0>();
+        else if (AHEAD > 3 && n == 3) wait_vmcnt<3 * ND <= 63 ? 3 * ND : 0>();
+        else if (AHEAD > 2 && n == 2) wait_vmcnt<2 * ND <= 63 ? 2 * ND : 0>();
+        else if (AHEAD > 1 && n == 1) wait_vmcnt<ND <= 63 ? ND : 0>();
+        else wait_vmcnt<0>();
+    }
+
+    // Rows along k whose end splits a chunk: its elements from that end on are
+    // cleared once the last tile has landed, one thread per row.
+    __device__ __forceinline__ void clear_split(unsigned char *smem, int t) const {
+        const int split = AKC || BKC ? len & 7 : 0;
+        if (split == 0 || t != nt - 1) return;
+        const int c = (len & 63) >> 3;
+        auto clear = [&](unsigned char *p) __attribute__((always_inline)) {
+            const u32x4 v = lds_read16(p);
+            u32x4 w;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int left = split - 2 * j;  // elements of word j that stay
+                w[j] = v[j] & (left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u);
+            }
+            lds_write16(p, w);
+        };
+        unsigned char *st = smem + stage(t);
+        if (AKC)
+            for (int r = threadIdx.x; r < BM; r += NT) clear(st + r * 128 + ((c ^ IA::swz(r)) << 4));
+        if (BKC)
+            for (int r = threadIdx.x; r < BN; r += NT) clear(st + IA::BYTES + r * 128 + ((c ^ IB::swz(r)) << 4));
+        __syncthreads();
+    }
+
+    // acc += the product of a tile whose copies have been started.  `stores`:
+    // STORES store instructions of this wave came after start():
+    // they may be under way still.  Loads and stores leave the vmcnt counter in the order
+    // of issue, so the waits for the tiles of start() let the stores run on.
+    // Every copy has landed at the end.
+    __device__ __forceinline__ void finish(unsigned char *smem, f32x16 (&acc)[MI][NI], bool stores) const {
+        if (nt <= 0) return;
+        const int tid = thread_again(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave % WM, wn = wave / WM;
         // Fragment reads: KC one offset per step, RC one per 32-wide block
         // (the swizzle of a k row repeats every four rows).
         uint32_t fa_off[AKC ? 4 : MI], fb_off[BKC ? 4 : NI];
@@ -416,12 +510,11 @@ struct GroupedRing {
             else return Mfma<DT_F16>::read_b(st + fb_off[ni] + (s * 16) * IB::ROWB,
                                              st + fb_off[ni] + (s * 16 + 4) * IB::ROWB);
         };
-        constexpr int FD = 3;
         u32x4 fa[4][MI], fb[4][NI];
 
         // One k step's MFMAs, with the fragment reads of step rs (of buffer
-        // rst) and copies [lo, hi) of tile dma_kt spread between them.
-        auto step = [&](int s, const unsigned char *rst, int rs, uint32_t dma_st, int dma_kt, int lo, int hi,
+        // rst) and copies [lo, hi) of tile kt spread between them.
+        auto step = [&](int s, const unsigned char *rst, int rs, int kt, int lo, int hi,
                         auto checked) __attribute__((always_inline)) {
             constexpr int NM = MI * NI, NR = MI + NI;
 #pragma unroll
@@ -436,61 +529,14 @@ struct GroupedRing {
                 const int nd = hi - lo;
 #pragma unroll
                 for (int d = (m * nd + NM - 1) / NM; d < ((m + 1) * nd + NM - 1) / NM; d++)
-                    issue(dma_st, dma_kt, lo + d, checked);
+                    issue<decltype(checked)::value>(kt, lo + d);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        auto stage = [&](int t) { return (uint32_t)((t % STAGES) * STAGE); };
-
-        // The tile that the end of k cuts is copied with the checked form.
-        const bool cut = ((k_hi - k_lo) & 63) != 0;
-        // Prologue: every buffer is free.
-#pragma unroll
-        for (int p = 0; p <= AHEAD; p++) {
-            if (p >= nt) break;
-            if (cut && p == nt - 1) {
-#pragma unroll
-                for (int d = 0; d < ND; d++) issue(stage(p), p, d, std::true_type{});
-            } else {
-#pragma unroll
-                for (int d = 0; d < ND; d++) issue(stage(p), p, d, std::false_type{});
-            }
-        }
-        // Waits until at most the n youngest tiles are still in flight.
-        auto wait_tiles = [&](int n) __attribute__((always_inline)) {
-            if (n >= AHEAD) wait_vmcnt<AHEAD * ND>();
-            else if (AHEAD > 4 && n == 4) wait_vmcnt<4 * ND <= 63 ? 4 * ND : 0>();
-            else if (AHEAD > 3 && n == 3) wait_vmcnt<3 * ND <= 63 ? 3 * ND : 0>();
-            else if (AHEAD > 2 && n == 2) wait_vmcnt<2 * ND <= 63 ? 2 * ND : 0>();
-            else if (AHEAD > 1 && n == 1) wait_vmcnt<ND <= 63 ? ND : 0>();
-            else wait_vmcnt<0>();
-        };
-        // Rows along k whose end splits a chunk: its elements from that end on
-        // are cleared once the last tile has landed, one thread per row.
-        const int split = AKC || BKC ? (k_hi - k_lo) & 7 : 0;
-        auto clear_split = [&](int t) __attribute__((always_inline)) {
-            if (split == 0 || t != nt - 1) return;
-            const int c = ((k_hi - k_lo) & 63) >> 3;
-            auto clear = [&](unsigned char *p) __attribute__((always_inline)) {
-                const u32x4 v = lds_read16(p);
-                u32x4 w;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int left = split - 2 * j;  // elements of word j that stay
-                    w[j] = v[j] & (left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u);
-                }
-                lds_write16(p, w);
-            };
-            unsigned char *st = smem + stage(t);
-            if (AKC)
-                for (int r = tid; r < BM; r += NT) clear(st + r * 128 + ((c ^ IA::swz(r)) << 4));
-            if (BKC)
-                for (int r = tid; r < BN; r += NT) clear(st + IA::BYTES + r * 128 + ((c ^ IB::swz(r)) << 4));
-            __syncthreads();
-        };
-        wait_tiles(min(AHEAD, nt - 1));
+        if (stores) wait_vmcnt<STORES <= 63 ? STORES : 63>();  // the tiles may be the older ones: all of them then
+        else wait_tiles(min(AHEAD, nt - 1));
         __syncthreads();
-        clear_split(0);
+        clear_split(smem, 0);
 #pragma unroll
         for (int s = 0; s < FD; s++) {
 #pragma unroll
@@ -509,21 +555,22 @@ struct GroupedRing {
                     if (r == 4) {
                         // tile t+1 has landed, and every wave has read tile t
                         if constexpr (decltype(copies)::value) {
-                            wait_vmcnt<(AHEAD - 1) * ND>();
+                            if (!(stores && t < AHEAD)) wait_vmcnt<(AHEAD - 1) * ND>();
                             __syncthreads();
                         } else if (t + 1 < nt) {
-                            wait_tiles(nt - 2 - t);
+                            if (!(stores && t < AHEAD)) wait_tiles(nt - 2 - t);
                             __syncthreads();
-                            clear_split(t + 1);
+                            clear_split(smem, t + 1);
                         }
                         next = smem + stage(t + 1);
                     }
                     const int part = decltype(copies)::value && r >= 4 && r < 6 ? r - 4 : -1;
-                    step(s, r < 4 ? cur : next, r & 3, stage(t), t + STAGES, part < 0 ? 0 : part * ND / 2,
+                    step(s, r < 4 ? cur : next, r & 3, t + STAGES, part < 0 ? 0 : part * ND / 2,
                          part < 0 ? 0 : (part + 1) * ND / 2, checked);
                 }
             }
         };
+        const bool cut = (len & 63) != 0;
         const int full = max(0, nt - STAGES);  // tiles with a later one to copy
         tiles(0, cut ? max(0, full - 1) : full, std::true_type{}, std::false_type{});
         if (cut) tiles(max(0, full - 1), full, std::true_type{}, std::true_type{});
@@ -549,36 +596,123 @@ __device__ static __forceinline__ void poison_lds(int flags, unsigned char *smem
     }
 }
 
-// One tile of a grouped product per workgroup; E is GroupedAny or GroupedRing.
-template <class E, int LAY, int BM, int BN, int WM, int WN>
-__device__ static __forceinline__ void grouped_product(const GroupedArgs &a, unsigned char *smem) {
-    constexpr bool TN = LAY == LAY_TN;
-    const GroupedTile t = find_tile<LAY, BM>(a);
-    if (!t.ok) return;
-    poison_lds<E::SMEM, E::NT>(a.flags, smem);
-    const int x_end = TN ? a.M : t.hi, y0 = t.tn * BN;
-    f32x16 acc[E::MI][E::NI];
-    clear_acc(acc);
-    E::run(a.A + (TN ? 0 : (int64_t)t.x0 * a.lda), a.lda, RowsFrom{t.x0, a.lda},
-           a.B + (TN ? 0 : (int64_t)t.g * a.stride_b), a.ldb, t.x0, x_end, y0, a.N, TN ? t.lo : 0, TN ? t.hi : a.K,
-           smem, acc);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    store_tile<E::MI, E::NI>(a.C + (TN ? (int64_t)t.g * a.stride_c : 0), a.ldc, t.x0 + (wave % WM) * E::WTM, x_end,
-                             y0 + (wave / WM) * E::WTN, a.N, acc);
-}
+// Whether C tiles remain for workgroup b, and where: A's and C's rows (TN:
+// A's columns) x0 .. x_end - 1, the columns from y0 on, k_lo .. k_hi - 1.
+template <int LAY, int BM, int BN>
+struct GroupedWork {
+    GroupedTile t;
+    __device__ __forceinline__ bool find(const GroupedArgs &a, int b) {
+        t = find_tile<LAY, BM>(a, b);
+        return t.ok;
+    }
+    __device__ __forceinline__ int x_end(const GroupedArgs &a) const { return LAY == LAY_TN ? a.M : t.hi; }
+    __device__ __forceinline__ int y0() const { return t.tn * BN; }
+    __device__ __forceinline__ const unsigned char *A(const GroupedArgs &a) const {
+        return a.A + (LAY == LAY_TN ? 0 : (int64_t)t.x0 * a.lda);
+    }
+    __device__ __forceinline__ const unsigned char *B(const GroupedArgs &a) const {
+        return a.B + (LAY == LAY_TN ? 0 : (int64_t)t.g * a.stride_b);
+    }
+    __device__ __forceinline__ int k_lo() const { return LAY == LAY_TN ? t.lo : 0; }
+    __device__ __forceinline__ int k_hi(const GroupedArgs &a) const { return LAY == LAY_TN ? t.hi : a.K; }
+    template <class E, int WM>
+    __device__ __forceinline__ bool store(const GroupedArgs &a, const f32x16 (&acc)[E::MI][E::NI]) const {
+        const int wave = __builtin_amdgcn_readfirstlane(thread_again() >> 6);
+        return store_tile<E::MI, E::NI>(a.C + (LAY == LAY_TN ? (int64_t)t.g * a.stride_c : 0), a.ldc,
+                                        t.x0 + (wave % WM) * E::WTM, x_end(a), y0() + (wave / WM) * E::WTN, a.N, acc);
+    }
+};
 
 template <int LAY, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a) {
     typedef GroupedAny<LAY, BM, BN, WM, WN> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    grouped_product<E, LAY, BM, BN, WM, WN>(a, smem);
+    GroupedWork<LAY, BM, BN> w;
+    if (!w.find(a, blockIdx.x)) return;
+    poison_lds<E::SMEM, E::NT>(a.flags, smem);
+    f32x16 acc[E::MI][E::NI];
+    clear_acc(acc);
+    E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
+           smem, acc);
+    w.template store<E, WM>(a, acc);
 }
 
 template <int LAY, int BM, int BN, int WM, int WN, int STAGES>
 __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_ring(GroupedArgs a) {
     typedef GroupedRing<LAY, BM, BN, WM, WN, STAGES> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    grouped_product<E, LAY, BM, BN, WM, WN>(a, smem);
+    GroupedWork<LAY, BM, BN> w;
+    if (!w.find(a, blockIdx.x)) return;
+    poison_lds<E::SMEM, E::NT>(a.flags, smem);
+    f32x16 acc[E::MI][E::NI];
+    clear_acc(acc);
+    E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
+           smem, acc);
+    w.template store<E, WM>(a, acc);
+}
+
+// Asks for a word of every 128-byte line of a rows x cols matrix of 2-byte
+// elements, the lines dealt to all threads of the grid; the words land in 256
+// bytes of LDS that nobody reads.
+__device__ static __forceinline__ void touch(const unsigned char *P, int64_t ld, int lo, int hi, int cols,
+                                             unsigned char *lds) {
+    const int lines = (cols * 2 + 127) / 128;
+    const uint32_t m0 = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)lds;
+    const int64_t all = (int64_t)(hi - lo) * lines, step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += step) {
+        const int row = (int)(i / lines), line = (int)(i - (int64_t)row * lines);
+        // a word that holds a byte of the row: it lies in that byte's page
+        const uint64_t src = (uint64_t)(uintptr_t)(P + (int64_t)(lo + row) * ld + line * 128) & ~(uint64_t)3;
+        asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+    }
+}
+
+// Weight gradients of many tiles: the sums are short (a group's rows), and
+// writing C takes most of the time.  A workgroup takes tiles b, b + gridDim.x,
+// ... (gridDim.x is a multiple of 8, so it stays with its XCD's run).  The
+// next tile's first copies go out before this one's stores: they land, and the
+// first K tiles are computed, while the stores drain.
+// `warm`: A and B are read once before all else, by all CUs at HBM's full
+// rate, which leaves them in the memory-side cache.  With HBM busy writing C,
+// a read that misses that cache takes long, and every tile waits for some.
+// (8192 rows, 32 groups, 2048 x 4000, A and B in no cache: 330 us
+// without, 271 with; one tile per workgroup 338.)
+template <int BM, int BN, int WM, int WN, int STAGES>
+__global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_tn_loop(GroupedArgs a) {
+    typedef GroupedRing<LAY_TN, BM, BN, WM, WN, STAGES> E;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM + 256];
+    if (a.warm) {
+        const int lo = group_offset(a, 0), hi = group_offset(a, a.groups);
+        touch(a.A, a.lda, lo, hi, a.M, smem + E::SMEM);
+        touch(a.B, a.ldb, lo, hi, a.N, smem + E::SMEM);
+    }
+    GroupedWork<LAY_TN, BM, BN> w;
+    int b = blockIdx.x;
+    if (w.find(a, b)) {
+        poison_lds<E::SMEM, E::NT>(a.flags, smem);
+        E r;
+        auto start = [&]() __attribute__((always_inline)) {
+            r.aim(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(),
+                  w.k_hi(a), smem);
+            r.start();
+        };
+        start();
+        bool stores = false;
+        for (bool more = true; more;) {
+            f32x16 acc[E::MI][E::NI];
+            clear_acc(acc);
+            r.finish(smem, acc, stores);
+            const GroupedWork<LAY_TN, BM, BN> done = w;
+            b += gridDim.x;
+            more = b < a.tiles_most && w.find(a, b);
+            if (more) {
+                __syncthreads();  // every wave has read this tile's last fragments
+                start();
+            }
+            stores = done.template store<E, WM>(a, acc);
+        }
+    }
+    wait_vmcnt<0>();  // the words of touch() land before the LDS is given away
 }
 
 }  // namespace tdg
