@@ -38,7 +38,7 @@ struct LoraArgs {
     _Float16 *cut;  // M rows of low's high part and rest, rank16 each (many rows)
     int32_t *ex;    // M: their rows' power of two
     int rank16;     // the rank, rounded up to 16
-    int32_t *order; // M: the rows, sorted by adapter (many rows)
+    int2 *seat;     // M: row and adapter, sorted by adapter (many rows)
     int64_t lda, ldb, ldc, ld_down, stride_down, ld_up, stride_up;  // bytes
     int M, N, K, adapters, rank;
     int row_tiles, col_tiles;           // of the shared product
@@ -49,8 +49,18 @@ struct LoraArgs {
     int flags;
 };
 
+// Row x of a product over sorted rows.
+struct RowsSeated {
+    const int2 *seat;
+    int64_t ld;
+    __device__ __forceinline__ int64_t off(int x) const { return (int64_t)seat[x].x * ld; }
+};
+
 // At most this many rows are "few": the key of sort_few holds them in 8 bits.
 constexpr int kFewRows = 256;
+
+// Most slices of K that a product is cut into: they are read again.
+constexpr int MAX_PARTS = 8;
 
 // Which adapter a row has, -1 for none.
 __device__ __forceinline__ int adapter_of(const LoraArgs &p, int row) {
@@ -85,13 +95,14 @@ __global__ void __launch_bounds__(SORT_THREADS) k_lora_sort(LoraArgs p) {
     const int base = blockIdx.x * SORT_ROWS;
     count[tid] = 0;
     __syncthreads();
-    int key[SORT_ROWS / SORT_THREADS];
+    int id[SORT_ROWS / SORT_THREADS], key[SORT_ROWS / SORT_THREADS];
 #pragma unroll
-    for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++) {
-        const int row = base + i * SORT_THREADS + tid;
-        const int a = adapter_of(p, row);
-        key[i] = row >= p.M ? -1 : a < 0 ? SORT_THREADS - 1 : a % (SORT_THREADS - 1);
-    }
+    for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++) id[i] = adapter_of(p, base + i * SORT_THREADS + tid);
+#pragma unroll
+    for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++)
+        key[i] = base + i * SORT_THREADS + tid >= p.M ? -1
+                 : id[i] < 0                          ? SORT_THREADS - 1
+                                                      : id[i] % (SORT_THREADS - 1);
 #pragma unroll
     for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++)
         if (key[i] >= 0) take(count, key[i], lane);
@@ -110,7 +121,8 @@ __global__ void __launch_bounds__(SORT_THREADS) k_lora_sort(LoraArgs p) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < SORT_ROWS / SORT_THREADS; i++)
-        if (key[i] >= 0) p.order[base + take(count, key[i], lane)] = base + i * SORT_THREADS + tid;
+        if (key[i] >= 0)
+            p.seat[base + take(count, key[i], lane)] = make_int2(base + i * SORT_THREADS + tid, id[i]);
 }
 
 // Few rows, more than one tile of them: every workgroup sorts them all for
@@ -174,11 +186,18 @@ __device__ __forceinline__ void lora_parts(const LoraArgs &p, unsigned char *sme
     if (row0 >= p.M) return;
     const int k_lo = part * p.low_k_per_part * 64, k_hi = min(p.K, k_lo + p.low_k_per_part * 64);
     float *low = p.low + (int64_t)part * p.M * p.rank;
-    if (!p.order && p.M > BM) sort_few(p, key, list);
+    if (!p.seat && p.M > BM) sort_few(p, key, list);
     const int rows = min(BM, p.M - row0);
-    int row = -1;
-    if (lane < rows) row = p.order ? p.order[row0 + lane] : p.M > BM ? list[row0 + lane] : lane;
-    const int id = row >= 0 ? adapter_of(p, row) : -1;
+    int row = -1, id = -1;
+    if (lane < rows) {
+        if (p.seat) {
+            const int2 seat = p.seat[row0 + lane];
+            row = seat.x, id = seat.y;
+        } else {
+            row = p.M > BM ? list[row0 + lane] : lane;
+            id = adapter_of(p, row);
+        }
+    }
     unsigned long long left = __ballot(id >= 0);
     for (int n = 0; left; n++) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffsll(left) - 1));
@@ -228,12 +247,18 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_lora_split(LoraArgs p) {
     const int row = blockIdx.x * (SPLIT_THREADS / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (row >= p.M || adapter_of(p, row) < 0) return;
     constexpr int PER = TDG_LORA_MAX_RANK / 64;
-    float x[PER] = {};
-    for (int i = 0; i < p.low_parts; i++) {
-        const float *low = p.low + ((int64_t)i * p.M + row) * p.rank;
+    float x[PER];
 #pragma unroll
-        for (int q = 0; q < PER; q++)
-            if (q * 64 + lane < p.rank) x[q] += low[q * 64 + lane];
+    for (int q = 0; q < PER; q++) {
+        float v[MAX_PARTS];
+#pragma unroll
+        for (int i = 0; i < MAX_PARTS; i++)
+            v[i] = i < p.low_parts && q * 64 + lane < p.rank
+                       ? p.low[((int64_t)i * p.M + row) * p.rank + q * 64 + lane]
+                       : 0.0f;
+        x[q] = v[0];
+#pragma unroll
+        for (int i = 1; i < MAX_PARTS; i++) x[q] += v[i];
     }
     float most = 0.0f;
 #pragma unroll
@@ -256,39 +281,64 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_lora_split(LoraArgs p) {
     }
 }
 
-// acc += scale * low . up for the wave's sorted rows from x0 and columns from
-// col0.  The columns of up[a] that the wave needs are staged in its own part
-// of LDS (no barrier), 64 of the rank at a time.  WHOLE: chunks of up
-// may be read whole (as the DMA reads those of B).
-template <int MI, int NI, bool WHOLE>
-__device__ __forceinline__ void add_adapters(const LoraArgs &p, int x0, int col0, unsigned char *lds,
-                                             f32x16 (&acc)[MI][NI]) {
+// What a tile's end needs of each of its rows, kept in LDS from the start.
+template <int BM>
+struct TileRows {
+    int32_t row[BM], id[BM], ex[BM];
+    __device__ __forceinline__ void fill(const LoraArgs &p, int x0) {
+        for (int i = threadIdx.x; i < BM; i += blockDim.x) {
+            const int2 seat = p.seat[min(x0 + i, p.M - 1)];
+            row[i] = seat.x;
+            id[i] = x0 + i < p.M ? seat.y : -1;
+            ex[i] = seat.y >= 0 ? p.ex[seat.x] : 0;
+        }
+    }
+};
+
+// acc += scale * low . up for a BM-row tile, 64 of the rank at a time.  Both
+// parts of low's rows are staged in LDS for the whole tile, as the products'
+// operands are; the columns of up[a] that a wave needs are staged in a part of
+// LDS of its own, one distinct adapter of its 32-row block after the other.
+// The wave's rows begin at r0, its columns at col0.  WHOLE: chunks of up may
+// be read whole (as the DMA reads those of B).
+template <int MI, int NI, bool WHOLE, int BM, int WAVES>
+__device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
+                                             unsigned char *smem, f32x16 (&acc)[MI][NI]) {
+    typedef Image<true, BM> IL;        // the tile's rows by 64 of the rank
     typedef Image<false, NI * 32> IU;  // 64 of the rank by the wave's columns
-    const int lane = threadIdx.x & 63;
-    int staged = -1, staged_c = 0;
+    const int tid = thread_again(), lane = tid & 63;
+    unsigned char *up_at = smem + 2 * IL::BYTES + (tid >> 6) * IU::BYTES;
+    for (int c0 = 0; c0 < p.rank; c0 += 64) {
+        if (c0) __syncthreads();  // every wave is done with the block before
+        constexpr int PER = 2 * IL::CHUNKS / (WAVES * 64);
+        u32x4 v[PER];
 #pragma unroll
-    for (int mi = 0; mi < MI; mi++) {
-        const int x = x0 + mi * 32 + (lane & 31);
-        const int row = p.order[min(x, p.M - 1)];
-        const int id = x < p.M ? adapter_of(p, row) : -1;
-        const int ex = id >= 0 ? p.ex[row] : 0;
-        // rows without an adapter read what is there: their sums are not used
-        const _Float16 *cut = p.cut + (int64_t)row * 2 * p.rank16 + (lane >> 5) * 8;
-        uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
-        while (left) {
-            const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
-            const uint32_t mine = (uint32_t)__ballot(id == a);
-            left &= ~mine;
-            f32x16 sum[NI];
+        for (int i = 0; i < PER; i++) {
+            const int q = i * WAVES * 64 + tid, part = q / IL::CHUNKS, r = q / IL::CPR % BM;
+            const int c = c0 + ((q % IL::CPR) ^ IL::swz(r)) * 8;
+            // rows without an adapter read what is there: their sums are not used
+            const _Float16 *src = p.cut + ((int64_t)rows.row[r] * 2 + part) * p.rank16 + c;
+            v[i] = load16_global(c < p.rank16 ? (const unsigned char *)src : (const unsigned char *)tdg_zero16);
+        }
 #pragma unroll
-            for (int ni = 0; ni < NI; ni++) sum[ni] = f32x16{};
-            for (int c0 = 0; c0 < p.rank; c0 += 64) {
-                if (staged != a || staged_c != c0) {
+        for (int i = 0; i < PER; i++) lds_write16(smem + (i * WAVES * 64 + tid) * 16, v[i]);
+        __syncthreads();
+        int staged = -1;
+#pragma unroll
+        for (int mi = 0; mi < MI; mi++) {
+            const int at = r0 + mi * 32;
+            const int id = rows.id[at + (lane & 31)];
+            uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
+            while (left) {
+                const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
+                const uint32_t mine = (uint32_t)__ballot(id == a);
+                left &= ~mine;
+                if (staged != a) {
                     const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col0 * 2;
                     // rows of the rank that are there, in steps of the MFMA's 16
                     const int need = min(64, p.rank16 - c0) * IU::CPR;
                     for (int q0 = 0; q0 < need; q0 += 256) {
-                        u32x4 v[4];
+                        u32x4 u[4];
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
                             const int q = q0 + i * 64 + lane, r = q / IU::CPR;
@@ -296,39 +346,41 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, int x0, int col0
                             const unsigned char *src = up + (int64_t)(c0 + r) * p.ld_up;
                             if (WHOLE) {
                                 const bool ok = c0 + r < p.rank && col0 + c < p.N;
-                                v[i] = load16_global(ok ? src + c * 2 : (const unsigned char *)tdg_zero16);
+                                u[i] = load16_global(ok ? src + c * 2 : (const unsigned char *)tdg_zero16);
                             } else {
-                                v[i] = load_chunk(src, c0 + r < p.rank, c, p.N - col0);
+                                u[i] = load_chunk(src, c0 + r < p.rank, c, p.N - col0);
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; i++) lds_write16(lds + (q0 + i * 64 + lane) * 16, v[i]);
+                        for (int i = 0; i < 4; i++) lds_write16(up_at + (q0 + i * 64 + lane) * 16, u[i]);
                     }
-                    staged = a, staged_c = c0;
+                    staged = a;
                     __builtin_amdgcn_wave_barrier();
                 }
+                f32x16 sum[NI];
+#pragma unroll
+                for (int ni = 0; ni < NI; ni++) sum[ni] = f32x16{};
 #pragma unroll
                 for (int s = 0; s < 4; s++) {
                     if (c0 + s * 16 >= p.rank) break;
-                    const u32x4 hi = *(const u32x4 *)(cut + c0 + s * 16);
-                    const u32x4 rest = *(const u32x4 *)(cut + p.rank16 + c0 + s * 16);
+                    const u32x4 hi = IL::read(smem, lane, at, s), rest = IL::read(smem + IL::BYTES, lane, at, s);
 #pragma unroll
                     for (int ni = 0; ni < NI; ni++) {
-                        const u32x4 u = IU::read(lds, lane, ni * 32, s);
+                        const u32x4 u = IU::read(up_at, lane, ni * 32, s);
                         sum[ni] = Mfma<DT_F16>::mac_sub(hi, u, sum[ni], 0);
                         sum[ni] = Mfma<DT_F16>::mac_sub(rest, u, sum[ni], 0);
                     }
                 }
                 __builtin_amdgcn_wave_barrier();
-            }
-            const float scale = p.scale ? p.scale[a] : 1.0f;
+                const float scale = p.scale ? p.scale[a] : 1.0f;
 #pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int r = (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-                const int e = __shfl(ex, r);
-                if ((mine >> r) & 1) {
+                for (int w = 0; w < 16; w++) {
+                    const int r = (w >> 2) * 8 + (lane >> 5) * 4 + (w & 3);
+                    const int e = rows.ex[at + r];
+                    if ((mine >> r) & 1) {
 #pragma unroll
-                    for (int ni = 0; ni < NI; ni++) acc[mi][ni][v] += scale * ldexpf(sum[ni][v], e);
+                        for (int ni = 0; ni < NI; ni++) acc[mi][ni][w] += scale * ldexpf(sum[ni][w], e);
+                    }
                 }
             }
         }
@@ -336,37 +388,40 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, int x0, int col0
 }
 
 // The shared product's tiles for many rows, with the adapters added to the
-// accumulators.  Tile row x is row order[x] of A and C.
+// accumulators.  Tile row x is row seat[x] of A and C.
 template <class E, int BM, int BN, int WM, int WN, bool WHOLE>
 __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem) {
-    static_assert(E::SMEM >= WM * WN * Image<false, E::NI * 32>::BYTES, "LDS for up");
-    const int total = p.row_tiles * p.col_tiles, per = (total + 7) >> 3;
-    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+    static_assert(E::SMEM >= 2 * Image<true, BM>::BYTES + WM * WN * Image<false, E::NI * 32>::BYTES,
+                  "LDS for low and up");
+    __shared__ TileRows<BM> rows;
+    const int id = xcd_tile(blockIdx.x, p.row_tiles * p.col_tiles);
+    if (id < 0) return;
     int tm, tn;
     order_tile(id, p.row_tiles, p.col_tiles, tm, tn);
     poison_lds<E::SMEM, E::NT>(p.flags, smem);
+    rows.fill(p, tm * BM);  // read behind the barriers of run()
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
-    E::run(p.A, p.lda, RowsBy{p.order, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, 0, p.K, smem, acc);
+    E::run(p.A, p.lda, RowsSeated{p.seat, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, 0, p.K, smem, acc);
     __syncthreads();  // every wave is done with the tiles in LDS
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int x0 = tm * BM + (wave % WM) * E::WTM, col0 = tn * BN + (wave / WM) * E::WTN;
-    if (x0 >= p.M || col0 >= p.N) return;
-    add_adapters<E::MI, E::NI, WHOLE>(p, x0, col0, smem + wave * Image<false, E::NI * 32>::BYTES, acc);
+    const int r0 = (wave % WM) * E::WTM, x0 = tm * BM + r0, col0 = tn * BN + (wave / WM) * E::WTN;
+    add_adapters<E::MI, E::NI, WHOLE, BM, WM * WN>(p, rows, r0, col0, smem, acc);
+    // whole 128-byte lines past the caches, as in store_tile
+    const bool inside = x0 + E::WTM <= p.M && col0 + E::WTN <= p.N;
+    const bool stream = inside && (((uintptr_t)p.C | (uint64_t)p.ldc) & 127) == 0;
 #pragma unroll
-    for (int mi = 0; mi < E::MI; mi++) {
-        const int at = p.order[min(x0 + mi * 32 + (lane & 31), p.M - 1)];
+    for (int mi = 0; mi < E::MI; mi++)
 #pragma unroll
         for (int v = 0; v < 16; v++) {
-            const int r = (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-            float *dst = (float *)((unsigned char *)p.C + (int64_t)__shfl(at, r) * p.ldc) + col0 + (lane & 31);
-            if (x0 + mi * 32 + r >= p.M) continue;
+            const int r = mi * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+            float *dst = (float *)((unsigned char *)p.C + (int64_t)rows.row[r0 + r] * p.ldc) + col0 + (lane & 31);
 #pragma unroll
-            for (int ni = 0; ni < E::NI; ni++)
-                if (col0 + ni * 32 + (lane & 31) < p.N) dst[ni * 32] = acc[mi][ni][v];
+            for (int ni = 0; ni < E::NI; ni++) {
+                if (stream) __builtin_nontemporal_store(acc[mi][ni][v], dst + ni * 32);
+                else if (inside || (x0 + r < p.M && col0 + ni * 32 + (lane & 31) < p.N)) dst[ni * 32] = acc[mi][ni][v];
+            }
         }
-    }
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
@@ -386,7 +441,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_any(LoraArgs p) {
 // order, plus scale * sum_c low[t][c] * up[c][n].  A thread owns V columns of
 // ROWS rows; neighbouring rows with the same adapter share up's loads.  Bound
 // by latency: up's loads go out eight at a time, and the parts' before them.
-constexpr int JOIN_THREADS = 256, MAX_PARTS = 8;
+constexpr int JOIN_THREADS = 256;
 
 template <int V, int ROWS>
 __global__ void __launch_bounds__(JOIN_THREADS) k_lora_join(LoraArgs p) {
@@ -478,7 +533,7 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank) {
 struct Plan {
     bool few;             // few rows: parts of the shared product and a join
     int64_t parts, k_per_part, low_parts, low_k_per_part;
-    uint64_t low_at, cut_at, ex_at, order_at, bytes;  // workspace: parts, low, its FP16 rows, their powers, the order
+    uint64_t low_at, cut_at, ex_at, seat_at, bytes;  // workspace: parts, low, its FP16 rows, their powers, the seats
 };
 
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t rank) {
@@ -495,13 +550,16 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t rank) {
         *parts = *per > 0 ? ceil_quot(kt, *per) : 1;
     };
     if (p.few) cut(row_tiles * ceil_quot(N, 64), 512, &p.parts, &p.k_per_part);
-    cut(row_tiles * ceil_quot(rank, 64), 256, &p.low_parts, &p.low_k_per_part);
+    // low has few tiles, and a workgroup of it starts slowly: slices of K as
+    // for 512 workgroups, but longer ones where a few tiles hold many adapters.
+    cut(row_tiles * ceil_quot(rank, 64), p.few && row_tiles > 1 ? 4 * row_tiles : 512, &p.low_parts,
+        &p.low_k_per_part);
     auto up16 = [](uint64_t n) { return (n + 15) / 16 * 16; };
     p.low_at = p.few ? up16((uint64_t)p.parts * M * N * 4) : 0;
     p.cut_at = p.low_at + up16((uint64_t)p.low_parts * M * rank * 4);
     p.ex_at = p.cut_at + (p.few ? 0 : (uint64_t)M * 2 * up16(rank) * 2);
-    p.order_at = p.ex_at + (p.few ? 0 : up16((uint64_t)M * 4));
-    p.bytes = p.order_at + (p.few ? 0 : up16((uint64_t)M * 4));
+    p.seat_at = p.ex_at + (p.few ? 0 : up16((uint64_t)M * 4));
+    p.bytes = p.seat_at + (p.few ? 0 : up16((uint64_t)M * 8));
     return p;
 }
 
@@ -555,7 +613,7 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     p.part = (float *)workspace, p.low = (float *)((unsigned char *)workspace + plan.low_at);
     p.cut = (_Float16 *)((unsigned char *)workspace + plan.cut_at);
     p.ex = (int32_t *)((unsigned char *)workspace + plan.ex_at);
-    p.order = plan.few ? nullptr : (int32_t *)((unsigned char *)workspace + plan.order_at);
+    p.seat = plan.few ? nullptr : (int2 *)((unsigned char *)workspace + plan.seat_at);
     p.rank16 = (int)((rank + 15) / 16 * 16);
     p.lda = lda * 2, p.ldb = ldb * 2, p.ldc = ldc * 4;
     p.ld_down = ld_down * 2, p.stride_down = stride_down * 2, p.ld_up = ld_up * 2, p.stride_up = stride_up * 2;
@@ -572,10 +630,11 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
 
     const int64_t low_tiles = ceil_quot(M, PART_TILE);
     p.low_cols = (int)ceil_quot(rank, 64);
-    // Workgroups that share a row tile's distinct adapters: as many as fill the
-    // chip a few times over (one without work costs about 3 us of a slot).
-    const int64_t lanes = 1024 / (low_tiles * plan.low_parts * p.low_cols);
-    p.low_lanes = (int)(lanes < 1 ? 1 : lanes > PART_TILE ? PART_TILE : lanes);
+    // Workgroups that share a row tile's distinct adapters, of which it has at
+    // most as many as rows (one without work costs about 3 us of a slot).
+    const int64_t tall = M < PART_TILE ? M : PART_TILE;
+    const int64_t lanes = (plan.few ? 512 : 1024) / (low_tiles * plan.low_parts * p.low_cols);
+    p.low_lanes = (int)(lanes < 1 ? 1 : lanes > tall ? tall : lanes);
     p.row_tiles = (int)low_tiles, p.col_tiles = (int)ceil_quot(N, 64);
     const int64_t shared = plan.few ? ceil_quot(low_tiles * p.col_tiles * plan.parts, 8) * 8 : 0;
     const int64_t low_wgs = ceil_quot(low_tiles * plan.low_parts * p.low_cols * p.low_lanes, 8) * 8;
