@@ -603,65 +603,96 @@ TDG_ELEM_F32 = 1
 TDG_LORA_MAX_RANK = 256
 
 
-def _elem(t, what):
+_FLOATS = _HALF = _SINGLE = _INT = None  # dtype tuples, once torch is loaded
+
+
+def _types():
+    """Loads torch's names that the calls below use, once."""
+    global _FLOATS, _HALF, _SINGLE, _INT, _empty, _device_now
     torch = _torch()
-    e = {torch.float16: TDG_ELEM_F16, torch.float32: TDG_ELEM_F32}.get(t.dtype)
-    if e is None:
-        raise TypeError("%s has dtype %s; expected float16 or float32" % (what, t.dtype))
-    return e
+    _FLOATS, _HALF = (torch.float16, torch.float32), (torch.float16, torch.int16)
+    _SINGLE, _INT = (torch.float32,), (torch.int32,)
+    _empty = torch.empty_strided  # a microsecond less than torch.empty with a device
+    _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _whole_numbers(t, what, device, shape=None):
+def _mat(t, types, what, dev=None):
+    """Checks a device matrix with contiguous rows, on device `dev` where one
+    is given: (rows, cols, address, ld, device index)."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D, got shape %s" % (what, tuple(shape)))
+    if t.dtype not in types:
+        raise TypeError("%s has dtype %s; expected one of %s" % (what, t.dtype, types))
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("%s must be a device tensor" % what)
+    if dev is not None and at != dev:
+        raise ValueError("%s is on device %d, expected %d" % (what, at, dev))
+    rows, cols = shape
+    if rows == 0 or cols == 0:
+        return rows, cols, t.data_ptr(), cols or 1, at
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s: elements within a row must be contiguous" % what)
+    return rows, cols, t.data_ptr(), ld if rows > 1 else cols, at
+
+
+def _stack(t, types, what, dev):
+    """A stack of such matrices: (count, rows, cols, address, ld, stride)."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError("%s must be 3-D, got shape %s" % (what, tuple(shape)))
+    if t.dtype not in types:
+        raise TypeError("%s has dtype %s; expected one of %s" % (what, t.dtype, types))
+    if t.get_device() != dev:
+        raise ValueError("%s must be a device tensor on device %d" % (what, dev))
+    count, rows, cols = shape
+    if count == 0 or rows == 0 or cols == 0:
+        return count, rows, cols, t.data_ptr(), cols or 1, rows * (cols or 1)
+    stride, ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s: elements within a row must be contiguous" % what)
+    if rows == 1:
+        ld = cols
+    return count, rows, cols, t.data_ptr(), ld, stride if count > 1 else rows * ld
+
+
+def _whole_numbers(t, what, dev, shape):
     """Checks a dense device int32 tensor; returns its address."""
-    torch = _torch()
-    if t.dtype != torch.int32:
+    if t.dtype not in _INT:
         raise TypeError("%s has dtype %s; expected torch.int32" % (what, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (what, t.device, device))
+    if t.get_device() != dev:
+        raise ValueError("%s must be a device tensor on device %d" % (what, dev))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
     return t.data_ptr()
 
 
-def _same_device(device, **tensors):
-    for what, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, expected %s" % (what, t.device, device))
-
-
-def _stack(t, dtypes, what):
-    """A stack of row-major matrices: (count, rows, cols, address, ld, stride)."""
-    if len(t.shape) != 3:
-        raise ValueError("%s must be 3-D, got shape %s" % (what, tuple(t.shape)))
-    if t.dtype not in dtypes:
-        raise TypeError("%s has dtype %s; expected one of %s" % (what, t.dtype, dtypes))
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % what)
-    count, rows, cols = t.shape
-    st = t.stride()
-    if cols > 1 and st[2] != 1 and t.numel():
-        raise ValueError("%s: elements within a row must be contiguous" % what)
-    if t.numel() == 0:
-        return count, rows, cols, t.data_ptr(), max(cols, 1), rows * max(cols, 1)
-    ld = st[1] if rows > 1 else cols
-    return count, rows, cols, t.data_ptr(), ld, st[0] if count > 1 else rows * ld
-
-
-def _launch(name, device, *args):
-    """Calls entry point `name` with torch's current stream of `device`."""
-    torch = _torch()
-    cur = torch.cuda.current_device()
-    dev = device.index
-    fn = _fn(name)
-    if dev is None or dev == cur:
-        rc = fn(*args, _stream_handle(cur))
+def _launch(name, dev, *args):
+    """Calls entry point `name` with torch's current stream of device `dev`."""
+    if _device_now() == dev:
+        rc = _fn(name)(*args, _stream_handle(dev))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream_handle(dev))
+        with _torch().cuda.device(dev):
+            rc = _fn(name)(*args, _stream_handle(dev))
     if rc != TDG_OK:
         raise TdgError(rc, name)
+
+
+def _workspace(ws, need, t):
+    """(tensor, address, bytes) of a workspace on t's device, allocated when
+    not given."""
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = _empty((need,), (1,), dtype=_torch().uint8, device=t.device)
+        return ws, ws.data_ptr(), need
+    if ws.get_device() != t.get_device() or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % t.device)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def tdg_route_workspace(tokens: int, top_k: int, experts: int) -> int:
@@ -673,55 +704,48 @@ def tdg_route_workspace(tokens: int, top_k: int, experts: int) -> int:
     return need.value
 
 
-def _workspace(ws, need, device):
-    """(tensor, address, bytes) of a workspace, allocated when not given."""
-    torch = _torch()
-    if ws is None:
-        if need == 0:
-            return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not ws.is_cuda or ws.device != device or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def tdg_route_plan(ids, experts: int, offsets=None, order=None, slots=None, workspace=None):
     """Sorts the choices ids (tokens x top_k, int32; an id outside
     [0, experts) is dropped) by expert, stably.  Returns (offsets, order,
     slots): expert g's sorted rows are offsets[g] .. offsets[g + 1] - 1,
     order[i] is the entry token * top_k + j of sorted row i (-1 behind the
     last), slots[t, j] the sorted row of an entry (-1 when dropped)."""
-    torch = _torch()
-    tokens, top_k, p_ids, ld = _matrix(ids, (torch.int32,), "ids")
-    dev = ids.device
-    experts = int(experts)
+    if _INT is None:
+        _types()
+    tokens, top_k, p_ids, ld, dev = _mat(ids, _INT, "ids")
+    experts, n = int(experts), tokens * top_k
+    need = tdg_route_workspace(tokens, top_k, experts)  # refuses bad sizes
     if offsets is None:
-        offsets = torch.empty(experts + 1 if experts >= 0 else 0, dtype=torch.int32, device=dev)
+        offsets = _empty((experts + 1,), (1,), dtype=ids.dtype, device=ids.device)
+        p_off = offsets.data_ptr()
+    else:
+        p_off = _whole_numbers(offsets, "offsets", dev, (experts + 1,))
     if order is None:
-        order = torch.empty(tokens * top_k, dtype=torch.int32, device=dev)
+        order = _empty((n,), (1,), dtype=ids.dtype, device=ids.device)
+        p_ord = order.data_ptr()
+    else:
+        p_ord = _whole_numbers(order, "order", dev, (n,))
     if slots is None:
-        slots = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-    args = (_whole_numbers(offsets, "offsets", dev, (experts + 1,)),
-            _whole_numbers(order, "order", dev, (tokens * top_k,)),
-            _whole_numbers(slots, "slots", dev, (tokens, top_k)))
-    _, p_ws, ws_bytes = _workspace(workspace, tdg_route_workspace(tokens, top_k, experts), dev)
-    _launch("tdg_route_plan", dev, tokens, top_k, experts, p_ids, ld, *args, p_ws, ws_bytes)
+        slots = _empty((tokens, top_k), (top_k, 1), dtype=ids.dtype, device=ids.device)
+        p_slots = slots.data_ptr()
+    else:
+        p_slots = _whole_numbers(slots, "slots", dev, (tokens, top_k))
+    ws, p_ws, ws_bytes = _workspace(workspace, need, ids)
+    _launch("tdg_route_plan", dev, tokens, top_k, experts, p_ids, ld, p_off, p_ord, p_slots, p_ws, ws_bytes)
     return offsets, order, slots
 
 
-def _slots_of(slots, device):
+def _slots_of(slots, dev):
     if len(slots.shape) != 2:
         raise ValueError("slots must be 2-D, got shape %s" % (tuple(slots.shape),))
-    return slots.shape[0], slots.shape[1], _whole_numbers(slots, "slots", device)
+    tokens, top_k = slots.shape
+    return tokens, top_k, _whole_numbers(slots, "slots", dev, slots.shape)
 
 
-def _weights_of(w, slots, what):
-    """(address, ld) of tokens x top_k FP32 weights; NULL for none."""
-    if w is None:
-        return None, max(slots.shape[1], 1)
-    torch = _torch()
-    tokens, top_k, p, ld = _matrix(w, (torch.float32,), what)
-    if (tokens, top_k) != tuple(slots.shape):
+def _weights_of(w, slots, what, dev):
+    """(address, ld) of tokens x top_k FP32 weights."""
+    tokens, top_k, p, ld, _ = _mat(w, _SINGLE, what, dev)
+    if w.shape != slots.shape:
         raise ValueError("%s has shape %s, expected %s" % (what, (tokens, top_k), tuple(slots.shape)))
     return p, ld
 
@@ -730,19 +754,18 @@ def tdg_rows_dispatch(x, slots, out=None):
     """out[slots[t, j]] = x[t] (float16 or float32).  `out` (rows x cols) has
     tokens * top_k rows when allocated here; rows that no slot names are left
     as they are."""
-    torch = _torch()
-    types = (torch.float16, torch.float32)
-    T, cols, px, ldx = _matrix(x, types, "x")
-    tokens, top_k, p_slots = _slots_of(slots, x.device)
+    if _INT is None:
+        _types()
+    T, cols, px, ldx, dev = _mat(x, _FLOATS, "x")
+    tokens, top_k, p_slots = _slots_of(slots, dev)
     if tokens != T:
         raise ValueError("x has %d rows, slots %d" % (T, tokens))
     if out is None:
-        out = torch.empty((tokens * top_k, cols), dtype=x.dtype, device=x.device)
-    rows, oc, po, ldo = _matrix(out, (x.dtype,), "out")
+        out = _empty((tokens * top_k, cols), (cols, 1), dtype=x.dtype, device=x.device)
+    rows, oc, po, ldo, _ = _mat(out, (x.dtype,), "out", dev)
     if oc != cols:
         raise ValueError("out has %d columns, x %d" % (oc, cols))
-    _same_device(x.device, out=out)
-    _launch("tdg_rows_dispatch", x.device, _elem(x, "x"), tokens, top_k, cols, px, ldx, p_slots, rows, po, ldo)
+    _launch("tdg_rows_dispatch", dev, _FLOATS.index(x.dtype), tokens, top_k, cols, px, ldx, p_slots, rows, po, ldo)
     return out
 
 
@@ -750,21 +773,20 @@ def tdg_rows_combine(z, slots, weights=None, out=None, out_dtype=None):
     """y[t] = sum over j of weights[t, j] * z[slots[t, j]], in FP32, rounded
     once to `out`'s type (out_dtype, else z's, when allocated here).  Without
     weights it is the gradient of tdg_rows_dispatch."""
-    torch = _torch()
-    types = (torch.float16, torch.float32)
-    rows, cols, pz, ldz = _matrix(z, types, "z")
-    tokens, top_k, p_slots = _slots_of(slots, z.device)
+    if _INT is None:
+        _types()
+    rows, cols, pz, ldz, dev = _mat(z, _FLOATS, "z")
+    tokens, top_k, p_slots = _slots_of(slots, dev)
     if out is None:
-        out = torch.empty((tokens, cols), dtype=out_dtype or z.dtype, device=z.device)
+        out = _empty((tokens, cols), (cols, 1), dtype=out_dtype or z.dtype, device=z.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out has dtype %s, out_dtype is %s" % (out.dtype, out_dtype))
-    orow, oc, po, ldo = _matrix(out, types, "out")
-    if (orow, oc) != (tokens, cols):
+    orow, oc, po, ldo, _ = _mat(out, _FLOATS, "out", dev)
+    if orow != tokens or oc != cols:
         raise ValueError("out has shape %s, expected %s" % ((orow, oc), (tokens, cols)))
-    pw, ldw = _weights_of(weights, slots, "weights")
-    _same_device(z.device, out=out, weights=weights)
-    _launch("tdg_rows_combine", z.device, _elem(z, "z"), _elem(out, "out"), tokens, top_k, cols, pz, ldz, rows,
-            p_slots, pw, ldw, po, ldo)
+    pw, ldw = (None, top_k) if weights is None else _weights_of(weights, slots, "weights", dev)
+    _launch("tdg_rows_combine", dev, _FLOATS.index(z.dtype), _FLOATS.index(out.dtype), tokens, top_k, cols, pz, ldz,
+            rows, p_slots, pw, ldw, po, ldo)
     return out
 
 
@@ -773,53 +795,52 @@ def tdg_rows_combine_grad(dy, z, slots, weights=None, dz=None, dweights=None):
     dz[slots[t, j]] = weights[t, j] * dy[t] (z's type) and dweights[t, j] =
     <dy[t], z[slots[t, j]]> (float32).  Rows of dz that no slot names are left
     as they are."""
-    torch = _torch()
-    types = (torch.float16, torch.float32)
-    T, cols, pdy, ldy = _matrix(dy, types, "dy")
-    rows, zc, pz, ldz = _matrix(z, types, "z")
-    tokens, top_k, p_slots = _slots_of(slots, z.device)
-    if tokens != T or zc != cols:
-        raise ValueError("dy is %dx%d, z has %d columns and slots %d rows" % (T, cols, zc, tokens))
+    if _INT is None:
+        _types()
+    rows, cols, pz, ldz, dev = _mat(z, _FLOATS, "z")
+    T, dc, pdy, ldy, _ = _mat(dy, _FLOATS, "dy", dev)
+    tokens, top_k, p_slots = _slots_of(slots, dev)
+    if tokens != T or dc != cols:
+        raise ValueError("dy is %dx%d, z has %d columns and slots %d rows" % (T, dc, cols, tokens))
     if dz is None:
-        dz = torch.empty((rows, cols), dtype=z.dtype, device=z.device)
-    zr, zcols, pdz, lddz = _matrix(dz, (z.dtype,), "dz")
-    if (zr, zcols) != (rows, cols):
-        raise ValueError("dz has shape %s, expected %s" % ((zr, zcols), (rows, cols)))
+        dz = _empty((rows, cols), (cols, 1), dtype=z.dtype, device=z.device)
+    zr, zc, pdz, lddz, _ = _mat(dz, (z.dtype,), "dz", dev)
+    if zr != rows or zc != cols:
+        raise ValueError("dz has shape %s, expected %s" % ((zr, zc), (rows, cols)))
     if dweights is None:
-        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=z.device)
-    pw, ldw = _weights_of(weights, slots, "weights")
-    pdw, lddw = _weights_of(dweights, slots, "dweights")
-    _same_device(z.device, dy=dy, dz=dz, weights=weights, dweights=dweights)
-    _launch("tdg_rows_combine_grad", z.device, _elem(z, "z"), _elem(dy, "dy"), tokens, top_k, cols, pdy, ldy, pz,
-            ldz, rows, p_slots, pw, ldw, pdz, lddz, pdw, lddw)
+        dweights = _empty((tokens, top_k), (top_k, 1), dtype=_SINGLE[0], device=z.device)
+    pw, ldw = (None, top_k) if weights is None else _weights_of(weights, slots, "weights", dev)
+    pdw, lddw = _weights_of(dweights, slots, "dweights", dev)
+    _launch("tdg_rows_combine_grad", dev, _FLOATS.index(z.dtype), _FLOATS.index(dy.dtype), tokens, top_k, cols, pdy,
+            ldy, pz, ldz, rows, p_slots, pw, ldw, pdz, lddz, pdw, lddw)
     return dz, dweights
 
 
-def _offsets_of(offsets, device):
+def _offsets_of(offsets, dev):
     """(groups, address) of groups + 1 row offsets."""
-    if len(offsets.shape) != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must hold groups + 1 values, got shape %s" % (tuple(offsets.shape),))
-    return offsets.shape[0] - 1, _whole_numbers(offsets, "offsets", device)
+    shape = offsets.shape
+    if len(shape) != 1 or shape[0] < 1:
+        raise ValueError("offsets must hold groups + 1 values, got shape %s" % (tuple(shape),))
+    return shape[0] - 1, _whole_numbers(offsets, "offsets", dev, shape)
 
 
 def _grouped(name, A, B, offsets, C, transposed):
-    torch = _torch()
-    f16 = (torch.float16, torch.int16)
-    M, K, pa, lda = _matrix(A, f16, "A")
-    groups, rb, cb, pb, ldb, stride = _stack(B, f16, "B")
+    if _INT is None:
+        _types()
+    M, K, pa, lda, dev = _mat(A, _HALF, "A")
+    groups, rb, cb, pb, ldb, stride = _stack(B, _HALF, "B", dev)
     N, K2 = (rb, cb) if transposed else (cb, rb)
-    n_off, p_off = _offsets_of(offsets, A.device)
+    n_off, p_off = _offsets_of(offsets, dev)
     if n_off != groups:
         raise ValueError("offsets name %d groups, B has %d" % (n_off, groups))
     if K != K2:
         raise ValueError("inner dimensions differ: A has %d columns, B's matrices are %dx%d" % (K, rb, cb))
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float32, device=A.device)
-    Mc, Nc, pc, ldc = _matrix(C, (torch.float32,), "C")
-    if (Mc, Nc) != (M, N):
+        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
+    Mc, Nc, pc, ldc, _ = _mat(C, _SINGLE, "C", dev)
+    if Mc != M or Nc != N:
         raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
-    _same_device(A.device, B=B, C=C)
-    _launch(name, A.device, groups, p_off, M, N, K, pa, lda, pb, ldb, stride, pc, ldc)
+    _launch(name, dev, groups, p_off, M, N, K, pa, lda, pb, ldb, stride, pc, ldc)
     return C
 
 
@@ -840,20 +861,19 @@ def gemm_f16f32_grouped_tn(A, B, offsets, C=None):
     """C[g] = A[rows of g]^T . B[rows of g] (groups x M x N): with
     gemm_f16f32_grouped's A and the gradient of its result, the gradient of
     its B.  Zeros for a group without rows."""
-    torch = _torch()
-    f16 = (torch.float16, torch.int16)
-    rows, M, pa, lda = _matrix(A, f16, "A")
-    rows_b, N, pb, ldb = _matrix(B, f16, "B")
+    if _INT is None:
+        _types()
+    rows, M, pa, lda, dev = _mat(A, _HALF, "A")
+    rows_b, N, pb, ldb, _ = _mat(B, _HALF, "B", dev)
     if rows != rows_b:
         raise ValueError("A has %d rows, B %d" % (rows, rows_b))
-    groups, p_off = _offsets_of(offsets, A.device)
+    groups, p_off = _offsets_of(offsets, dev)
     if C is None:
-        C = torch.empty((groups, M, N), dtype=torch.float32, device=A.device)
-    gc, mc, nc, pc, ldc, stride = _stack(C, (torch.float32,), "C")
+        C = _empty((groups, M, N), (M * N, N, 1), dtype=_SINGLE[0], device=A.device)
+    gc, mc, nc, pc, ldc, stride = _stack(C, _SINGLE, "C", dev)
     if (gc, mc, nc) != (groups, M, N):
         raise ValueError("C has shape %s, expected %s" % ((gc, mc, nc), (groups, M, N)))
-    _same_device(A.device, B=B, C=C)
-    _launch("gemm_f16f32_grouped_tn", A.device, groups, p_off, rows, M, N, pa, lda, pb, ldb, pc, ldc, stride)
+    _launch("gemm_f16f32_grouped_tn", dev, groups, p_off, rows, M, N, pa, lda, pb, ldb, pc, ldc, stride)
     return C
 
 
@@ -872,31 +892,31 @@ def gemm_f16f32_lora(A, B, down, up, adapter, scale=None, C=None, workspace=None
     alone).  A: M x K, B: K x N, down: adapters x K x rank, up: adapters x
     rank x N (float16); scale: float32 or None (1).  The workspace is
     allocated here when not given."""
-    torch = _torch()
-    f16 = (torch.float16, torch.int16)
-    M, K, pa, lda = _matrix(A, f16, "A")
-    K2, N, pb, ldb = _matrix(B, f16, "B")
-    n, kd, rank, pd, ldd, sd = _stack(down, f16, "down")
-    nu, ru, cu, pu, ldu, su = _stack(up, f16, "up")
+    if _INT is None:
+        _types()
+    M, K, pa, lda, dev = _mat(A, _HALF, "A")
+    K2, N, pb, ldb, _ = _mat(B, _HALF, "B", dev)
+    n, kd, rank, pd, ldd, sd = _stack(down, _HALF, "down", dev)
+    nu, ru, cu, pu, ldu, su = _stack(up, _HALF, "up", dev)
     if K != K2:
         raise ValueError("inner dimensions differ: A is %dx%d, B is %dx%d" % (M, K, K2, N))
-    if (kd, nu, ru, cu) != (K, n, rank, N):
+    if kd != K or nu != n or ru != rank or cu != N:
         raise ValueError("down is %s and up %s; expected adapters x %d x rank and adapters x rank x %d"
                          % (tuple(down.shape), tuple(up.shape), K, N))
-    dev = A.device
     p_ad = _whole_numbers(adapter, "adapter", dev, (M,))
     p_sc = None
     if scale is not None:
-        if scale.dtype != torch.float32 or tuple(scale.shape) != (n,) or not scale.is_contiguous():
+        if scale.dtype not in _SINGLE or scale.shape != (n,) or not scale.is_contiguous():
             raise ValueError("scale must be a contiguous float32 tensor of %d values" % n)
+        if scale.get_device() != dev:
+            raise ValueError("scale must be a device tensor on device %d" % dev)
         p_sc = scale.data_ptr()
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float32, device=dev)
-    Mc, Nc, pc, ldc = _matrix(C, (torch.float32,), "C")
-    if (Mc, Nc) != (M, N):
+        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
+    Mc, Nc, pc, ldc, _ = _mat(C, _SINGLE, "C", dev)
+    if Mc != M or Nc != N:
         raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
-    _same_device(dev, B=B, down=down, up=up, scale=scale, C=C)
-    _, p_ws, ws_bytes = _workspace(workspace, tdg_lora_workspace(M, N, K, n, rank), dev)
+    ws, p_ws, ws_bytes = _workspace(workspace, tdg_lora_workspace(M, N, K, n, rank), A)
     _launch("gemm_f16f32_lora", dev, M, N, K, pa, lda, pb, ldb, n, rank, pd, ldd, sd, pu, ldu, su, p_ad, p_sc, pc,
             ldc, p_ws, ws_bytes)
     return C
