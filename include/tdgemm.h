@@ -418,8 +418,8 @@ int64_t tdg_lds_probe_bytes(int mode, int64_t iters);
  * any HIP call, TDG_ERR_NO_DEVICE off gfx950, thread-safe.  Outputs (and a
  * workspace) may not overlap each other or an input; sizes are 0 .. 2^31 -
  * 2^16; leading dimensions and strides are in elements; every array is aligned
- * to its element.  Shapes past one launch's grid (over 16 million rows, or
- * rows past 65535 workgroups) are TDG_ERR_UNSUPPORTED.  Results are the same
+ * to its element.  Shapes past one launch's grid (over 16 million workgroups)
+ * are TDG_ERR_UNSUPPORTED.  Results are the same
  * from run to run.  Ids, slots and offsets are read on the device and never
  * lead a read or write outside the arrays as described here, whatever they
  * hold. */

@@ -40,7 +40,7 @@ REFUSED = [
         dict(ld_ids=1), dict(ids=None), dict(offsets=None), dict(order=None), dict(slots=None), dict(ids=A + 2),
         dict(offsets=B + 1), dict(slots=C + 4), dict(order=A), dict(offsets=D), dict(ld_ids=FAR),
         dict(tokens=4097, top_k=1), dict(tokens=4097, top_k=1, ws=E, ws_bytes=63),
-        dict(tokens=4097, top_k=1, ws=C, ws_bytes=64), dict(tokens=4097, top_k=1, ws=E + 2, ws_bytes=64)]),
+        dict(tokens=4097, top_k=1, ws=C, ws_bytes=4096), dict(tokens=4097, top_k=1, ws=E + 2, ws_bytes=4096)]),
     ("tdg_rows_dispatch", DISPATCH, [
         dict(elem=2), dict(elem=-1), dict(tokens=-1), dict(top_k=0), dict(cols=-1), dict(rows=-1), dict(ldx=63),
         dict(ldo=63), dict(x=None), dict(out=None), dict(slots=None), dict(out=A), dict(out=B), dict(x=A + 1),
@@ -115,7 +115,7 @@ def test_adapter_arguments_are_not_needed_without_adapters():
 def test_workspace_sizes():
     assert tdg.tdg_route_workspace(0, 1, 8) == 0
     assert tdg.tdg_route_workspace(512, 8, 1024) == 0
-    assert tdg.tdg_route_workspace(4097, 1, 8) == 2 * 8 * 4
+    assert 2 * 8 * 4 <= tdg.tdg_route_workspace(4097, 1, 8) <= 1 << 20
     assert tdg.tdg_route_workspace(1 << 27, 8, 1024) <= 1 << 20
     for bad in ((-1, 1, 8), (1, 0, 8), (1, 1, 0), (1, 1, 1025), (1 << 30, 2, 8)):
         with pytest.raises(tdg.TdgError):

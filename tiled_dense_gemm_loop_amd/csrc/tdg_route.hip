@@ -35,8 +35,12 @@ typedef f32x4 f32x4_ua __attribute__((aligned(4)));
 
 constexpr int MAX_EXPERTS = 1024;
 constexpr int PLAN_THREADS = 1024;
-constexpr int PLAN_ENTRIES = 4096;  // entries per workgroup, more when there are over 256 such
-constexpr int PLAN_BLOCKS = 256;
+// Up to PLAN_ALONE entries one workgroup does it all (7.9 us for 4096, as two
+// launches take); above, 1024 or 2048 entries per workgroup, or more where
+// that would be over PLAN_BLOCKS (us for 16000 and 65536 entries of 64
+// experts: 8.5 and 9.5 by 1024, 9.3 and 9.7 by 2048, 10.9 and 11.4 by 4096;
+// for 262144: 13.3, 11.8, 12.5).
+constexpr int PLAN_ALONE = 4096, PLAN_BLOCKS = 256;
 
 struct RouteArgs {
     const int32_t *ids;
@@ -183,7 +187,13 @@ constexpr int ROW_THREADS = 256;
 // Rows of `units` 16-byte (or, for the last, shorter) pieces.  A workgroup is
 // ROW_THREADS / tx token rows of tx threads, and covers tx pieces of each; tx
 // is the power of two that covers a row, at most ROW_THREADS, and long rows
-// are cut over gridDim.y, so that a few tokens still spread over many CUs.
+// are cut into `segs` segments, so that a few tokens still spread over many
+// CUs.  A token's segments are neighbours in the grid: with all tokens' first
+// segments together, rows whose length is a power of two keep a part of the
+// memory channels busy at a time (4096 tokens, 4 rows of 16 KiB each: dispatch
+// 79 us against 72, combine 96 against 72).  Rows off the 16-byte grid are the
+// other way round (rows 4 bytes shorter: combine 84 us with the segments
+// apart, 91 with them together; dispatch of 8191 FP16 columns 89 and 97).
 // Pieces start at any byte address: the chip runs in unaligned-access mode.
 struct RowsArgs {
     const unsigned char *tok;  // token rows read (dispatch: x, gradient: dy)
@@ -197,16 +207,28 @@ struct RowsArgs {
     float *dw;
     int64_t ld_dw;
     int tokens, top_k, cols, rows;
-    int tx_log2;
+    int tx_log2, segs;
+    int apart;  // a token's segments lie apart in the grid
 };
+
+__device__ __forceinline__ void row_block(const RowsArgs &a, int &tb, int &seg) {
+    if (a.apart) {
+        const int n = gridDim.x / a.segs;
+        seg = blockIdx.x / n, tb = blockIdx.x - seg * n;
+    } else {
+        tb = blockIdx.x / a.segs, seg = blockIdx.x - tb * a.segs;
+    }
+}
 
 template <int ES>
 __global__ void __launch_bounds__(ROW_THREADS) k_rows_dispatch(RowsArgs a) {
     const int tx = 1 << a.tx_log2;
-    const int t = blockIdx.x * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
+    int tb, seg;
+    row_block(a, tb, seg);
+    const int t = tb * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
     if (t >= a.tokens) return;
     constexpr int EPC = 16 / ES;
-    const int64_t col = ((int64_t)blockIdx.y * tx + (threadIdx.x & (tx - 1))) * EPC;
+    const int64_t col = ((int64_t)seg * tx + (threadIdx.x & (tx - 1))) * EPC;
     if (col >= a.cols) return;
     const unsigned char *src = a.tok + (int64_t)t * a.ld_tok + col * ES;
     const int32_t *slots = a.slots + (int64_t)t * a.top_k;
@@ -271,9 +293,11 @@ template <typename Z, typename Y>
 __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine(RowsArgs a) {
     constexpr int V = 16 / sizeof(Z);
     const int tx = 1 << a.tx_log2;
-    const int t = blockIdx.x * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
+    int tb, seg;
+    row_block(a, tb, seg);
+    const int t = tb * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
     if (t >= a.tokens) return;
-    const int64_t col = ((int64_t)blockIdx.y * tx + (threadIdx.x & (tx - 1))) * V;
+    const int64_t col = ((int64_t)seg * tx + (threadIdx.x & (tx - 1))) * V;
     if (col >= a.cols) return;
     const int32_t *slots = a.slots + (int64_t)t * a.top_k;
     const float *w = a.w ? a.w + (int64_t)t * a.ld_w : nullptr;
@@ -323,7 +347,12 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine_grad(RowsArgs a) {
         w[j] = slot[j] >= 0 && a.w ? a.w[(int64_t)t * a.ld_w + j0 + j] : 1.0f;
         dot[j] = 0.0f;
     }
-    for (int64_t col = (int64_t)tid * V; col < a.cols; col += ROW_THREADS * V) {
+    // Neighbouring tokens start in different segments of their rows: see above.
+    const int segs = (a.cols + ROW_THREADS * V - 1) / (ROW_THREADS * V);
+    int seg = segs > 0 ? t % segs : 0;
+    for (int i = 0; i < segs; i++, seg = seg + 1 == segs ? 0 : seg + 1) {
+        const int64_t col = ((int64_t)seg * ROW_THREADS + tid) * V;
+        if (col >= a.cols) continue;
         if (col + V <= a.cols) {
             float g[V];
             load_v<Y, V>(dy + col * sizeof(Y), g);
@@ -388,20 +417,26 @@ bool elem_ok(int e) { return e == TDG_ELEM_F16 || e == TDG_ELEM_F32; }
 int64_t elem_bytes(int e) { return e == TDG_ELEM_F16 ? 2 : 4; }
 
 // Threads along a row, as a power of two, and the grid.
-bool rows_grid(int64_t tokens, int64_t cols, int per_thread, int *tx_log2, dim3 *grid) {
+bool rows_grid(int64_t tokens, int64_t cols, int per_thread, RowsArgs *a, dim3 *grid) {
     const int64_t units = tdg::ceil_quot(cols, per_thread);
     int lg = 0;
     while ((1 << lg) < ROW_THREADS && (1 << lg) < units) lg++;
-    *tx_log2 = lg;
-    const int64_t gy = tdg::ceil_quot(units, (int64_t)1 << lg);
-    const int64_t gx = tdg::ceil_quot(tokens, ROW_THREADS >> lg);
-    if (gy > 65535 || !grid_ok(gx, ROW_THREADS)) return false;
-    *grid = dim3((unsigned)gx, (unsigned)gy);
+    const int64_t segs = tdg::ceil_quot(units, (int64_t)1 << lg);
+    const int64_t blocks = tdg::ceil_quot(tokens, ROW_THREADS >> lg) * segs;
+    if (!grid_ok(blocks, ROW_THREADS)) return false;
+    a->tx_log2 = lg, a->segs = (int)segs;
+    a->apart = (((uintptr_t)a->row | (uintptr_t)a->row_out | (uint64_t)a->ld_row | (uint64_t)a->ld_out) & 15) != 0;
+    *grid = dim3((unsigned)blocks);
     return true;
 }
 
 void plan_split(int64_t entries, int *per_block, int *blocks) {
-    int64_t per = entries < PLAN_ENTRIES ? (entries > 0 ? entries : 1) : PLAN_ENTRIES;
+    if (entries <= PLAN_ALONE) {
+        *per_block = entries > 0 ? (int)entries : 1;
+        *blocks = 1;
+        return;
+    }
+    int64_t per = entries <= 16384 ? 1024 : 2048;
     if (tdg::ceil_quot(entries, per) > PLAN_BLOCKS)
         per = tdg::ceil_quot(tdg::ceil_quot(entries, PLAN_BLOCKS), 64) * 64;
     *per_block = (int)per;
@@ -476,7 +511,7 @@ int tdg_rows_dispatch(int elem, int64_t tokens, int64_t top_k, int64_t cols, con
     a.ld_tok = ldx * es, a.ld_out = ldo * es, a.slots = slots;
     a.tokens = (int)tokens, a.top_k = (int)top_k, a.cols = (int)cols, a.rows = (int)rows;
     dim3 grid;
-    if (!rows_grid(tokens, cols, (int)(16 / es), &a.tx_log2, &grid)) return TDG_ERR_UNSUPPORTED;
+    if (!rows_grid(tokens, cols, (int)(16 / es), &a, &grid)) return TDG_ERR_UNSUPPORTED;
     const int rc = tdg::device_check();
     if (rc != TDG_OK) return rc;
     const void *fn = elem == TDG_ELEM_F16 ? (const void *)&k_rows_dispatch<2> : (const void *)&k_rows_dispatch<4>;
@@ -507,7 +542,7 @@ int tdg_rows_combine(int row_elem, int token_elem, int64_t tokens, int64_t top_k
     a.ld_row = ldz * zs, a.ld_tok = ldy * ys, a.slots = slots, a.w = weights, a.ld_w = ld_weights;
     a.tokens = (int)tokens, a.top_k = (int)top_k, a.cols = (int)cols, a.rows = (int)rows;
     dim3 grid;
-    if (!rows_grid(tokens, cols, (int)(16 / zs), &a.tx_log2, &grid)) return TDG_ERR_UNSUPPORTED;
+    if (!rows_grid(tokens, cols, (int)(16 / zs), &a, &grid)) return TDG_ERR_UNSUPPORTED;
     const int rc = tdg::device_check();
     if (rc != TDG_OK) return rc;
     const void *fn;
