@@ -56,10 +56,6 @@ struct Variant {
      : lay == tdg::LAY_NT ? (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__> \
                           : (const void *)&tdg::KERNEL<tdg::LAY_TN, __VA_ARGS__>)
 
-#define TDG_ROWS(KERNEL, ...)                                                   \
-    (lay == tdg::LAY_NN ? (const void *)&tdg::KERNEL<tdg::LAY_NN, __VA_ARGS__> \
-                        : (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__>)
-
 Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
                const void *B, int64_t ldb, int64_t stride_b) {
     const bool tn = lay == tdg::LAY_TN;
@@ -90,7 +86,9 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
     // = 1000: 13 / 9).
     if (tiles(256) >= 256 && (tn || rows >= 192 * live))
         return tn ? Variant{(const void *)&tdg::tdg_grouped_tn_loop<256, 256, 2, 4, 2>, 256, 256, 512, 256}
-                  : Variant{TDG_ROWS(tdg_grouped_ring, 256, 256, 2, 4, 2), 256, 256, 512, INT32_MAX};
+                  : Variant{lay == tdg::LAY_NN ? (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NN>
+                                               : (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NT>,
+                            256, 256, 512, INT32_MAX};
     if (tiles(128) > 256) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256, INT32_MAX};
     if (tiles(128) >= 192) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256, INT32_MAX};
     return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 64, 2, 2, 4), 64, 64, 256, INT32_MAX};
@@ -120,7 +118,8 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     const int64_t row_tiles = lay == tdg::LAY_TN ? groups * a.tiles_m
                                                  : rows / v.bm + (groups < rows ? groups : rows);
     if (row_tiles > INT32_MAX / a.tiles_n) return TDG_ERR_UNSUPPORTED;
-    int64_t grid = tdg::ceil_quot(row_tiles * a.tiles_n, 8) * 8;
+    // (And up to 16 tiles of each XCD can be cut in two.)
+    int64_t grid = tdg::ceil_quot(row_tiles * a.tiles_n, 8) * 8 + 8 * 16;
     if (grid > INT32_MAX - 65536) return TDG_ERR_UNSUPPORTED;
     a.tiles_most = (int)grid;
     if (grid > v.most_wgs) grid = v.most_wgs;

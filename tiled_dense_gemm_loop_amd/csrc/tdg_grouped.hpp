@@ -86,6 +86,7 @@ __device__ static __forceinline__ int thread_again() {
 // first row (TN: column of A) and its column tile.
 struct GroupedTile {
     int g, lo, hi, x0, tn;
+    int half;  // -1: the whole tile; 0, 1: its left or right half (CUT)
     bool ok;
 };
 
@@ -115,14 +116,30 @@ __device__ static __forceinline__ int xcd_tile(int b, int total) {
     return (b >> 3) < per && id < total ? id : -1;
 }
 
+// The same where a CU holds one workgroup: when the last round of an XCD's 32
+// CUs would have work for half of them or fewer, its tiles are cut in two,
+// left and right.  `half`: -1 for a whole tile, else which half.
+__device__ static __forceinline__ int xcd_tile_cut(int b, int total, int &half) {
+    const int per = (total + 7) >> 3, last = per & 31, whole = last <= 16 ? per - last : per;
+    int j = b >> 3;
+    half = -1;
+    if (j >= whole) {
+        half = (j - whole) & 1;
+        j = whole + ((j - whole) >> 1);
+    }
+    const int id = (b & 7) * per + j;
+    return j < per && id < total ? id : -1;
+}
+
 // Workgroup -> tile.  Tiles are numbered group by group.  For NN and NT the tile counts depend on the offsets:
 // every wave sums them itself (64 lanes, a run of groups each), which costs
 // less than a launch that would write them down.  The grid is sized for the
 // most tiles that the rows can make; workgroups past the total end at once.
-template <int LAY, int BM>
+template <int LAY, int BM, bool CUT>
 __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a, int b) {
     GroupedTile t;
     t.ok = false;
+    t.half = -1;
     if constexpr (LAY == LAY_TN) {
         const int per_g = a.tiles_m * a.tiles_n;
         const int id = xcd_tile(b, a.groups * per_g);
@@ -153,7 +170,8 @@ __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a, in
         const int up = __shfl_up(upto, d);
         if (lane >= d) upto += up;
     }
-    const int id = xcd_tile(b, __builtin_amdgcn_readlane(upto, 63) * a.tiles_n);
+    const int total = __builtin_amdgcn_readlane(upto, 63) * a.tiles_n;
+    const int id = CUT ? xcd_tile_cut(b, total, t.half) : xcd_tile(b, total);
     if (id < 0) return t;
     const int at = id / a.tiles_n;  // the how manieth row tile: finds the group
     const int owner = __builtin_amdgcn_readfirstlane(__ffsll(__ballot(upto > at)) - 1);
@@ -598,15 +616,15 @@ __device__ static __forceinline__ void poison_lds(int flags, unsigned char *smem
 
 // Whether C tiles remain for workgroup b, and where: A's and C's rows (TN:
 // A's columns) x0 .. x_end - 1, the columns from y0 on, k_lo .. k_hi - 1.
-template <int LAY, int BM, int BN>
+template <int LAY, int BM, int BN, bool CUT = false>
 struct GroupedWork {
     GroupedTile t;
     __device__ __forceinline__ bool find(const GroupedArgs &a, int b) {
-        t = find_tile<LAY, BM>(a, b);
+        t = find_tile<LAY, BM, CUT>(a, b);
         return t.ok;
     }
     __device__ __forceinline__ int x_end(const GroupedArgs &a) const { return LAY == LAY_TN ? a.M : t.hi; }
-    __device__ __forceinline__ int y0() const { return t.tn * BN; }
+    __device__ __forceinline__ int y0() const { return t.tn * BN + (CUT && t.half > 0 ? BN / 2 : 0); }
     __device__ __forceinline__ const unsigned char *A(const GroupedArgs &a) const {
         return a.A + (LAY == LAY_TN ? 0 : (int64_t)t.x0 * a.lda);
     }
@@ -649,6 +667,32 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_ring(GroupedArgs a
     E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
            smem, acc);
     w.template store<E, WM>(a, acc);
+}
+
+// 256 x 256 tiles, one workgroup per CU: the last round's are cut where that
+// fills the CUs (xcd_tile_cut).
+template <int LAY>
+__global__ void __launch_bounds__(512, 1) tdg_grouped_cut(GroupedArgs a) {
+    typedef GroupedRing<LAY, 256, 256, 2, 4, 2> E;
+    typedef GroupedRing<LAY, 256, 128, 4, 2, 3> H;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[H::SMEM > E::SMEM ? H::SMEM : E::SMEM];
+    GroupedWork<LAY, 256, 256, true> w;
+    if (!w.find(a, blockIdx.x)) return;
+    if (w.y0() >= a.N) return;
+    poison_lds<sizeof(smem), E::NT>(a.flags, smem);
+    if (w.t.half < 0) {
+        f32x16 acc[E::MI][E::NI];
+        clear_acc(acc);
+        E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(),
+               w.k_hi(a), smem, acc);
+        w.template store<E, 2>(a, acc);
+    } else {
+        f32x16 acc[H::MI][H::NI];
+        clear_acc(acc);
+        H::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(),
+               min(a.N, w.y0() + 128), w.k_lo(), w.k_hi(a), smem, acc);
+        w.template store<H, 4>(a, acc);
+    }
 }
 
 // Asks for a word of every 128-byte line of a rows x cols matrix of 2-byte

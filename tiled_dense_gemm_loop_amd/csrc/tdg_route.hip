@@ -211,24 +211,21 @@ struct RowsArgs {
     int apart;  // a token's segments lie apart in the grid
 };
 
-__device__ __forceinline__ void row_block(const RowsArgs &a, int &tb, int &seg) {
-    if (a.apart) {
-        const int n = gridDim.x / a.segs;
-        seg = blockIdx.x / n, tb = blockIdx.x - seg * n;
-    } else {
-        tb = blockIdx.x / a.segs, seg = blockIdx.x - tb * a.segs;
-    }
+// The block of token rows (x) and the segment (y) of this workgroup.
+__device__ __forceinline__ int2 row_block(const RowsArgs &a) {
+    const int per = a.apart ? gridDim.x / a.segs : a.segs;
+    const int q = blockIdx.x / per, r = blockIdx.x - q * per;
+    return a.apart ? make_int2(r, q) : make_int2(q, r);
 }
 
 template <int ES>
 __global__ void __launch_bounds__(ROW_THREADS) k_rows_dispatch(RowsArgs a) {
     const int tx = 1 << a.tx_log2;
-    int tb, seg;
-    row_block(a, tb, seg);
-    const int t = tb * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
+    const int2 at = row_block(a);
+    const int t = at.x * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
     if (t >= a.tokens) return;
     constexpr int EPC = 16 / ES;
-    const int64_t col = ((int64_t)seg * tx + (threadIdx.x & (tx - 1))) * EPC;
+    const int64_t col = ((int64_t)at.y * tx + (threadIdx.x & (tx - 1))) * EPC;
     if (col >= a.cols) return;
     const unsigned char *src = a.tok + (int64_t)t * a.ld_tok + col * ES;
     const int32_t *slots = a.slots + (int64_t)t * a.top_k;
@@ -248,6 +245,9 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows_dispatch(RowsArgs a) {
         }
     }
 }
+
+// What is loaded, and not used, in place of a row that is not there.
+static __device__ __attribute__((aligned(16))) const uint32_t no_row[8] = {};
 
 // V consecutive elements as floats, and back (rounded to nearest even).
 template <typename T, int V>
@@ -293,25 +293,37 @@ template <typename Z, typename Y>
 __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine(RowsArgs a) {
     constexpr int V = 16 / sizeof(Z);
     const int tx = 1 << a.tx_log2;
-    int tb, seg;
-    row_block(a, tb, seg);
-    const int t = tb * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
+    const int2 at = row_block(a);
+    const int t = at.x * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
     if (t >= a.tokens) return;
-    const int64_t col = ((int64_t)seg * tx + (threadIdx.x & (tx - 1))) * V;
+    const int64_t col = ((int64_t)at.y * tx + (threadIdx.x & (tx - 1))) * V;
     if (col >= a.cols) return;
     const int32_t *slots = a.slots + (int64_t)t * a.top_k;
     const float *w = a.w ? a.w + (int64_t)t * a.ld_w : nullptr;
     unsigned char *dst = a.tok_out + (int64_t)t * a.ld_tok + col * sizeof(Y);
+    const unsigned char *none = (const unsigned char *)no_row;
     if (col + V <= a.cols) {
         float acc[V] = {};
-        for (int j = 0; j < a.top_k; j++) {
-            const int s = slots[j];
-            if ((unsigned)s >= (unsigned)a.rows) continue;
-            const float wj = w ? w[j] : 1.0f;
-            float z[V];
-            load_v<Z, V>(a.row + (int64_t)s * a.ld_row + col * sizeof(Z), z);
+        // Four rows' loads go out together: one at a time, the loads in flight
+        // on the chip are too few for HBM's rate.
+        for (int j0 = 0; j0 < a.top_k; j0 += 4) {
+            int s[4];
+            float wj[4], z[4][V];
 #pragma unroll
-            for (int q = 0; q < V; q++) acc[q] = fmaf(wj, z[q], acc[q]);
+            for (int j = 0; j < 4; j++) {
+                s[j] = j0 + j < a.top_k ? slots[j0 + j] : -1;
+                wj[j] = w && j0 + j < a.top_k ? w[j0 + j] : 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                load_v<Z, V>((unsigned)s[j] < (unsigned)a.rows ? a.row + (int64_t)s[j] * a.ld_row + col * sizeof(Z) : none,
+                             z[j]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if ((unsigned)s[j] >= (unsigned)a.rows) continue;
+#pragma unroll
+                for (int q = 0; q < V; q++) acc[q] = fmaf(wj[j], z[j][q], acc[q]);
+            }
         }
         store_v<Y, V>(dst, acc);
     } else {
@@ -356,17 +368,21 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine_grad(RowsArgs a) {
         if (col + V <= a.cols) {
             float g[V];
             load_v<Y, V>(dy + col * sizeof(Y), g);
+            float z[J][V];
+#pragma unroll
+            for (int j = 0; j < J; j++)
+                load_v<Z, V>(slot[j] >= 0 ? a.row + (int64_t)slot[j] * a.ld_row + col * sizeof(Z)
+                                          : (const unsigned char *)no_row,
+                             z[j]);
 #pragma unroll
             for (int j = 0; j < J; j++) {
                 if (slot[j] < 0) continue;
-                float z[V];
-                load_v<Z, V>(a.row + (int64_t)slot[j] * a.ld_row + col * sizeof(Z), z);
 #pragma unroll
                 for (int q = 0; q < V; q++) {
-                    dot[j] = fmaf(g[q], z[q], dot[j]);
-                    z[q] = w[j] * g[q];
+                    dot[j] = fmaf(g[q], z[j][q], dot[j]);
+                    z[j][q] = w[j] * g[q];
                 }
-                store_v<Z, V>(a.row_out + (int64_t)slot[j] * a.ld_out + col * sizeof(Z), z);
+                store_v<Z, V>(a.row_out + (int64_t)slot[j] * a.ld_out + col * sizeof(Z), z[j]);
             }
         } else {
             for (int c = (int)col; c < a.cols; c++) {
