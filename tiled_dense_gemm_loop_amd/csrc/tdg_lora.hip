@@ -312,6 +312,42 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
     unsigned char *up_at = smem + 2 * IL::BYTES + (tid >> 6) * IU::BYTES;
     for (int c0 = 0; c0 < p.rank; c0 += 64) {
         if (c0) __syncthreads();  // every wave is done with the block before
+        // Chunks of up[a]'s rows c0 + q / CPR: U of them per lane at a time.
+        constexpr int U = MI * NI <= 4 ? 8 : 4;
+        const int need = min(64, p.rank16 - c0) * IU::CPR;  // the rank's rows, in steps of the MFMA's 16
+        auto load_up = [&](int a, int q0, u32x4 (&u)[U]) __attribute__((always_inline)) {
+            const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col0 * 2;
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                const int q = q0 + i * 64 + lane, r = q / IU::CPR, c = ((q % IU::CPR) ^ IU::swz(r)) * 8;
+                const unsigned char *src = up + (int64_t)(c0 + r) * p.ld_up;
+                if (WHOLE) {
+                    const bool ok = c0 + r < p.rank && col0 + c < p.N;
+                    u[i] = load16_global(ok ? src + c * 2 : (const unsigned char *)tdg_zero16);
+                } else {
+                    u[i] = load_chunk(src, c0 + r < p.rank, c, p.N - col0);
+                }
+            }
+        };
+        auto store_up = [&](int q0, const u32x4 (&u)[U]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < U; i++) lds_write16(up_at + (q0 + i * 64 + lane) * 16, u[i]);
+        };
+        // Small tiles have the registers to load the first adapter's up beside
+        // low, and each later one's while the matrix cores work on the one
+        // before.
+        constexpr bool early = MI * NI <= 4;
+        static_assert(!early || IU::CHUNKS <= U * 64, "one batch holds a block of up");
+        u32x4 u[U];
+        int loaded = -1;
+        if (early) {
+            const int id = rows.id[r0 + (lane & 31)];
+            const uint32_t some = (uint32_t)__ballot(id >= 0);
+            if (some) {
+                loaded = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(some) - 1));
+                load_up(loaded, 0, u);
+            }
+        }
         constexpr int PER = 2 * IL::CHUNKS / (WAVES * 64);
         u32x4 v[PER];
 #pragma unroll
@@ -331,34 +367,28 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
             const int at = r0 + mi * 32;
             const int id = rows.id[at + (lane & 31)];
             uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
-            while (left) {
-                const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
+            if (!left) continue;
+            int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
+            if (early && staged != a && loaded != a) load_up(a, 0, u);
+            for (;;) {
                 const uint32_t mine = (uint32_t)__ballot(id == a);
                 left &= ~mine;
                 if (staged != a) {
-                    const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col0 * 2;
-                    // rows of the rank that are there, in steps of the MFMA's 16
-                    const int need = min(64, p.rank16 - c0) * IU::CPR;
-                    for (int q0 = 0; q0 < need; q0 += 256) {
-                        u32x4 u[4];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int q = q0 + i * 64 + lane, r = q / IU::CPR;
-                            const int c = ((q % IU::CPR) ^ IU::swz(r)) * 8;
-                            const unsigned char *src = up + (int64_t)(c0 + r) * p.ld_up;
-                            if (WHOLE) {
-                                const bool ok = c0 + r < p.rank && col0 + c < p.N;
-                                u[i] = load16_global(ok ? src + c * 2 : (const unsigned char *)tdg_zero16);
-                            } else {
-                                u[i] = load_chunk(src, c0 + r < p.rank, c, p.N - col0);
-                            }
+                    if (early) {
+                        store_up(0, u);
+                    } else {
+                        for (int q0 = 0; q0 < need; q0 += U * 64) {
+                            load_up(a, q0, u);
+                            store_up(q0, u);
                         }
-#pragma unroll
-                        for (int i = 0; i < 4; i++) lds_write16(up_at + (q0 + i * 64 + lane) * 16, u[i]);
                     }
                     staged = a;
                     __builtin_amdgcn_wave_barrier();
                 }
+                const int next =
+                    left ? __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1)) : a;
+                if (early && next != a) load_up(next, 0, u);
+                loaded = -1;
                 f32x16 sum[NI];
 #pragma unroll
                 for (int ni = 0; ni < NI; ni++) sum[ni] = f32x16{};
@@ -368,9 +398,9 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                     const u32x4 hi = IL::read(smem, lane, at, s), rest = IL::read(smem + IL::BYTES, lane, at, s);
 #pragma unroll
                     for (int ni = 0; ni < NI; ni++) {
-                        const u32x4 u = IU::read(up_at, lane, ni * 32, s);
-                        sum[ni] = Mfma<DT_F16>::mac_sub(hi, u, sum[ni], 0);
-                        sum[ni] = Mfma<DT_F16>::mac_sub(rest, u, sum[ni], 0);
+                        const u32x4 b = IU::read(up_at, lane, ni * 32, s);
+                        sum[ni] = Mfma<DT_F16>::mac_sub(hi, b, sum[ni], 0);
+                        sum[ni] = Mfma<DT_F16>::mac_sub(rest, b, sum[ni], 0);
                     }
                 }
                 __builtin_amdgcn_wave_barrier();
@@ -384,6 +414,8 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                         for (int ni = 0; ni < NI; ni++) acc[mi][ni][w] += scale * ldexpf(sum[ni][w], e);
                     }
                 }
+                if (!left) break;
+                a = next;
             }
         }
     }
@@ -635,7 +667,7 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     // Workgroups that share a row tile's distinct adapters, of which it has at
     // most as many as rows (one without work costs about 3 us of a slot).
     const int64_t tall = M < PART_TILE ? M : PART_TILE;
-    const int64_t lanes = (plan.few ? 512 : 1024) / (low_tiles * plan.low_parts * p.low_cols);
+    const int64_t lanes = 512 / (low_tiles * plan.low_parts * p.low_cols);
     p.low_lanes = (int)(lanes < 1 ? 1 : lanes > tall ? tall : lanes);
     p.row_tiles = (int)low_tiles, p.col_tiles = (int)ceil_quot(N, 64);
     const int64_t shared = plan.few ? ceil_quot(low_tiles * p.col_tiles * plan.parts, 8) * 8 : 0;
