@@ -451,11 +451,11 @@ struct GroupedRing {
         }
     }
 
-    // The first tiles into the buffers, all of which are free.
+    // The first tiles into the buffers, all of which are free.  (Not unrolled:
+    // a workgroup that runs once waits for its instructions too.)
     __device__ __forceinline__ void start() const {
-#pragma unroll
-        for (int p = 0; p < STAGES; p++) {
-            if (p >= nt) break;
+#pragma unroll 1
+        for (int p = 0; p < min(STAGES, nt); p++) {
             if ((len & 63) != 0 && p == nt - 1) {  // the tile that the end of k cuts
 #pragma unroll
                 for (int d = 0; d < ND; d++) issue<true>(p, d);

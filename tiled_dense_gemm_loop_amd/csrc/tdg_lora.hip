@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_lora_split(LoraArgs p) {
 // What a tile's end needs of each of its rows, kept in LDS from the start.
 template <int BM>
 struct TileRows {
-    int32_t row[BM], id[BM], ex[BM];
+    __attribute__((aligned(16))) int32_t row[BM], id[BM], ex[BM];
     __device__ __forceinline__ void fill(const LoraArgs &p, int x0) {
         for (int i = threadIdx.x; i < BM; i += blockDim.x) {
             const int2 seat = p.seat[min(x0 + i, p.M - 1)];
@@ -315,18 +315,20 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
         // Chunks of up[a]'s rows c0 + q / CPR: U of them per lane at a time.
         constexpr int U = MI * NI <= 4 ? 8 : 4;
         const int need = min(64, p.rank16 - c0) * IU::CPR;  // the rank's rows, in steps of the MFMA's 16
+        // (The chunk of a lane is the same in every eighth row: swz repeats.)
+        static_assert(64 % IU::CPR == 0 && (64 / IU::CPR) % 4 == 0, "the swizzle must repeat");
+        const int up_r = lane / IU::CPR, up_c = ((lane % IU::CPR) ^ IU::swz(up_r)) * 8;
         auto load_up = [&](int a, int q0, u32x4 (&u)[U]) __attribute__((always_inline)) {
-            const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col0 * 2;
+            const int r0 = c0 + q0 / IU::CPR + up_r;
+            const unsigned char *src = p.up + (int64_t)a * p.stride_up + (int64_t)r0 * p.ld_up + (int64_t)(col0 + up_c) * 2;
+            const int64_t step = 64 / IU::CPR * p.ld_up;
 #pragma unroll
             for (int i = 0; i < U; i++) {
-                const int q = q0 + i * 64 + lane, r = q / IU::CPR, c = ((q % IU::CPR) ^ IU::swz(r)) * 8;
-                const unsigned char *src = up + (int64_t)(c0 + r) * p.ld_up;
-                if (WHOLE) {
-                    const bool ok = c0 + r < p.rank && col0 + c < p.N;
-                    u[i] = load16_global(ok ? src + c * 2 : (const unsigned char *)tdg_zero16);
-                } else {
-                    u[i] = load_chunk(src, c0 + r < p.rank, c, p.N - col0);
-                }
+                const bool ok = r0 + i * (64 / IU::CPR) < p.rank;
+                if (WHOLE)
+                    u[i] = load16_global(ok && col0 + up_c < p.N ? src + i * step : (const unsigned char *)tdg_zero16);
+                else
+                    u[i] = load_chunk(src + i * step, ok, 0, p.N - col0 - up_c);
             }
         };
         auto store_up = [&](int q0, const u32x4 (&u)[U]) __attribute__((always_inline)) {
@@ -369,7 +371,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
             uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
             if (!left) continue;
             int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
-            if (early && staged != a && loaded != a) load_up(a, 0, u);
+            if (early && MI > 1 && staged != a && loaded != a) load_up(a, 0, u);  // (one block: loaded above)
             for (;;) {
                 const uint32_t mine = (uint32_t)__ballot(id == a);
                 left &= ~mine;
@@ -389,6 +391,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                     left ? __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1)) : a;
                 if (early && next != a) load_up(next, 0, u);
                 loaded = -1;
+                const float scale = p.scale ? p.scale[a] : 1.0f;
                 f32x16 sum[NI];
 #pragma unroll
                 for (int ni = 0; ni < NI; ni++) sum[ni] = f32x16{};
@@ -404,14 +407,20 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                     }
                 }
                 __builtin_amdgcn_wave_barrier();
-                const float scale = p.scale ? p.scale[a] : 1.0f;
+                // an accumulator's rows 4 q .. 4 q + 3 follow each other
 #pragma unroll
-                for (int w = 0; w < 16; w++) {
-                    const int r = (w >> 2) * 8 + (lane >> 5) * 4 + (w & 3);
-                    const int e = rows.ex[at + r];
-                    if ((mine >> r) & 1) {
+                for (int q = 0; q < 4; q++) {
+                    const int r = q * 8 + (lane >> 5) * 4;
+                    const i32x4 e = *(const i32x4 *)&rows.ex[at + r];
 #pragma unroll
-                        for (int ni = 0; ni < NI; ni++) acc[mi][ni][w] += scale * ldexpf(sum[ni][w], e);
+                    for (int w = 0; w < 4; w++) {
+                        const bool on = (mine >> (r + w)) & 1;
+#pragma unroll
+                        for (int ni = 0; ni < NI; ni++) {
+                            const float c = acc[mi][ni][q * 4 + w];
+                            const float more = c + scale * ldexpf(sum[ni][q * 4 + w], e[w]);
+                            acc[mi][ni][q * 4 + w] = on ? more : c;
+                        }
                     }
                 }
                 if (!left) break;
@@ -442,20 +451,33 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     const int r0 = (wave % WM) * E::WTM, x0 = tm * BM + r0, col0 = tn * BN + (wave / WM) * E::WTN;
     add_adapters<E::MI, E::NI, WHOLE, BM, WM * WN>(p, rows, r0, col0, smem, acc);
     // whole 128-byte lines past the caches, as in store_tile
-    const bool inside = x0 + E::WTM <= p.M && col0 + E::WTN <= p.N;
-    const bool stream = inside && (((uintptr_t)p.C | (uint64_t)p.ldc) & 127) == 0;
+    auto store = [&](auto masked, auto streaming) __attribute__((always_inline)) {
 #pragma unroll
-    for (int mi = 0; mi < E::MI; mi++)
+        for (int mi = 0; mi < E::MI; mi++)
 #pragma unroll
-        for (int v = 0; v < 16; v++) {
-            const int r = mi * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-            float *dst = (float *)((unsigned char *)p.C + (int64_t)rows.row[r0 + r] * p.ldc) + col0 + (lane & 31);
+            for (int q = 0; q < 4; q++) {
+                const int r = mi * 32 + q * 8 + (lane >> 5) * 4;
+                const i32x4 at = *(const i32x4 *)&rows.row[r0 + r];
 #pragma unroll
-            for (int ni = 0; ni < E::NI; ni++) {
-                if (stream) __builtin_nontemporal_store(acc[mi][ni][v], dst + ni * 32);
-                else if (inside || (x0 + r < p.M && col0 + ni * 32 + (lane & 31) < p.N)) dst[ni * 32] = acc[mi][ni][v];
+                for (int w = 0; w < 4; w++) {
+                    float *dst = (float *)((unsigned char *)p.C + (int64_t)at[w] * p.ldc) + col0 + (lane & 31);
+                    const bool row_on = !decltype(masked)::value || x0 + r + w < p.M;
+#pragma unroll
+                    for (int ni = 0; ni < E::NI; ni++) {
+                        if (decltype(masked)::value && !(row_on && col0 + ni * 32 + (lane & 31) < p.N)) continue;
+                        if constexpr (decltype(streaming)::value)
+                            __builtin_nontemporal_store(acc[mi][ni][q * 4 + w], dst + ni * 32);
+                        else
+                            dst[ni * 32] = acc[mi][ni][q * 4 + w];
+                    }
+                }
             }
-        }
+    };
+    const bool inside = x0 + E::WTM <= p.M && col0 + E::WTN <= p.N;
+    const bool lines = (((uintptr_t)p.C | (uint64_t)p.ldc) & 127) == 0;
+    if (inside && lines) store(std::false_type{}, std::true_type{});
+    else if (inside) store(std::false_type{}, std::false_type{});
+    else store(std::true_type{}, std::false_type{});
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
