@@ -452,6 +452,39 @@ def test_grouped_past_32_bits(lib):
         assert torch.equal(got[s].double(), a[s, K - 64:].double() @ small[g].cpu().double())
 
 
+def test_grouped_rows_far_apart(lib):
+    """Leading dimensions past what a lane's 32-bit offsets reach, each operand
+    in turn; and rows that all lie in one group."""
+    r = rng(23)
+    far = 9000000
+    off = torch.tensor([0, 30, 260], dtype=torch.int32, device="cuda")
+    a, b, dy = whole(r, 260, 40), whole(r, 2, 40, 24), whole(r, 260, 24)
+    want, _ = grouped64(a, b, off.cpu())
+    buf = torch.zeros(259 * far + 64, dtype=F16, device="cuda")
+    wide = lambda t: torch.as_strided(buf, tuple(t.shape), (far, 1), 5).copy_(t)
+    deep = lambda t: torch.as_strided(buf, tuple(t.shape), (t.shape[1] * far, far, 1), 3).copy_(t)
+    same = lambda got, want: near(got, want, torch.zeros_like(want))
+    same(lib.gemm_f16f32_grouped(wide(a), b.cuda(), off), want)
+    same(lib.gemm_f16f32_grouped(a.cuda(), deep(b), off), want)
+    bt = b.transpose(1, 2).contiguous()
+    same(lib.gemm_f16f32_grouped_nt(a.cuda(), deep(bt), off), want)
+    dw = torch.stack([a[:30].double().t() @ dy[:30].double(), a[30:].double().t() @ dy[30:].double()])
+    same(lib.gemm_f16f32_grouped_tn(wide(a), dy.cuda(), off), dw)
+    same(lib.gemm_f16f32_grouped_tn(a.cuda(), wide(dy), off), dw)
+
+
+def test_grouped_without_rows(lib):
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, 40, dtype=F16, device="cuda")
+    dw = lib.gemm_f16f32_grouped_tn(none, torch.empty(0, 24, dtype=F16, device="cuda"), off,
+                                    torch.full((3, 40, 24), -7.0, device="cuda"))
+    assert not dw.any()
+    big = lib.gemm_f16f32_grouped_tn(torch.empty(0, 2048, dtype=F16, device="cuda"),
+                                     torch.empty(0, 8192, dtype=F16, device="cuda"), off)
+    assert big.shape == (3, 2048, 8192) and not big.any()
+    assert lib.gemm_f16f32_grouped(none, torch.ones(3, 40, 24, dtype=F16, device="cuda"), off).shape == (0, 24)
+
+
 # ------------------------------------------------------------------ adapters
 
 LORA = [  # M, K, N, adapters, rank, tokens of a request
@@ -520,6 +553,42 @@ def test_adapters_do_not_touch_each_other(lib, M, run):
     none = pick < 0
     tol = K * U2 * (a.double().abs() @ b.double().abs())
     near(got[none], plain[none], 2 * tol[none])
+
+
+@pytest.mark.parametrize("M", [5, 200, 600])
+def test_lora_operands_far_apart(lib, M):
+    """Leading dimensions past what a lane's 32-bit offsets reach."""
+    r = rng(24, M)
+    far = 9000000
+    K, N, n, rank = 40, 56, 2, 6
+    a, b, down, up = whole(r, M, K, most=2), whole(r, K, N), whole(r, n, K, rank, most=1), whole(r, n, rank, N)
+    pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
+    want, _, _ = lora64(a, b, down, up, pick, None)
+    buf = torch.zeros(max(M, n * K) * far, dtype=F16, device="cuda")
+    at = lambda t, i: (torch.as_strided(buf, tuple(t.shape), (far, 1), 3) if t.dim() == 2 else torch.as_strided(
+        buf, tuple(t.shape), (t.shape[1] * far, far, 1), 3)).copy_(t)
+    for i in range(4):
+        args = [t.cuda() for t in (a, b, down, up)]
+        args[i] = at((a, b, down, up)[i], i)
+        near(lib.gemm_f16f32_lora(*args, pick.cuda()), want, torch.zeros_like(want))
+
+
+def test_lora_many_adapters_and_one_workspace(lib):
+    """More adapters than the sort has counters, rows over several of its
+    blocks, and one workspace for calls of different sizes on one stream."""
+    r = rng(25)
+    K, N, n, rank = 48, 72, 3000, 8
+    down, up = whole(r, n, K, rank, most=1), whole(r, n, rank, N, most=2)
+    b = whole(r, K, N)
+    ws = torch.empty(lib.tdg_lora_workspace(9000, N, K, n, rank), dtype=torch.uint8, device="cuda")
+    for M in (9000, 300, 100, 4097, 20):
+        a = whole(r, M, K, most=2)
+        pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
+        x, at = a.double(), pick.clamp(min=0).long()
+        low = torch.bmm(x[:, None, :], down.double()[at])
+        want = x @ b.double() + torch.bmm(low, up.double()[at])[:, 0] * (pick >= 0)[:, None]
+        got = lib.gemm_f16f32_lora(a.cuda(), b.cuda(), down.cuda(), up.cuda(), pick.cuda(), workspace=ws)
+        near(got, want, torch.zeros_like(want))
 
 
 @pytest.mark.parametrize("M", [3, 400])
