@@ -419,10 +419,14 @@ int64_t tdg_lds_probe_bytes(int mode, int64_t iters);
  * workspace) may not overlap each other or an input; sizes are 0 .. 2^31 -
  * 2^16; leading dimensions and strides are in elements; every array is aligned
  * to its element.  Shapes past one launch's grid (over 16 million workgroups)
- * are TDG_ERR_UNSUPPORTED.  Results are the same
- * from run to run.  Ids, slots and offsets are read on the device and never
- * lead a read or write outside the arrays as described here, whatever they
- * hold. */
+ * are TDG_ERR_UNSUPPORTED.  Results are the same from run to run, and the
+ * calls can be captured into a graph.  Ids, slots and offsets are read on the
+ * device and never lead a read or write outside the arrays as described here,
+ * whatever they hold.  The products read A, B, down and up to the end of the
+ * 16-byte piece that holds their last element, within its 4 KiB page; what is
+ * read there is not used.  Calls that may run at the same time (on several
+ * streams, or in graphs that are replayed side by side) need a workspace
+ * each; calls that follow each other on one stream can share it. */
 
 /* Element of the rows that tdg_rows_* move. */
 typedef enum { TDG_ELEM_F16 = 0, TDG_ELEM_F32 = 1 } tdg_elem;

@@ -10,6 +10,7 @@ import tiled_dense_gemm_loop_amd as tdg
 from conftest import no_device_only
 
 BAD, OK, NODEV = tdg.TDG_ERR_INVALID_ARG, tdg.TDG_OK, tdg.TDG_ERR_NO_DEVICE
+TOO_BIG = tdg.TDG_ERR_UNSUPPORTED
 G = 1 << 30  # addresses a gibibyte apart never overlap here
 A, B, C, D, E, F = (G * i for i in range(1, 7))
 
@@ -110,6 +111,28 @@ def test_adapter_arguments_are_not_needed_without_adapters():
     assert call("gemm_f16f32_lora", LORA, rank=0, **none) == NODEV
     assert call("tdg_rows_combine", COMBINE, weights=None, ld_weights=0) == NODEV
     assert call("gemm_f16f32_grouped", NN, stride_b=0) == NODEV  # one B for all groups
+
+
+def test_grids_past_one_launch_are_refused():
+    """Sizes that pass every check but would need more workgroups than one
+    launch counts, in any of a call's launches."""
+    far = [1 << 50, 2 << 50, 3 << 50, 4 << 50, 5 << 50, 6 << 50, 7 << 50]
+    M = (1 << 26) + 4  # the launch that cuts low's rows has a workgroup for four
+    big = dict(K=1, rank=1, a=far[0], lda=1, b=far[1], down=far[2], ld_down=1, stride_down=1, up=far[3],
+               adapter=far[4], c=far[5], ws=far[6], ws_bytes=1 << 45)
+    for size in (dict(M=M, N=1), dict(M=1 << 20, N=1 << 20)):
+        n = size["N"]
+        assert call("gemm_f16f32_lora", LORA, **{**big, **size}, ldb=n, ld_up=n, stride_up=n, ldc=n) == TOO_BIG
+    n = 1 << 25  # few rows: 65536 workgroups across at the join
+    assert call("gemm_f16f32_lora", LORA, **big, M=4, N=n + 1, ldb=n + 1, ld_up=n + 1, stride_up=n + 1,
+                ldc=n + 1) == TOO_BIG
+    assert call("tdg_rows_dispatch", DISPATCH, tokens=1 << 24, top_k=1, cols=8192, ldx=8192, ldo=8192, rows=1,
+                x=far[0], out=far[1], slots=far[2]) == TOO_BIG
+    m = 1 << 30
+    for name, args, more in (("gemm_f16f32_grouped", NN, dict(lda=1, ldb=m, stride_b=m)),
+                             ("gemm_f16f32_grouped_nt", NT, dict(lda=1, ldb=1, stride_b=m))):
+        assert call(name, args, M=m, N=m, K=1, ldc=m, offsets=far[3], a=far[0], b=far[1], c=1 << 62, groups=1,
+                    **more) == TOO_BIG
 
 
 def test_workspace_sizes():

@@ -452,11 +452,11 @@ def test_grouped_past_32_bits(lib):
         assert torch.equal(got[s].double(), a[s, K - 64:].double() @ small[g].cpu().double())
 
 
-def test_grouped_rows_far_apart(lib):
-    """Leading dimensions past what a lane's 32-bit offsets reach, each operand
-    in turn; and rows that all lie in one group."""
+@pytest.mark.parametrize("far", [8388351, 8388352, 8388353, 9000000])
+def test_grouped_rows_far_apart(lib, far):
+    """Leading dimensions around and past what a lane's 32-bit offsets reach,
+    each operand in turn; and rows that all lie in one group."""
     r = rng(23)
-    far = 9000000
     off = torch.tensor([0, 30, 260], dtype=torch.int32, device="cuda")
     a, b, dy = whole(r, 260, 40), whole(r, 2, 40, 24), whole(r, 260, 24)
     want, _ = grouped64(a, b, off.cpu())
@@ -471,6 +471,25 @@ def test_grouped_rows_far_apart(lib):
     dw = torch.stack([a[:30].double().t() @ dy[:30].double(), a[30:].double().t() @ dy[30:].double()])
     same(lib.gemm_f16f32_grouped_tn(wide(a), dy.cuda(), off), dw)
     same(lib.gemm_f16f32_grouped_tn(a.cuda(), wide(dy), off), dw)
+
+
+@pytest.mark.parametrize("far", [8388352, 8388353])
+def test_grouped_large_tiles_far_apart(lib, far):
+    """The same for 256 rows by 256 columns at a time."""
+    r = rng(26)
+    off = torch.tensor([0, 260], dtype=torch.int32, device="cuda")
+    a, b = whole(r, 260, 40), whole(r, 1, 40, 65536)
+    buf = torch.zeros(259 * far + 64, dtype=F16, device="cuda")
+    a_far = torch.as_strided(buf, (260, 40), (far, 1), 7).copy_(a)
+    got = lib.gemm_f16f32_grouped(a_far, b.cuda(), off)
+    want = (a.float() @ b[0].float()).double()  # small whole numbers: exact
+    near(got, want, torch.zeros_like(want))
+    bt = whole(r, 1, 300, 40)
+    a2 = whole(r, 60000, 40)
+    bt_far = torch.as_strided(buf.zero_()[:259 * far + 64], (1, 260, 40), (260 * far, far, 1), 7).copy_(bt[:, :260])
+    off2 = torch.tensor([0, 60000], dtype=torch.int32, device="cuda")
+    want = (a2.float() @ bt[0, :260].float().t()).double()
+    near(lib.gemm_f16f32_grouped_nt(a2.cuda(), bt_far, off2), want, torch.zeros_like(want))
 
 
 def test_grouped_without_rows(lib):
@@ -555,16 +574,16 @@ def test_adapters_do_not_touch_each_other(lib, M, run):
     near(got[none], plain[none], 2 * tol[none])
 
 
-@pytest.mark.parametrize("M", [5, 200, 600])
-def test_lora_operands_far_apart(lib, M):
-    """Leading dimensions past what a lane's 32-bit offsets reach."""
+@pytest.mark.parametrize("M,far", [(5, 8388352), (200, 8388352), (255, 8388352), (256, 8388352), (5, 9000000),
+                                   (200, 9000000), (600, 9000000), (1000, 2147483), (1000, 2147484)])
+def test_lora_operands_far_apart(lib, M, far):
+    """Leading dimensions around and past what a lane's 32-bit offsets reach."""
     r = rng(24, M)
-    far = 9000000
     K, N, n, rank = 40, 56, 2, 6
     a, b, down, up = whole(r, M, K, most=2), whole(r, K, N), whole(r, n, K, rank, most=1), whole(r, n, rank, N)
     pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
     want, _, _ = lora64(a, b, down, up, pick, None)
-    buf = torch.zeros(max(M, n * K) * far, dtype=F16, device="cuda")
+    buf = torch.zeros(max(M, n * K) * far + 64, dtype=F16, device="cuda")
     at = lambda t, i: (torch.as_strided(buf, tuple(t.shape), (far, 1), 3) if t.dim() == 2 else torch.as_strided(
         buf, tuple(t.shape), (t.shape[1] * far, far, 1), 3)).copy_(t)
     for i in range(4):

@@ -610,10 +610,11 @@ def _types():
     """Loads torch's names that the calls below use, once."""
     global _FLOATS, _HALF, _SINGLE, _INT, _empty, _device_now
     torch = _torch()
-    _FLOATS, _HALF = (torch.float16, torch.float32), (torch.float16, torch.int16)
-    _SINGLE, _INT = (torch.float32,), (torch.int32,)
     _empty = torch.empty_strided  # a microsecond less than torch.empty with a device
     _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _FLOATS, _HALF = (torch.float16, torch.float32), (torch.float16, torch.int16)
+    _SINGLE = (torch.float32,)
+    _INT = (torch.int32,)  # the last: callers in other threads look at it
 
 
 def _mat(t, types, what, dev=None):

@@ -494,81 +494,63 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_any(LoraArgs p) {
 }
 
 // The second launch for few rows: C[t][n] = the shared product's parts, in
-// order, plus scale * sum_c low[t][c] * up[c][n].  A thread owns V columns of
-// ROWS rows; neighbouring rows with the same adapter share up's loads.  Bound
-// by latency: up's loads go out eight at a time, and the parts' before them.
+// order, plus scale * sum_c low[t][c] * up[c][n].  A workgroup has one row, a
+// thread V of its columns.  Bound by latency: up's loads go out eight at a
+// time, and the parts' before them.
 constexpr int JOIN_THREADS = 256;
+static_assert(JOIN_THREADS >= TDG_LORA_MAX_RANK, "a thread per element of low's row");
 
-template <int V, int ROWS>
+template <int V>
 __global__ void __launch_bounds__(JOIN_THREADS) k_lora_join(LoraArgs p) {
     typedef float fv __attribute__((ext_vector_type(V)));
     typedef _Float16 hv __attribute__((ext_vector_type(V)));
     typedef fv fv_ua __attribute__((aligned(4)));
     typedef hv hv_ua __attribute__((aligned(2)));
-    __shared__ float low[ROWS][TDG_LORA_MAX_RANK];
-    const int t0 = blockIdx.x * ROWS, tid = threadIdx.x;
+    __shared__ float low[TDG_LORA_MAX_RANK];
+    const int t = blockIdx.x, tid = threadIdx.x;
     const int64_t n = ((int64_t)blockIdx.y * JOIN_THREADS + tid) * V;
     const bool on = n < p.N;
-    fv sum[ROWS];
+    fv v[MAX_PARTS];
 #pragma unroll
-    for (int j = 0; j < ROWS; j++) {
-        fv v[MAX_PARTS];
+    for (int i = 0; i < MAX_PARTS; i++)
+        v[i] = on && i < p.parts ? *(const fv_ua *)(p.part + ((int64_t)i * p.M + t) * p.N + n) : fv{};
+    fv sum = v[0];
 #pragma unroll
-        for (int i = 0; i < MAX_PARTS; i++)
-            v[i] = on && i < p.parts && t0 + j < p.M ? *(const fv_ua *)(p.part + ((int64_t)i * p.M + t0 + j) * p.N + n)
-                                                     : fv{};
-        sum[j] = v[0];
-#pragma unroll
-        for (int i = 1; i < MAX_PARTS; i++) sum[j] += v[i];
-    }
-    int id[ROWS];
-#pragma unroll
-    for (int j = 0; j < ROWS; j++) id[j] = __builtin_amdgcn_readfirstlane(adapter_of(p, t0 + j));
-#pragma unroll
-    for (int j = 0; j < ROWS; j++) {
-        if (id[j] < 0 || tid >= p.rank) continue;
-        float v[MAX_PARTS];
+    for (int i = 1; i < MAX_PARTS; i++) sum += v[i];
+    const int id = __builtin_amdgcn_readfirstlane(adapter_of(p, t));
+    if (id >= 0 && tid < p.rank) {
+        float l[MAX_PARTS];
 #pragma unroll
         for (int i = 0; i < MAX_PARTS; i++)
-            v[i] = i < p.low_parts ? p.low[((int64_t)i * p.M + t0 + j) * p.rank + tid] : 0.0f;
-        float s = v[0];
+            l[i] = i < p.low_parts ? p.low[((int64_t)i * p.M + t) * p.rank + tid] : 0.0f;
+        float s = l[0];
 #pragma unroll
-        for (int i = 1; i < MAX_PARTS; i++) s += v[i];
-        low[j][tid] = s;
+        for (int i = 1; i < MAX_PARTS; i++) s += l[i];
+        low[tid] = s;
     }
     __syncthreads();
     if (!on) return;
-    fv side[ROWS] = {};
-    for (int c0 = 0; c0 < p.rank; c0 += 8) {
-        hv u[8];
+    if (id >= 0) {
+        const unsigned char *up = p.up + (int64_t)id * p.stride_up + n * 2;
+        fv side = {};
+        for (int c0 = 0; c0 < p.rank; c0 += 8) {
+            hv u[8];
 #pragma unroll
-        for (int j = 0; j < ROWS; j++) {
-            if (id[j] < 0) continue;
-            if (j == 0 || id[j] != id[j - 1]) {
-                const unsigned char *up = p.up + (int64_t)id[j] * p.stride_up + n * 2;
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (c0 + e < p.rank) u[e] = *(const hv_ua *)(up + (int64_t)(c0 + e) * p.ld_up);
-            }
+            for (int e = 0; e < 8; e++)
+                if (c0 + e < p.rank) u[e] = *(const hv_ua *)(up + (int64_t)(c0 + e) * p.ld_up);
 #pragma unroll
             for (int e = 0; e < 8; e++)
                 if (c0 + e < p.rank) {
-                    const float l = low[j][c0 + e];
+                    const float l = low[c0 + e];
 #pragma unroll
-                    for (int q = 0; q < V; q++) side[j][q] = fmaf(l, (float)u[e][q], side[j][q]);
+                    for (int q = 0; q < V; q++) side[q] = fmaf(l, (float)u[e][q], side[q]);
                 }
         }
-    }
+        const float scale = p.scale ? p.scale[id] : 1.0f;
 #pragma unroll
-    for (int j = 0; j < ROWS; j++) {
-        if (t0 + j >= p.M) continue;
-        if (id[j] >= 0) {
-            const float scale = p.scale ? p.scale[id[j]] : 1.0f;
-#pragma unroll
-            for (int q = 0; q < V; q++) sum[j][q] = fmaf(scale, side[j][q], sum[j][q]);
-        }
-        *(fv_ua *)((unsigned char *)p.C + (int64_t)(t0 + j) * p.ldc + n * 4) = sum[j];
+        for (int q = 0; q < V; q++) sum[q] = fmaf(scale, side[q], sum[q]);
     }
+    *(fv_ua *)((unsigned char *)p.C + (int64_t)t * p.ldc + n * 4) = sum;
 }
 
 // ------------------------------------------------------------------ host side
@@ -691,53 +673,56 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     const int64_t tall = M < PART_TILE ? M : PART_TILE;
     const int64_t lanes = 512 / (low_tiles * plan.low_parts * p.low_cols);
     p.low_lanes = (int)(lanes < 1 ? 1 : lanes > tall ? tall : lanes);
-    p.row_tiles = (int)low_tiles, p.col_tiles = (int)ceil_quot(N, 64);
-    const int64_t shared = plan.few ? ceil_quot(low_tiles * p.col_tiles * plan.parts, 8) * 8 : 0;
+    // Every launch's grid is looked at before the first one goes out.
     const int64_t low_wgs = ceil_quot(low_tiles * plan.low_parts * p.low_cols * p.low_lanes, 8) * 8;
-    const int64_t wgs = low_wgs + shared;
-    if (wgs > (int64_t)UINT32_MAX / 256 || ceil_quot(M, 64) > INT32_MAX / 8 / ceil_quot(N, 64) ||
-        ceil_quot(N, JOIN_THREADS) > 65535)
+    const void *main_fn = nullptr, *join_fn = nullptr;
+    int bm = PART_TILE, bn = PART_TILE, main_threads = 256, join_v = 1;
+    if (plan.few) {
+        join_v = N % 4 == 0 ? (M <= 64 ? 2 : 4) : 1;
+        join_fn = join_v == 4   ? (const void *)&k_lora_join<4>
+                  : join_v == 2 ? (const void *)&k_lora_join<2>
+                                : (const void *)&k_lora_join<1>;
+    } else {
+        // The largest tile that gives most CUs a workgroup (M x 4096 x 4096 with 8
+        // adapters of rank 64, us, 256 / 128 / 128 x 64 wide tiles: M = 4096 172 /
+        // 221 / 274, M = 1024 121 / 77 / 91, M = 512 131 / 72 / 59).
+        auto tiles = [&](int64_t m, int64_t n) { return ceil_quot(M, m) * ceil_quot(N, n); };
+        const bool ring_up = ring_main && chunk_stays_in_page(up, rank, N, ld_up, adapters, stride_up);
+        bm = bn = 128;
+        if (!ring_up) {
+            main_fn = (const void *)&k_lora_main_any<128, 128, 2, 2>;
+        } else if (tiles(256, 256) >= 128) {
+            main_fn = (const void *)&k_lora_main_ring<256, 256, 2, 4, 2>;
+            bm = bn = 256, main_threads = 512;
+        } else if (tiles(128, 128) >= 192) {
+            main_fn = (const void *)&k_lora_main_ring<128, 128, 2, 2, 4>;
+        } else {
+            main_fn = (const void *)&k_lora_main_ring<128, 64, 4, 1, 4>;
+            bn = 64;
+        }
+    }
+    const int64_t row_tiles = ceil_quot(M, bm), col_tiles = ceil_quot(N, bn);
+    const int64_t join_y = ceil_quot(N, (int64_t)JOIN_THREADS * join_v);
+    // HIP counts a launch's threads in 32 bits (row_tiles * col_tiles fits 64).
+    auto grid_ok = [](int64_t wgs, int64_t threads) { return wgs <= (int64_t)UINT32_MAX / threads; };
+    const int64_t tiles = ceil_quot(row_tiles * col_tiles * (plan.few ? plan.parts : 1), 8) * 8;
+    const int64_t parts_wgs = low_wgs + (plan.few ? tiles : 0), split_wgs = ceil_quot(M, SPLIT_THREADS / 64);
+    if (!grid_ok(parts_wgs, 256) || !grid_ok(tiles, main_threads) || (!plan.few && !grid_ok(split_wgs, SPLIT_THREADS)) ||
+        (plan.few && (join_y > 65535 || !grid_ok(M * join_y, JOIN_THREADS))))
         return TDG_ERR_UNSUPPORTED;
-    p.low_wgs = (int)low_wgs;
+    p.low_wgs = (int)low_wgs, p.row_tiles = (int)row_tiles, p.col_tiles = (int)col_tiles;
     rc = device_check();
     if (rc != TDG_OK) return rc;
-    const void *fn;
-    if (!plan.few) {
-        rc = launch((const void *)&k_lora_sort, dim3((unsigned)ceil_quot(M, SORT_ROWS)), SORT_THREADS, &p, stream);
-        if (rc != TDG_OK) return rc;
-    }
-    fn = ring ? (const void *)&k_lora_parts_ring : (const void *)&k_lora_parts_any;
-    rc = launch(fn, dim3((unsigned)wgs), 256, &p, stream);
-    if (rc != TDG_OK) return rc;
+    const void *parts_fn = ring ? (const void *)&k_lora_parts_ring : (const void *)&k_lora_parts_any;
     if (plan.few) {
-        const int v = N % 4 == 0 ? (M <= 64 ? 2 : 4) : 1, rows = 1;
-        fn = v == 4   ? (const void *)&k_lora_join<4, 1>
-             : v == 2 ? (const void *)&k_lora_join<2, 1> : (const void *)&k_lora_join<1, 1>;
-        return launch(fn, dim3((unsigned)ceil_quot(M, rows), (unsigned)ceil_quot(N, JOIN_THREADS * v)), JOIN_THREADS,
-                      &p, stream);
+        rc = launch(parts_fn, dim3((unsigned)parts_wgs), 256, &p, stream);
+        return rc != TDG_OK ? rc
+                            : launch(join_fn, dim3((unsigned)M, (unsigned)join_y), JOIN_THREADS, &p, stream);
     }
-    rc = launch((const void *)&k_lora_split, dim3((unsigned)ceil_quot(M, SPLIT_THREADS / 64)), SPLIT_THREADS, &p, stream);
-    if (rc != TDG_OK) return rc;
-    const bool ring_up = ring_main && chunk_stays_in_page(up, rank, N, ld_up, adapters, stride_up);
-    // The largest tile that gives most CUs a workgroup (M x 4096 x 4096 with 8
-    // adapters of rank 64, us, 256 / 128 / 128 x 64 wide tiles: M = 4096 172 /
-    // 221 / 274, M = 1024 121 / 77 / 91, M = 512 131 / 72 / 59).
-    auto tiles = [&](int bm, int bn) { return ceil_quot(M, bm) * ceil_quot(N, bn); };
-    int bm = 128, bn = 128, threads = 256;
-    if (!ring_up) {
-        fn = (const void *)&k_lora_main_any<128, 128, 2, 2>;
-    } else if (tiles(256, 256) >= 128) {
-        fn = (const void *)&k_lora_main_ring<256, 256, 2, 4, 2>;
-        bm = bn = 256, threads = 512;
-    } else if (tiles(128, 128) >= 192) {
-        fn = (const void *)&k_lora_main_ring<128, 128, 2, 2, 4>;
-    } else {
-        fn = (const void *)&k_lora_main_ring<128, 64, 4, 1, 4>;
-        bn = 64;
-    }
-    p.row_tiles = (int)ceil_quot(M, bm), p.col_tiles = (int)ceil_quot(N, bn);
-    const int64_t grid = ceil_quot((int64_t)p.row_tiles * p.col_tiles, 8) * 8;
-    return launch(fn, dim3((unsigned)grid), threads, &p, stream);
+    rc = launch((const void *)&k_lora_sort, dim3((unsigned)ceil_quot(M, SORT_ROWS)), SORT_THREADS, &p, stream);
+    if (rc == TDG_OK) rc = launch(parts_fn, dim3((unsigned)parts_wgs), 256, &p, stream);
+    if (rc == TDG_OK) rc = launch((const void *)&k_lora_split, dim3((unsigned)split_wgs), SPLIT_THREADS, &p, stream);
+    return rc != TDG_OK ? rc : launch(main_fn, dim3((unsigned)tiles), main_threads, &p, stream);
 }
 
 }  // extern "C"
