@@ -592,6 +592,21 @@ def test_lora_operands_far_apart(lib, M, far):
         near(lib.gemm_f16f32_lora(*args, pick.cuda()), want, torch.zeros_like(want))
 
 
+@pytest.mark.parametrize("M", [7, 200, 300])
+def test_lora_few_columns(lib, M):
+    """Every number of columns around a thread's share of them; the columns
+    beside C's stay as they were."""
+    r = rng(27, M)
+    for N in list(range(1, 10)) + [1021, 1023, 1026, 2049]:
+        a, b, down, up = whole(r, M, 40, most=2), whole(r, 40, N), whole(r, 3, 40, 6, most=1), whole(r, 3, 6, N)
+        pick = torch.from_numpy(r.integers(-1, 3, M)).to(torch.int32)
+        want, _, _ = lora64(a, b, down, up, pick, None)
+        buf = torch.full((M, N + 3), -7.0, device="cuda")
+        lib.gemm_f16f32_lora(a.cuda(), b.cuda(), down.cuda(), up.cuda(), pick.cuda(), C=buf[:, 1:N + 1])
+        near(buf[:, 1:N + 1], want, torch.zeros_like(want))
+        assert (buf[:, 0] == -7.0).all() and (buf[:, N + 1:] == -7.0).all()
+
+
 def test_lora_many_adapters_and_one_workspace(lib):
     """More adapters than the sort has counters, rows over several of its
     blocks, and one workspace for calls of different sizes on one stream."""

@@ -77,13 +77,13 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
     };
     // 256 x 256 needs the fewest bytes per operation, but a workgroup for
     // every CU, and rows to fill it (us, 256 / 128 / 64 wide): 16384 rows, 16
-    // groups, K = N = 4096: 568 / 653 / 1061; 4096 rows, 32 groups, K = N =
-    // 2048: 111 / 84 / 92.  128 x 128 holds two workgroups per CU with two
+    // groups, K = N = 4096: 564 / 668 / 1076; 4096 rows, 32 groups, K = N =
+    // 2048: 102 / 97 / 94.  128 x 128 holds two workgroups per CU with two
     // buffers, and where there is only one to hold it has four (TN of 16384
-    // rows, 4 groups, 1024 x 1024: 48 / 41).  64 x 64 is for products with few
-    // tiles, the ones of few rows that are bound by reading B among them (8
-    // rows, 64 groups, K = 2048, N = 1408: 24 / 13; 500 rows, 4 groups, K = N
-    // = 1000: 13 / 9).
+    // rows, 4 groups, 1024 x 1024: 50 / 43).  64 x 64 is for products with few
+    // tiles, the ones of few rows that are bound by reading B among them
+    // (against 128 x 128 with four buffers, 8 rows, 64 groups, K = 2048, N =
+    // 1408: 17 / 11; 500 rows, 4 groups, K = N = 1000: 13 / 9).
     if (tiles(256) >= 256 && (tn || rows >= 192 * live))
         return tn ? Variant{(const void *)&tdg::tdg_grouped_tn_loop<256, 256, 2, 4, 2>, 256, 256, 512, 256}
                   : Variant{lay == tdg::LAY_NN ? (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NN>

@@ -721,8 +721,8 @@ __device__ static __forceinline__ void touch(const unsigned char *P, int64_t ld,
 // `warm`: A and B are read once before all else, by all CUs at HBM's full
 // rate, which leaves them in the memory-side cache.  With HBM busy writing C,
 // a read that misses that cache takes long, and every tile waits for some.
-// (8192 rows, 32 groups, 2048 x 4000, A and B in no cache: 330 us
-// without, 271 with; one tile per workgroup 338.)
+// (8192 rows, 32 groups, 2048 x 4000: 330 us without, 271 with, A and B in no
+// cache; 269 and 277 where they are in it.  One tile per workgroup: 338.)
 template <int BM, int BN, int WM, int WN, int STAGES>
 __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_tn_loop(GroupedArgs a) {
     typedef GroupedRing<LAY_TN, BM, BN, WM, WN, STAGES> E;

@@ -57,8 +57,9 @@ struct RowsSeated {
 };
 
 // At most this many rows are "few": the key of sort_few holds them in 8 bits.
-// (300 x 4096 x 4096 with 8 adapters of rank 64: 49 us as few, 42 as many; 512
-// rows of them 66 and 50.)
+// (us as few / as many, 8 adapters of rank 64, K x N = 4096 x 4096: 128 rows
+// 28 / 39, 192 rows 34 / 36, 256 rows 38 / 39; 9 of rank 24, 1000 x 5095: 128
+// rows 22 / 27, 192 rows 25 / 25, 256 rows 29 / 27.)
 constexpr int kFewRows = 256;
 
 // Most slices of K that a product is cut into: they are read again.
@@ -495,8 +496,10 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_any(LoraArgs p) {
 
 // The second launch for few rows: C[t][n] = the shared product's parts, in
 // order, plus scale * sum_c low[t][c] * up[c][n].  A workgroup has one row, a
-// thread V of its columns.  Bound by latency: up's loads go out eight at a
-// time, and the parts' before them.
+// thread V <= N of its columns; where V does not divide N the last thread's
+// begin earlier, and it and the one before make the same values for those that
+// both have.  Bound by latency: up's loads go out eight at a time, and the
+// parts' before them.
 constexpr int JOIN_THREADS = 256;
 static_assert(JOIN_THREADS >= TDG_LORA_MAX_RANK, "a thread per element of low's row");
 
@@ -508,8 +511,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_lora_join(LoraArgs p) {
     typedef hv hv_ua __attribute__((aligned(2)));
     __shared__ float low[TDG_LORA_MAX_RANK];
     const int t = blockIdx.x, tid = threadIdx.x;
-    const int64_t n = ((int64_t)blockIdx.y * JOIN_THREADS + tid) * V;
+    int64_t n = ((int64_t)blockIdx.y * JOIN_THREADS + tid) * V;
     const bool on = n < p.N;
+    n = min(n, (int64_t)p.N - V);
     fv v[MAX_PARTS];
 #pragma unroll
     for (int i = 0; i < MAX_PARTS; i++)
@@ -678,14 +682,14 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     const void *main_fn = nullptr, *join_fn = nullptr;
     int bm = PART_TILE, bn = PART_TILE, main_threads = 256, join_v = 1;
     if (plan.few) {
-        join_v = N % 4 == 0 ? (M <= 64 ? 2 : 4) : 1;
-        join_fn = join_v == 4   ? (const void *)&k_lora_join<4>
-                  : join_v == 2 ? (const void *)&k_lora_join<2>
-                                : (const void *)&k_lora_join<1>;
+        // (4 columns a thread: 4 x 4096 x 4096 with adapters of rank 64 20.8 us,
+        // 128 rows 29.1; 2: 19.9 and 28.1.)
+        join_v = N > 1 ? 2 : 1;
+        join_fn = N > 1 ? (const void *)&k_lora_join<2> : (const void *)&k_lora_join<1>;
     } else {
         // The largest tile that gives most CUs a workgroup (M x 4096 x 4096 with 8
-        // adapters of rank 64, us, 256 / 128 / 128 x 64 wide tiles: M = 4096 172 /
-        // 221 / 274, M = 1024 121 / 77 / 91, M = 512 131 / 72 / 59).
+        // adapters of rank 64, us, 256 / 128 / 128 x 64 wide tiles: M = 4096 148 /
+        // 186 / 237, M = 1024 95 / 59 / 72, M = 512 96 / 48 / 44).
         auto tiles = [&](int64_t m, int64_t n) { return ceil_quot(M, m) * ceil_quot(N, n); };
         const bool ring_up = ring_main && chunk_stays_in_page(up, rank, N, ld_up, adapters, stride_up);
         bm = bn = 128;
