@@ -276,6 +276,8 @@ GROUPED = [  # rows of each group, K, N
     # enough tiles for the larger ones, and for several of them per workgroup
     ([300, 200], 72, 6400), ([300, 200], 72, 9001), ([1100, 947], 72, 8200), ([20, 31], 1000, 1600),
     ([20, 31], 1000, 2400), ([3, 0, 70, 1] * 66, 264, 250),
+    # many groups of a few rows
+    ([2, 0, 1, 5] * 11 + [60], 200, 1000), ([1, 3] * 15 + [33, 32], 65, 777), ([4, 1] * 13, 520, 1030),
 ]
 
 
@@ -736,6 +738,27 @@ def test_no_tile_is_read_before_it_lands(lib):
     try:
         for f, p in zip(calls, plain):
             assert torch.equal(f(), p)
+    finally:
+        lib.tdg_set_debug_flags(before)
+
+
+@pytest.mark.parametrize("rows,K,N", GROUPED[16:])
+def test_no_large_tile_is_read_before_it_lands(lib, rows, K, N):
+    r = rng(28, K, N)
+    off, R = groups_of(rows, 0, 0)
+    o, G = off.cuda(), len(rows)
+    a, b, dy = normal(r, R, K).cuda(), normal(r, G, K, N).cuda(), normal(r, R, N).cuda()
+    down, up = normal(r, G, K, 16).cuda(), normal(r, G, 16, N).cuda()
+    pick = torch.from_numpy(r.integers(-1, G, R)).to(torch.int32).cuda()
+    bt = b.transpose(1, 2).contiguous()
+    calls = [lambda: lib.gemm_f16f32_grouped(a, b, o), lambda: lib.gemm_f16f32_grouped_nt(a, bt, o),
+             lambda: lib.gemm_f16f32_grouped_tn(a, dy, o), lambda: lib.gemm_f16f32_lora(a, b[0], down, up, pick)]
+    plain = [f().clone() for f in calls]
+    before = lib.tdg_set_debug_flags(lib.TDG_DEBUG_POISON_LDS)
+    try:
+        for f, p in zip(calls, plain):
+            for _ in range(3):
+                assert torch.equal(f(), p)
     finally:
         lib.tdg_set_debug_flags(before)
 

@@ -89,8 +89,18 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
                   : Variant{lay == tdg::LAY_NN ? (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NN>
                                                : (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NT>,
                             256, 256, 512, INT32_MAX};
-    if (tiles(128) > 256) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256, INT32_MAX};
-    if (tiles(128) >= 192) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256, INT32_MAX};
+    // A few rows of each group are bound by reading B from HBM: 32 x 256 spends
+    // the copies in flight on B and reads 512 bytes of a row of it, where the
+    // tiles fill half of the CUs (us against the rules below; 64 rows, 32
+    // groups, 2048 x 2048: 41 / 45; 128 rows, 128 groups, 4096 x 1536: 157 /
+    // 171; with 16 rows a group too many groups need two: 68 / 52).
+    if (lay == tdg::LAY_NN && rows <= 8 * live && live * tdg::ceil_quot(N, 256) >= 128)
+        return {(const void *)&tdg::tdg_grouped_ring<tdg::LAY_NN, 32, 256, 1, 4, 4>, 32, 256, 256, INT32_MAX};
+    // NT reads whole rows of B, and a narrow tile more of each at a time (512
+    // rows, 32 groups, 2048 x 2048: 64 wide 58, 128 wide 69; 64 rows: 51 / 55).
+    const bool few_nt = lay == tdg::LAY_NT && rows <= 16 * live;
+    if (tiles(128) > 256 && !few_nt) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256, INT32_MAX};
+    if (tiles(128) >= 192 && !few_nt) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256, INT32_MAX};
     return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 64, 2, 2, 4), 64, 64, 256, INT32_MAX};
 }
 
