@@ -381,6 +381,60 @@ def test_lora_operands_at_a_page_end(lib, M, K, N, rank):
     near(got, want, torch.zeros_like(want))
 
 
+def wide_at_page_end(t, pad):
+    """As at_page_end, rows of `pad` elements more (the last one without)."""
+    n, r, c = t.shape if t.dim() == 3 else (1,) + tuple(t.shape)
+    flat = torch.full((n * r, c + pad), float("nan"), dtype=t.dtype)
+    flat[:, :c] = t.reshape(n * r, c)
+    held = at_page_end(flat.reshape(-1)[:(n * r - 1) * (c + pad) + c])
+    v = torch.as_strided(held, (n, r, c), (r * (c + pad), c + pad, 1))
+    return v if t.dim() == 3 else v[0]
+
+
+# each of the tiles, k in one, two and more steps, whole and cut, a few columns
+PAGE_ENDS = [([40, 0, 70], 64, 67), ([64, 128], 128, 129), ([128, 64], 192, 131), ([9, 64], 320, 65),
+             ([100, 28], 128, 3), ([70], 64, 1), ([33, 30], 65, 7), ([64], 8, 9), ([300, 212], 64, 9001),
+             ([300, 200], 72, 6403), ([1100, 948], 71, 8201), ([20, 31], 1000, 1601), ([64, 192], 256, 2401),
+             ([3, 0, 70, 1] * 66, 263, 251), ([1, 3] * 15 + [33, 31], 64, 777), ([4, 1] * 13, 521, 1029),
+             ([2, 0, 5] * 20, 192, 1001)]
+
+
+@pytest.mark.parametrize("rows,K,N", PAGE_ENDS)
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_grouped_tiles_at_a_page_end(lib, rows, K, N, pad):
+    r = rng(29, K, N, pad)
+    off, R = groups_of(rows, 0, 0)
+    a, b, dy = whole(r, R, K), whole(r, len(rows), K, N), whole(r, R, N)
+    o, zero, end = off.cuda(), lambda t: torch.zeros_like(t), lambda t: wide_at_page_end(t, pad)
+    want, _ = grouped64(a, b, off)
+    near(lib.gemm_f16f32_grouped(end(a), end(b), o), want, zero(want))
+    near(lib.gemm_f16f32_grouped(a.cuda(), end(b), o), want, zero(want))
+    near(lib.gemm_f16f32_grouped(end(a), b.cuda(), o), want, zero(want))
+    bt = b.transpose(1, 2).contiguous()
+    near(lib.gemm_f16f32_grouped_nt(end(a), end(bt), o), want, zero(want))
+    near(lib.gemm_f16f32_grouped_nt(a.cuda(), end(bt), o), want, zero(want))
+    want = torch.stack([a[int(off[g]):int(off[g + 1])].double().t() @ dy[int(off[g]):int(off[g + 1])].double()
+                        for g in range(len(rows))])
+    near(lib.gemm_f16f32_grouped_tn(end(a), end(dy), o), want, zero(want))
+    near(lib.gemm_f16f32_grouped_tn(a.cuda(), end(dy), o), want, zero(want))
+
+
+@pytest.mark.parametrize("M,K,N,rank", [(3, 64, 67, 8), (20, 128, 129, 9), (70, 192, 131, 33), (256, 65, 7, 3),
+                                        (300, 64, 129, 16), (257, 128, 3, 1), (400, 72, 1001, 40), (600, 130, 5001, 9),
+                                        (1100, 64, 6601, 17), (1100, 71, 6603, 65)])
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_lora_tiles_at_a_page_end(lib, M, K, N, rank, pad):
+    r = rng(30, M, K, pad)
+    a, b, down, up = whole(r, M, K, most=2), whole(r, K, N), whole(r, 3, K, rank, most=1), whole(r, 3, rank, N, most=2)
+    pick = torch.from_numpy(r.integers(-1, 3, M)).to(torch.int32)
+    want, _, _ = lora64(a, b, down, up, pick, None)
+    plain = [t.cuda() for t in (a, b, down, up)]
+    ends = [wide_at_page_end(t, pad) for t in (a, b, down, up)]
+    for args in (ends, [ends[0]] + plain[1:], plain[:1] + [ends[1]] + plain[2:], plain[:2] + [ends[2], plain[3]],
+                 plain[:3] + [ends[3]]):
+        near(lib.gemm_f16f32_lora(*args, pick.cuda()), want, torch.zeros_like(want))
+
+
 @pytest.mark.parametrize("K,N", [(128, 128), (72, 100), (65, 67)])
 def test_groups_do_not_touch_each_other(lib, K, N):
     """Infinities and NaN in one group's rows and weights stay in that group."""

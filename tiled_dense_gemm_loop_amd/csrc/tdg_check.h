@@ -46,15 +46,17 @@ inline bool overlaps(const void *a, uint64_t alen, const void *b, uint64_t blen)
 
 inline bool aligned_to(const void *p, uintptr_t bytes) { return (uintptr_t)p % bytes == 0; }
 
-// Whether the 16-byte chunk that holds a matrix's last 2-byte element (chunks
-// sit on a 16-byte grid from each row's start) ends in that element's 4 KiB
-// page: the next page need not be mapped.
-inline bool chunk_stays_in_page(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t count = 1,
-                                int64_t stride = 0) {
-    if (rows <= 0 || cols <= 0 || count <= 0) return true;
+// Chunks of 16 bytes sit on a 16-byte grid from each row's start, and the last
+// one of an operand can reach past its last element.  Where it would reach into
+// another 4 KiB page, which need not be mapped: that page's address, so that
+// the kernels load what they need of it element by element.  kNoStop: nowhere.
+constexpr uint64_t kNoStop = ~(uint64_t)0;
+inline uint64_t chunk_stop(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t count = 1,
+                           int64_t stride = 0) {
+    if (rows <= 0 || cols <= 0 || count <= 0) return kNoStop;
     const uintptr_t row = (uintptr_t)p + (uintptr_t)((count - 1) * stride + (rows - 1) * ld) * 2;
     const uintptr_t last = row + (uintptr_t)cols * 2 - 1, end = row + (uintptr_t)((cols - 1) / 8 * 16 + 15);
-    return last >> 12 == end >> 12;
+    return last >> 12 == end >> 12 ? kNoStop : (uint64_t)((last >> 12) + 1) << 12;
 }
 
 inline int64_t ceil_quot(int64_t a, int64_t b) { return (a + b - 1) / b; }

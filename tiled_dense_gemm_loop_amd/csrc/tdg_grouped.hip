@@ -56,17 +56,16 @@ struct Variant {
      : lay == tdg::LAY_NT ? (const void *)&tdg::KERNEL<tdg::LAY_NT, __VA_ARGS__> \
                           : (const void *)&tdg::KERNEL<tdg::LAY_TN, __VA_ARGS__>)
 
-Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
-               const void *B, int64_t ldb, int64_t stride_b) {
+Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t lda, int64_t ldb,
+               uint64_t a_stop, uint64_t b_stop) {
     const bool tn = lay == tdg::LAY_TN;
-    // The DMA copies whole 16-byte chunks, and its lanes reach a tile's rows
-    // with 32-bit byte offsets.
-    const bool chunks = tdg::chunk_stays_in_page(A, rows, tn ? M : K, lda) &&
-                        (tn ? tdg::chunk_stays_in_page(B, rows, N, ldb)
-                            : tdg::chunk_stays_in_page(B, lay == tdg::LAY_NN ? K : N, lay == tdg::LAY_NN ? N : K, ldb,
-                                                       groups, stride_b));
+    // The DMA's lanes reach a tile's rows with 32-bit byte offsets.  Where
+    // an operand's rows lie at one k each and its last chunk must not be copied
+    // (a_stop, b_stop), the rows have to be long enough for no other row's
+    // chunk to reach as far.
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
-    if (!chunks || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256, INT32_MAX};
+    const bool thin = (tn && lda < 8 && a_stop != tdg::kNoStop) || (lay != tdg::LAY_NT && ldb < 8 && b_stop != tdg::kNoStop);
+    if (thin || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256, INT32_MAX};
     // Tiles that the product is expected to have: half a row tile more per
     // group that can have rows than the rows fill, one at the least.
     const int64_t live = groups < rows ? groups : rows;
@@ -111,8 +110,12 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     if (rc != TDG_OK) return rc;
     if (groups == 0 || N == 0 || (lay == tdg::LAY_TN ? M == 0 : rows == 0)) return TDG_OK;
 
-    const Variant v = choose(lay, groups, rows, M, N, K, A, lda, B, ldb, stride_b);
     GroupedArgs a;
+    const bool tn = lay == tdg::LAY_TN;
+    a.a_stop = tdg::chunk_stop(A, rows, tn ? M : K, lda);
+    a.b_stop = tn ? tdg::chunk_stop(B, rows, N, ldb)
+                  : tdg::chunk_stop(B, lay == tdg::LAY_NN ? K : N, lay == tdg::LAY_NN ? N : K, ldb, groups, stride_b);
+    const Variant v = choose(lay, groups, rows, M, N, lda, ldb, a.a_stop, a.b_stop);
     a.A = (const unsigned char *)A, a.B = (const unsigned char *)B, a.C = (unsigned char *)C;
     a.lda = lda * 2, a.ldb = ldb * 2, a.ldc = ldc * 4;
     a.stride_b = stride_b * 2, a.stride_c = stride_c * 4;

@@ -37,6 +37,7 @@ struct GroupedArgs {
     int tiles_m;   // TN only: ceil(M / BM)
     int tiles_n;   // ceil(N / BN)
     int tiles_most;  // no tile has this number or a higher one
+    uint64_t a_stop, b_stop;  // chunks end at this address or below (chunk_stop)
     int warm;        // read A and B once at the start (tdg_grouped_tn_loop)
     int flags;       // TDG_DEBUG_* bits
 };
@@ -201,8 +202,9 @@ __device__ static __forceinline__ GroupedTile find_tile(const GroupedArgs &a, in
 // Accumulators -> C: lane l of a 32x32 block holds column l % 32 of rows
 // 8 (v / 4) + 4 (l / 32) + v % 4.  Where C's rows are whole 128-byte lines the
 // stores stream past the caches, which leaves those to A and B (8192 rows, 32
-// groups, 2048 x 4000, TN: 377 us without, 258 with).  Returns whether the tile
-// was stored whole.
+// groups, 2048 x 4000, TN: 377 us without, 258 with; 3999 columns, whose rows
+// share lines: 487 without, 815 with).  Returns whether the tile was stored
+// whole.
 template <int MI, int NI>
 __device__ static __forceinline__ bool store_tile(unsigned char *C, int64_t ldc, int row0, int row_end, int col0,
                                                   int col_end, const f32x16 (&acc)[MI][NI]) {
@@ -286,8 +288,8 @@ struct GroupedAny {
     template <class Rows>
     __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, Rows rows,
                                                const unsigned char *B, int64_t ldb, int x0, int x_end, int y0,
-                                               int y_end, int k_lo, int k_hi, unsigned char *smem,
-                                               f32x16 (&acc)[MI][NI]) {
+                                               int y_end, int k_lo, int k_hi, uint64_t, uint64_t,
+                                               unsigned char *smem, f32x16 (&acc)[MI][NI]) {
         const int nt = (k_hi - k_lo + 63) >> 6;
         if (nt <= 0) return;
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -353,7 +355,11 @@ struct GroupedAny {
 // of zeros.  Chunks that start inside a row are copied whole: what they hold
 // past a row's end feeds C elements that are not stored, or, where the row
 // runs along k, is cleared in LDS.  Past an operand's last byte they read only
-// within its 4 KiB page: the host sees to that (chunk_stays_in_page).
+// within its 4 KiB page: where its last chunk would leave it (a_stop, b_stop),
+// the last K tile takes that chunk from the block of zeros too, and its lane
+// writes the elements to LDS once the tile has landed.  (A matrix of an even
+// count of odd rows often ends with a page: 16384 rows, 16 groups of 4096 x 4095
+// 625 us, through registers 1174; 64 rows, 32 groups of 2048 x 2047 45 and 245.)
 template <int LAY, int BM, int BN, int WM, int WN, int STAGES>
 struct GroupedRing {
     typedef Image<LAY != LAY_TN, BM> IA;
@@ -380,16 +386,17 @@ struct GroupedRing {
     const unsigned char *a_base, *b_base;
     int64_t lda, ldb;
     int len, nt;       // k of the tile, and its K tiles
+    uint64_t a_stop, b_stop;
     uint32_t lds_at;   // where the wave's first chunks go in the first buffer
 
     // As GroupedAny::run; here `rows` gives offsets below 2^32.
     template <class Rows>
     __device__ static __forceinline__ void run(const unsigned char *A, int64_t lda, Rows rows,
                                                const unsigned char *B, int64_t ldb, int x0, int x_end, int y0,
-                                               int y_end, int k_lo, int k_hi, unsigned char *smem,
-                                               f32x16 (&acc)[MI][NI]) {
+                                               int y_end, int k_lo, int k_hi, uint64_t a_stop, uint64_t b_stop,
+                                               unsigned char *smem, f32x16 (&acc)[MI][NI]) {
         GroupedRing r;
-        r.aim(A, lda, rows, B, ldb, x0, x_end, y0, y_end, k_lo, k_hi, smem);
+        r.aim(A, lda, rows, B, ldb, x0, x_end, y0, y_end, k_lo, k_hi, a_stop, b_stop, smem);
         r.start();
         r.finish(smem, acc, false);
     }
@@ -397,10 +404,11 @@ struct GroupedRing {
     template <class Rows>
     __device__ __forceinline__ void aim(const unsigned char *A, int64_t lda_, Rows rows, const unsigned char *B,
                                         int64_t ldb_, int x0, int x_end, int y0, int y_end, int k_lo, int k_hi,
-                                        unsigned char *smem) {
+                                        uint64_t a_stop_, uint64_t b_stop_, unsigned char *smem) {
         lds_at = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)smem +
                  (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
         lda = lda_, ldb = ldb_;
+        a_stop = a_stop_, b_stop = b_stop_;
         len = k_hi - k_lo;
         nt = (len + 63) >> 6;
         if (nt <= 0) return;
@@ -421,24 +429,43 @@ struct GroupedRing {
 
     __device__ static __forceinline__ uint32_t stage(int t) { return (uint32_t)((t % STAGES) * STAGE); }
 
-    // Copies chunk set d (A's first, then B's) of K tile kt into its buffer.
-    template <bool CHECKED>
-    __device__ __forceinline__ void issue(int kt, int d) const {
+    // Whether the last K tile needs looking after: the end of k cuts it, or an
+    // operand's last chunk is kept off the DMA.
+    __device__ __forceinline__ bool edge() const { return (a_stop & b_stop) != ~(uint64_t)0; }
+    __device__ __forceinline__ bool cut() const { return (len & 63) != 0 || edge(); }
+
+    // Where chunk set d (A's first, then B's) of K tile kt is.
+    __device__ __forceinline__ const unsigned char *base_of(int kt, int d) const {
         const bool is_a = d < CA;
         const int i = is_a ? d : d - CA;
-        const uint32_t m0 = lds_at + stage(kt) + (uint32_t)((is_a ? 0 : IA::BYTES) + i * NT * 16);
+        return is_a ? a_base + (AKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * A_STEP) * lda)
+                    : b_base + (BKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * B_STEP) * ldb);
+    }
+    __device__ __forceinline__ uint32_t off_of(int d) const {
+        return d < CA ? a_off[AKC ? d : 0] : b_off[BKC ? d - CA : 0];
+    }
+    // The lane's chunk of the set, and whether it begins before the end of k.
+    __device__ __forceinline__ bool chunk_of(int kt, int d, uint64_t &p) const {
+        const bool is_a = d < CA;
+        const int i = is_a ? d : d - CA;
+        const int tid = thread_again();
+        const int a_r = tid / IA::CPR, a_c = (tid % IA::CPR) ^ IA::swz(a_r);
+        const int b_r = tid / IB::CPR, b_c = (tid % IB::CPR) ^ IB::swz(b_r);
+        // first k of the chunk, counted from the tile's
+        const int k = is_a ? (AKC ? a_c * 8 : i * A_STEP + a_r) : (BKC ? b_c * 8 : i * B_STEP + b_r);
+        p = (uint64_t)(uintptr_t)(base_of(kt, d) + off_of(d));
+        return k < len - kt * 64;
+    }
+
+    // Copies chunk set d of K tile kt into its buffer.
+    template <bool CHECKED>
+    __device__ __forceinline__ void issue(int kt, int d) const {
+        const uint32_t m0 = lds_at + stage(kt) + (uint32_t)((d < CA ? 0 : IA::BYTES) + (d < CA ? d : d - CA) * NT * 16);
         kt = __builtin_amdgcn_readfirstlane(kt);
-        const unsigned char *base = is_a ? a_base + (AKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * A_STEP) * lda)
-                                         : b_base + (BKC ? (int64_t)kt * 128 : (int64_t)(kt * 64 + i * B_STEP) * ldb);
-        const uint32_t off = is_a ? a_off[AKC ? i : 0] : b_off[BKC ? i : 0];
         if constexpr (CHECKED) {
-            // first k of the chunk, counted from the tile's
-            const int tid = thread_again();
-            const int a_r = tid / IA::CPR, a_c = (tid % IA::CPR) ^ IA::swz(a_r);
-            const int b_r = tid / IB::CPR, b_c = (tid % IB::CPR) ^ IB::swz(b_r);
-            const int k = is_a ? (AKC ? a_c * 8 : i * A_STEP + a_r) : (BKC ? b_c * 8 : i * B_STEP + b_r);
-            const uint64_t p = (uint64_t)(uintptr_t)(base + off);
-            const uint64_t src = k < len - kt * 64 ? p : (uint64_t)(uintptr_t)tdg_zero16;
+            uint64_t p;
+            const bool in = chunk_of(kt, d, p) && p + 16 <= (d < CA ? a_stop : b_stop);
+            const uint64_t src = in ? p : (uint64_t)(uintptr_t)tdg_zero16;
             asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
         } else {
             // The base may have been written to its scalar registers by a
@@ -447,6 +474,8 @@ struct GroupedRing {
             // them five wait states later at the earliest, which the compiler
             // does not count for inline assembly; a scalar one may read them
             // at once, and what it writes is safe.
+            const unsigned char *base = base_of(kt, d);
+            const uint32_t off = off_of(d);
             uint64_t safe;
             asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
                          : "=&s"(safe)
@@ -460,7 +489,7 @@ struct GroupedRing {
     __device__ __forceinline__ void start() const {
 #pragma unroll 1
         for (int p = 0; p < min(STAGES, nt); p++) {
-            if ((len & 63) != 0 && p == nt - 1) {  // the tile that the end of k cuts
+            if (cut() && p == nt - 1) {
 #pragma unroll
                 for (int d = 0; d < ND; d++) issue<true>(p, d);
             } else {
@@ -478,11 +507,28 @@ struct GroupedRing {
         else wait_vmcnt<0>();
     }
 
-    // Rows along k whose end splits a chunk: its elements from that end on are
-    // cleared once the last tile has landed, one thread per row.
-    __device__ __forceinline__ void clear_split(unsigned char *smem, int t) const {
+    // What the last K tile lacks when it has landed.  Chunks that were kept off
+    // the DMA: each lane writes what there is of its own.  Rows along k whose
+    // end splits a chunk: its elements from that end on are cleared, one thread
+    // per row.
+    __device__ __forceinline__ void mend_last(unsigned char *smem, int t) const {
+        if (t != nt - 1) return;
+        if (edge()) {
+#pragma unroll
+            for (int d = 0; d < ND; d++) {
+                uint64_t p;
+                const uint64_t stop = d < CA ? a_stop : b_stop;
+                if (!chunk_of(t, d, p) || p + 16 <= stop) continue;
+                u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 7; e++)
+                    if (p + 2 * e < stop) v[e / 2] |= (uint32_t)*(const TDG_GLOBAL uint16_t *)(p + 2 * e) << (16 * (e & 1));
+                lds_write16(smem + stage(t) + (d < CA ? 0 : IA::BYTES) + ((d < CA ? d : d - CA) * NT + threadIdx.x) * 16, v);
+            }
+            __syncthreads();
+        }
         const int split = AKC || BKC ? len & 7 : 0;
-        if (split == 0 || t != nt - 1) return;
+        if (split == 0) return;
         const int c = (len & 63) >> 3;
         auto clear = [&](unsigned char *p) __attribute__((always_inline)) {
             const u32x4 v = lds_read16(p);
@@ -556,7 +602,7 @@ struct GroupedRing {
         if (stores) wait_vmcnt<STORES <= 63 ? STORES : 63>();  // the tiles may be the older ones: all of them then
         else wait_tiles(min(AHEAD, nt - 1));
         __syncthreads();
-        clear_split(smem, 0);
+        mend_last(smem, 0);
 #pragma unroll
         for (int s = 0; s < FD; s++) {
 #pragma unroll
@@ -580,7 +626,7 @@ struct GroupedRing {
                         } else if (t + 1 < nt) {
                             if (!(stores && t < AHEAD)) wait_tiles(nt - 2 - t);
                             __syncthreads();
-                            clear_split(smem, t + 1);
+                            mend_last(smem, t + 1);
                         }
                         next = smem + stage(t + 1);
                     }
@@ -590,7 +636,7 @@ struct GroupedRing {
                 }
             }
         };
-        const bool cut = (len & 63) != 0;
+        const bool cut = this->cut();
         const int full = max(0, nt - STAGES);  // tiles with a later one to copy
         tiles(0, cut ? max(0, full - 1) : full, std::true_type{}, std::false_type{});
         if (cut) tiles(max(0, full - 1), full, std::true_type{}, std::true_type{});
@@ -653,7 +699,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a)
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
     E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
-           smem, acc);
+           a.a_stop, a.b_stop, smem, acc);
     w.template store<E, WM>(a, acc);
 }
 
@@ -667,7 +713,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_ring(GroupedArgs a
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
     E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
-           smem, acc);
+           a.a_stop, a.b_stop, smem, acc);
     w.template store<E, WM>(a, acc);
 }
 
@@ -686,13 +732,13 @@ __global__ void __launch_bounds__(512, 1) tdg_grouped_cut(GroupedArgs a) {
         f32x16 acc[E::MI][E::NI];
         clear_acc(acc);
         E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(),
-               w.k_hi(a), smem, acc);
+               w.k_hi(a), a.a_stop, a.b_stop, smem, acc);
         w.template store<E, 2>(a, acc);
     } else {
         f32x16 acc[H::MI][H::NI];
         clear_acc(acc);
         H::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(),
-               min(a.N, w.y0() + 128), w.k_lo(), w.k_hi(a), smem, acc);
+               min(a.N, w.y0() + 128), w.k_lo(), w.k_hi(a), a.a_stop, a.b_stop, smem, acc);
         w.template store<H, 4>(a, acc);
     }
 }
@@ -739,7 +785,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_tn_loop(GroupedArg
         E r;
         auto start = [&]() __attribute__((always_inline)) {
             r.aim(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(),
-                  w.k_hi(a), smem);
+                  w.k_hi(a), a.a_stop, a.b_stop, smem);
             r.start();
         };
         start();

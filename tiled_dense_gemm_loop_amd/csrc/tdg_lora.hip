@@ -40,6 +40,8 @@ struct LoraArgs {
     int rank16;     // the rank, rounded up to 16
     int2 *seat;     // M: row and adapter, sorted by adapter (many rows)
     int64_t lda, ldb, ldc, ld_down, stride_down, ld_up, stride_up;  // bytes
+    uint64_t a_stop, b_stop, down_stop;  // chunks end at this address or below (chunk_stop)
+    int up_apart;  // up's rows' last chunks are loaded element by element
     int M, N, K, adapters, rank;
     int row_tiles, col_tiles;           // of the shared product
     int parts, k_per_part;              // K tiles of each slice
@@ -175,7 +177,7 @@ __device__ __forceinline__ void lora_parts(const LoraArgs &p, unsigned char *sme
         const int k_lo = part * p.k_per_part * 64, k_hi = min(p.K, k_lo + p.k_per_part * 64);
         clear_acc(acc);
         E::run(p.A + (int64_t)(tm * BM) * p.lda, p.lda, RowsFrom{tm * BM, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN,
-               p.N, k_lo, k_hi, smem, acc);
+               p.N, k_lo, k_hi, p.a_stop, p.b_stop, smem, acc);
         store_tile<E::MI, E::NI>((unsigned char *)(p.part + (int64_t)part * p.M * p.N), (int64_t)p.N * 4,
                                  tm * BM + wm * E::WTM, p.M, tn * BN + wn * E::WTN, p.N, acc);
         return;
@@ -213,7 +215,7 @@ __device__ __forceinline__ void lora_parts(const LoraArgs &p, unsigned char *sme
         __syncthreads();
         clear_acc(acc);
         E::run(p.A, p.lda, RowsBy{key, p.lda}, p.down + (int64_t)a * p.stride_down, p.ld_down, 0, rows, tc * BN,
-               p.rank, k_lo, k_hi, smem, acc);
+               p.rank, k_lo, k_hi, p.a_stop, p.down_stop, smem, acc);
 #pragma unroll
         for (int mi = 0; mi < E::MI; mi++)
 #pragma unroll
@@ -302,9 +304,9 @@ struct TileRows {
 // parts of low's rows are staged in LDS for the whole tile, as the products'
 // operands are; the columns of up[a] that a wave needs are staged in a part of
 // LDS of its own, one distinct adapter of its 32-row block after the other.
-// The wave's rows begin at r0, its columns at col0.  WHOLE: chunks of up may
-// be read whole (as the DMA reads those of B).
-template <int MI, int NI, bool WHOLE, int BM, int WAVES>
+// The wave's rows begin at r0, its columns at col0.  Chunks of up are read whole,
+// as the DMA reads those of B, unless one of them would leave up's last page.
+template <int MI, int NI, int BM, int WAVES>
 __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
                                              unsigned char *smem, f32x16 (&acc)[MI][NI]) {
     typedef Image<true, BM> IL;        // the tile's rows by 64 of the rank
@@ -319,6 +321,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
         // (The chunk of a lane is the same in every eighth row: swz repeats.)
         static_assert(64 % IU::CPR == 0 && (64 / IU::CPR) % 4 == 0, "the swizzle must repeat");
         const int up_r = lane / IU::CPR, up_c = ((lane % IU::CPR) ^ IU::swz(up_r)) * 8;
+        const bool up_on = col0 + up_c < p.N, up_whole = !p.up_apart || col0 + up_c + 8 <= p.N;
         auto load_up = [&](int a, int q0, u32x4 (&u)[U]) __attribute__((always_inline)) {
             const int r0 = c0 + q0 / IU::CPR + up_r;
             const unsigned char *src = p.up + (int64_t)a * p.stride_up + (int64_t)r0 * p.ld_up + (int64_t)(col0 + up_c) * 2;
@@ -326,15 +329,20 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
 #pragma unroll
             for (int i = 0; i < U; i++) {
                 const bool ok = r0 + i * (64 / IU::CPR) < p.rank;
-                if (WHOLE)
-                    u[i] = load16_global(ok && col0 + up_c < p.N ? src + i * step : (const unsigned char *)tdg_zero16);
-                else
-                    u[i] = load_chunk(src + i * step, ok, 0, p.N - col0 - up_c);
+                u[i] = load16_global(ok && up_on && up_whole ? src + i * step : (const unsigned char *)tdg_zero16);
             }
         };
-        auto store_up = [&](int q0, const u32x4 (&u)[U]) __attribute__((always_inline)) {
+        auto store_up = [&](int a, int q0, const u32x4 (&u)[U]) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < U; i++) lds_write16(up_at + (q0 + i * 64 + lane) * 16, u[i]);
+            if (up_on && !up_whole) {  // (zeros so far)
+#pragma unroll 1
+                for (int q = q0; q < q0 + U * 64; q += 64) {
+                    const int r = c0 + q / IU::CPR + up_r;
+                    const unsigned char *src = p.up + (int64_t)a * p.stride_up + (int64_t)r * p.ld_up;
+                    lds_write16(up_at + (q + lane) * 16, load_chunk(src, r < p.rank, col0 + up_c, p.N));
+                }
+            }
         };
         // Small tiles have the registers to load the first adapter's up beside
         // low, and each later one's while the matrix cores work on the one
@@ -378,11 +386,11 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                 left &= ~mine;
                 if (staged != a) {
                     if (early) {
-                        store_up(0, u);
+                        store_up(a, 0, u);
                     } else {
                         for (int q0 = 0; q0 < need; q0 += U * 64) {
                             load_up(a, q0, u);
-                            store_up(q0, u);
+                            store_up(a, q0, u);
                         }
                     }
                     staged = a;
@@ -433,7 +441,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
 
 // The shared product's tiles for many rows, with the adapters added to the
 // accumulators.  Tile row x is row seat[x] of A and C.
-template <class E, int BM, int BN, int WM, int WN, bool WHOLE>
+template <class E, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem) {
     static_assert(E::SMEM >= 2 * Image<true, BM>::BYTES + WM * WN * Image<false, E::NI * 32>::BYTES,
                   "LDS for low and up");
@@ -446,11 +454,11 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     rows.fill(p, tm * BM);  // read behind the barriers of run()
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
-    E::run(p.A, p.lda, RowsSeated{p.seat, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, 0, p.K, smem, acc);
+    E::run(p.A, p.lda, RowsSeated{p.seat, p.lda}, p.B, p.ldb, tm * BM, p.M, tn * BN, p.N, 0, p.K, p.a_stop, p.b_stop, smem, acc);
     __syncthreads();  // every wave is done with the tiles in LDS
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r0 = (wave % WM) * E::WTM, x0 = tm * BM + r0, col0 = tn * BN + (wave / WM) * E::WTN;
-    add_adapters<E::MI, E::NI, WHOLE, BM, WM * WN>(p, rows, r0, col0, smem, acc);
+    add_adapters<E::MI, E::NI, BM, WM * WN>(p, rows, r0, col0, smem, acc);
     // whole 128-byte lines past the caches, as in store_tile
     auto store = [&](auto masked, auto streaming) __attribute__((always_inline)) {
 #pragma unroll
@@ -485,13 +493,13 @@ template <int BM, int BN, int WM, int WN, int STAGES>
 __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_ring(LoraArgs p) {
     typedef GroupedRing<LAY_NN, BM, BN, WM, WN, STAGES> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    lora_main<E, BM, BN, WM, WN, true>(p, smem);
+    lora_main<E, BM, BN, WM, WN>(p, smem);
 }
 template <int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_any(LoraArgs p) {
     typedef GroupedAny<LAY_NN, BM, BN, WM, WN> E;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[E::SMEM];
-    lora_main<E, BM, BN, WM, WN, false>(p, smem);
+    lora_main<E, BM, BN, WM, WN>(p, smem);
 }
 
 // The second launch for few rows: C[t][n] = the shared product's parts, in
@@ -663,12 +671,16 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     p.flags = debug_flags_now();
     p.parts = (int)plan.parts, p.k_per_part = (int)plan.k_per_part;
     p.low_parts = (int)plan.low_parts, p.low_k_per_part = (int)plan.low_k_per_part;
-    // The DMA copies whole 16-byte chunks and reaches a tile's rows with
-    // 32-bit byte offsets.
+    p.a_stop = chunk_stop(A, M, K, lda), p.b_stop = chunk_stop(B, K, N, ldb);
+    p.down_stop = chunk_stop(down, K, rank, ld_down, adapters, stride_down);
+    p.up_apart = chunk_stop(up, rank, N, ld_up, adapters, stride_up) != kNoStop;
+    // The DMA's lanes reach a tile's rows with 32-bit byte offsets; and rows of
+    // B and down whose last chunk must not be copied have to be long enough for
+    // no other row's chunk to reach as far.
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
-    const bool near = lda <= far && ldb <= far && ld_down <= far && M * lda <= (int64_t)UINT32_MAX / 2;
-    const bool ring_main = near && chunk_stays_in_page(A, M, K, lda) && chunk_stays_in_page(B, K, N, ldb);
-    const bool ring = ring_main && chunk_stays_in_page(down, K, rank, ld_down, adapters, stride_down);
+    const bool ring_main = lda <= far && ldb <= far && M * lda <= (int64_t)UINT32_MAX / 2 &&
+                           (ldb >= 8 || p.b_stop == kNoStop);
+    const bool ring = ring_main && ld_down <= far && (ld_down >= 8 || p.down_stop == kNoStop);
 
     const int64_t low_tiles = ceil_quot(M, PART_TILE);
     p.low_cols = (int)ceil_quot(rank, 64);
@@ -691,9 +703,8 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
         // adapters of rank 64, us, 256 / 128 / 128 x 64 wide tiles: M = 4096 148 /
         // 186 / 237, M = 1024 95 / 59 / 72, M = 512 96 / 48 / 44).
         auto tiles = [&](int64_t m, int64_t n) { return ceil_quot(M, m) * ceil_quot(N, n); };
-        const bool ring_up = ring_main && chunk_stays_in_page(up, rank, N, ld_up, adapters, stride_up);
         bm = bn = 128;
-        if (!ring_up) {
+        if (!ring_main) {
             main_fn = (const void *)&k_lora_main_any<128, 128, 2, 2>;
         } else if (tiles(256, 256) >= 128) {
             main_fn = (const void *)&k_lora_main_ring<256, 256, 2, 4, 2>;
