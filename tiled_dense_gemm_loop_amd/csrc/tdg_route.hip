@@ -339,16 +339,19 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine(RowsArgs a) {
     }
 }
 
-// One workgroup per token and group of J choices: dy's row is read once for
-// the J rows of z and dz, and the J dot products are reduced in a fixed order
-// (columns by thread, lanes by a butterfly, waves in order).
+// A token and a group of J choices belong to 1 << tx_log2 threads, one to four
+// waves: dy's row is read once for the J rows of z and dz, and the J dot
+// products are reduced in a fixed order (columns by thread, lanes by a
+// butterfly, waves in order).  Short rows take the fewest waves that cover them.
 template <typename Z, typename Y, int J>
 __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine_grad(RowsArgs a) {
     constexpr int V = 16 / sizeof(Z);
     __shared__ float part[J][ROW_THREADS / 64];
-    const int t = blockIdx.x, j0 = blockIdx.y * J;
-    const int nj = min(J, a.top_k - j0);
-    const int tid = threadIdx.x;
+    const int tx = 1 << a.tx_log2, tid = threadIdx.x & (tx - 1);
+    const int t_all = blockIdx.x * (ROW_THREADS >> a.tx_log2) + (threadIdx.x >> a.tx_log2);
+    const bool on = t_all < a.tokens;
+    const int t = on ? t_all : 0, j0 = blockIdx.y * J;
+    const int nj = on ? min(J, a.top_k - j0) : 0;
     const unsigned char *dy = a.tok + (int64_t)t * a.ld_tok;
     int slot[J];
     float w[J], dot[J];
@@ -360,10 +363,10 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine_grad(RowsArgs a) {
         dot[j] = 0.0f;
     }
     // Neighbouring tokens start in different segments of their rows: see above.
-    const int segs = (a.cols + ROW_THREADS * V - 1) / (ROW_THREADS * V);
+    const int segs = on ? (a.cols + tx * V - 1) / (tx * V) : 0;
     int seg = segs > 0 ? t % segs : 0;
     for (int i = 0; i < segs; i++, seg = seg + 1 == segs ? 0 : seg + 1) {
-        const int64_t col = ((int64_t)seg * ROW_THREADS + tid) * V;
+        const int64_t col = ((int64_t)seg * tx + tid) * V;
         if (col >= a.cols) continue;
         if (col + V <= a.cols) {
             float g[V];
@@ -399,12 +402,12 @@ __global__ void __launch_bounds__(ROW_THREADS) k_rows_combine_grad(RowsArgs a) {
 #pragma unroll
     for (int j = 0; j < J; j++) {
         for (int d = 32; d > 0; d >>= 1) dot[j] += __shfl_xor(dot[j], d);
-        if ((tid & 63) == 0) part[j][tid >> 6] = dot[j];
+        if ((threadIdx.x & 63) == 0) part[j][threadIdx.x >> 6] = dot[j];
     }
     __syncthreads();
     if (tid < nj) {
         float s = 0.0f;
-        for (int i = 0; i < ROW_THREADS / 64; i++) s += part[tid][i];
+        for (int i = 0; i < tx >> 6; i++) s += part[tid][(threadIdx.x - tid) / 64 + i];
         a.dw[(int64_t)t * a.ld_dw + j0 + tid] = s;
     }
 }
@@ -604,7 +607,12 @@ int tdg_rows_combine_grad(int row_elem, int token_elem, int64_t tokens, int64_t 
     a.tokens = (int)tokens, a.top_k = (int)top_k, a.cols = (int)cols, a.rows = (int)rows;
     const int J = top_k >= 5 ? 8 : top_k >= 3 ? 4 : top_k >= 2 ? 2 : 1;
     const int64_t gy = tdg::ceil_quot(top_k, J);
-    if (gy > 65535 || !grid_ok(tokens, ROW_THREADS)) return TDG_ERR_UNSUPPORTED;
+    // (12601 tokens x 8 rows of 177 FP16 columns: 62 us with a workgroup to
+    // each token.)
+    const int64_t units = tdg::ceil_quot(cols, 16 / zs);
+    a.tx_log2 = units <= 64 ? 6 : units <= 128 ? 7 : 8;
+    const int64_t gx = tdg::ceil_quot(tokens, ROW_THREADS >> a.tx_log2);
+    if (gy > 65535 || !grid_ok(gx, ROW_THREADS)) return TDG_ERR_UNSUPPORTED;
     const int rc = tdg::device_check();
     if (rc != TDG_OK) return rc;
 #define TDG_GRAD(Z, Y)                                                       \
@@ -616,7 +624,7 @@ int tdg_rows_combine_grad(int row_elem, int token_elem, int64_t tokens, int64_t 
                          ? (token_elem == TDG_ELEM_F16 ? TDG_GRAD(_Float16, _Float16) : TDG_GRAD(_Float16, float))
                          : (token_elem == TDG_ELEM_F16 ? TDG_GRAD(float, _Float16) : TDG_GRAD(float, float));
 #undef TDG_GRAD
-    return launch(fn, dim3((unsigned)tokens, (unsigned)gy), ROW_THREADS, 0, &a, stream);
+    return launch(fn, dim3((unsigned)gx, (unsigned)gy), ROW_THREADS, 0, &a, stream);
 }
 
 }  // extern "C"
