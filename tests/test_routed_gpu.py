@@ -278,6 +278,9 @@ GROUPED = [  # rows of each group, K, N
     ([20, 31], 1000, 2400), ([3, 0, 70, 1] * 66, 264, 250),
     # many groups of a few rows
     ([2, 0, 1, 5] * 11 + [60], 200, 1000), ([1, 3] * 15 + [33, 32], 65, 777), ([4, 1] * 13, 520, 1030),
+    # several rounds of the largest tiles
+    ([2000, 1990], 200, 4100), ([1990, 2055], 321, 4097), ([3, 0, 70, 1] * 16 + [5, 2], 510, 1023),
+    ([64, 1, 0, 130] * 16, 512, 1024),
 ]
 
 
@@ -396,7 +399,7 @@ PAGE_ENDS = [([40, 0, 70], 64, 67), ([64, 128], 128, 129), ([128, 64], 192, 131)
              ([100, 28], 128, 3), ([70], 64, 1), ([33, 30], 65, 7), ([64], 8, 9), ([300, 212], 64, 9001),
              ([300, 200], 72, 6403), ([1100, 948], 71, 8201), ([20, 31], 1000, 1601), ([64, 192], 256, 2401),
              ([3, 0, 70, 1] * 66, 263, 251), ([1, 3] * 15 + [33, 31], 64, 777), ([4, 1] * 13, 521, 1029),
-             ([2, 0, 5] * 20, 192, 1001)]
+             ([2, 0, 5] * 20, 192, 1001), ([2000, 1990], 321, 4099), ([3, 0, 64, 1] * 16 + [5, 2], 511, 1023)]
 
 
 @pytest.mark.parametrize("rows,K,N", PAGE_ENDS)

@@ -74,16 +74,20 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
         if (high < live) high = live;
         return (tn ? groups * tdg::ceil_quot(M, b) : high) * tdg::ceil_quot(N, b);
     };
-    // 256 x 256 needs the fewest bytes per operation, but a workgroup for
-    // every CU, and rows to fill it (us, 256 / 128 / 64 wide): 16384 rows, 16
-    // groups, K = N = 4096: 564 / 668 / 1076; 4096 rows, 32 groups, K = N =
-    // 2048: 102 / 97 / 94.  128 x 128 holds two workgroups per CU with two
-    // buffers, and where there is only one to hold it has four (TN of 16384
-    // rows, 4 groups, 1024 x 1024: 50 / 43).  64 x 64 is for products with few
-    // tiles, the ones of few rows that are bound by reading B among them
-    // (against 128 x 128 with four buffers, 8 rows, 64 groups, K = 2048, N =
-    // 1408: 17 / 11; 500 rows, 4 groups, K = N = 1000: 13 / 9).
-    if (tiles(256) >= 256 && (tn || rows >= 192 * live))
+    const int64_t t256 = tiles(256), t128 = tiles(128);
+    // Rounds of workgroups, in tenths of one of 256 x 256 tiles (256 at a time).
+    // A round of 128 x 128 tiles with two buffers has two for each CU, 512, and
+    // takes 0.6 of that: half the operations at 0.84 of the rate.  A last round
+    // of few large tiles is cut in two (not TN's), and takes 0.7.
+    const int64_t rest = t256 % 256;
+    const int64_t large = t256 / 256 * 10 + (rest == 0 ? 0 : !tn && t256 > 256 && rest <= 128 ? 7 : 10);
+    const int64_t small = tdg::ceil_quot(t128, 512) * 6;
+    // So 256 x 256 where its rounds are the shorter ones and the groups have
+    // the rows for it (us, 256 / 128 wide; NN 4096 rows, 4 groups of 2048 x 2048,
+    // 144 tiles: 49 / 56; of 2048 x 1792, 126 tiles: 47 / 38; TN 14815 rows, 9
+    // groups of 1480 x 1216, 270 tiles: 98 / 85; NN 16384 rows, 16 groups of 4096
+    // x 4096: 564 / 668; 4096 rows, 32 groups of 2048 x 2048: 102 / 97).
+    if (large <= small && (tn || rows >= 192 * live))
         return tn ? Variant{(const void *)&tdg::tdg_grouped_tn_loop<256, 256, 2, 4, 2>, 256, 256, 512, 256}
                   : Variant{lay == tdg::LAY_NN ? (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NN>
                                                : (const void *)&tdg::tdg_grouped_cut<tdg::LAY_NT>,
@@ -95,11 +99,19 @@ Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int6
     // 171; with 16 rows a group too many groups need two: 68 / 52).
     if (lay == tdg::LAY_NN && rows <= 8 * live && live * tdg::ceil_quot(N, 256) >= 128)
         return {(const void *)&tdg::tdg_grouped_ring<tdg::LAY_NN, 32, 256, 1, 4, 4>, 32, 256, 256, INT32_MAX};
-    // NT reads whole rows of B, and a narrow tile more of each at a time (512
-    // rows, 32 groups, 2048 x 2048: 64 wide 58, 128 wide 69; 64 rows: 51 / 55).
-    const bool few_nt = lay == tdg::LAY_NT && rows <= 16 * live;
-    if (tiles(128) > 256 && !few_nt) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256, INT32_MAX};
-    if (tiles(128) >= 192 && !few_nt) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256, INT32_MAX};
+    // Otherwise 64 x 64 for few rows, down to one tile that reads B (8 rows, 64
+    // groups of 2048 x 1408, 64 / 128 wide: 11 / 17), and where NT reads whole
+    // rows of B, a narrow tile more of each at a time (512 rows, 32 groups of
+    // 2048 x 2048: 58 / 69); NN's many groups do better with 128 x 128 (52 / 56).
+    const bool few = !tn && rows <= 16 * live;
+    if (t128 > 256 && !(few && lay == tdg::LAY_NT))
+        return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 2), 128, 128, 256, INT32_MAX};
+    // And 64 x 64, of which a CU holds two, for products that it can do in one
+    // round (64 wide / 128 wide with four buffers, one to a CU: NN 6144 rows, 6
+    // groups of 2048 x 384, 153 large tiles: 24 / 20; 4096 rows, 8 groups, 108:
+    // 16 / 19; TN 16384 rows, 1536 x 1536, 144: 167 / 109; 8192 rows, 8 groups
+    // of 512 x 512, 128: 14 / 16).
+    if (t128 > 128 && !few) return {TDG_BY_LAYOUT(tdg_grouped_ring, 128, 128, 2, 2, 4), 128, 128, 256, INT32_MAX};
     return {TDG_BY_LAYOUT(tdg_grouped_ring, 64, 64, 2, 2, 4), 64, 64, 256, INT32_MAX};
 }
 
