@@ -570,6 +570,8 @@ LORA = [  # M, K, N, adapters, rank, tokens of a request
     (33, 100, 67, 5, 9, 4), (64, 1000, 129, 70, 33, 1), (130, 256, 264, 2, 64, 50), (300, 72, 300, 7, 1, 9),
     (257, 520, 512, 6, 128, 40), (40, 48, 64, 4, 256, 3), (513, 128, 136, 3, 16, 300), (700, 65, 35, 9, 17, 1),
     (12, 0, 24, 2, 4, 2), (9, 64, 32, 0, 8, 1), (9, 64, 32, 3, 0, 1),
+    # more rows: their product cut in K or not
+    (277, 1023, 410, 30, 4, 7), (700, 640, 4100, 5, 20, 40), (4100, 300, 130, 3, 65, 1), (320, 1100, 4090, 9, 33, 3),
 ]
 
 

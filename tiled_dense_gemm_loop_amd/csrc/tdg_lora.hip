@@ -15,10 +15,11 @@
 //     cores, one pass per distinct adapter of the block, added to the
 //     accumulators of that adapter's rows alone: C is written once, and no row
 //     sees another's adapter.
-//   * Few rows: the shared product is bound by reading B, and has too few
-//     tiles to do it at full rate.  Its parts over K are made in the same
-//     launch as low's, and a second (k_lora_join) sums them and adds low . up
-//     in FP32.  The rows are sorted in each workgroup.
+//   * Few rows or few tiles: the shared product is bound by reading B, or by
+//     the latency of its K loop, and has too few tiles to do it at full rate.
+//     Its parts over K are made in the same launch as low's, and a second
+//     (k_lora_join) sums them and adds low . up in FP32.  Up to 256 rows are
+//     sorted in each workgroup, more by k_lora_sort.
 #include "tdg_grouped.hpp"
 
 #include "tdg_check.h"
@@ -33,12 +34,12 @@ struct LoraArgs {
     const int32_t *adapter;
     const float *scale;
     float *C;
-    float *part;  // parts x M x N: the shared product over slices of K (few rows)
+    float *part;  // parts x M x N: the shared product over slices of K (cut in K)
     float *low;   // low_parts x M x rank
     _Float16 *cut;  // M rows of low's high part and rest, rank16 each (many rows)
     int32_t *ex;    // M: their rows' power of two
     int rank16;     // the rank, rounded up to 16
-    int2 *seat;     // M: row and adapter, sorted by adapter (many rows)
+    int2 *seat;     // M: row and adapter, sorted by adapter (more than kFewRows)
     int64_t lda, ldb, ldc, ld_down, stride_down, ld_up, stride_up;  // bytes
     uint64_t a_stop, b_stop, down_stop;  // chunks end at this address or below (chunk_stop)
     int up_apart;  // up's rows' last chunks are loaded element by element
@@ -58,7 +59,8 @@ struct RowsSeated {
     __device__ __forceinline__ int64_t off(int x) const { return (int64_t)seat[x].x * ld; }
 };
 
-// At most this many rows are "few": the key of sort_few holds them in 8 bits.
+// At most this many rows are sorted in each workgroup, and their product is
+// always cut in K: the key of sort_few holds them in 8 bits.
 // (us as few / as many, 8 adapters of rank 64, K x N = 4096 x 4096: 128 rows
 // 28 / 39, 192 rows 34 / 36, 256 rows 38 / 39; 9 of rank 24, 1000 x 5095: 128
 // rows 22 / 27, 192 rows 25 / 25, 256 rows 29 / 27.)
@@ -151,7 +153,7 @@ __device__ __forceinline__ void sort_few(const LoraArgs &p, int32_t *key, int32_
     __syncthreads();
 }
 
-// Tiles of the shared product over a slice of K (few rows only), and of low.
+// Tiles of the shared product over a slice of K (where it is cut), and of low.
 // A tile of low belongs to 64 rows of the sorted order; its workgroups take
 // the distinct adapters among them in turn, each a whole product of which the
 // adapter's own rows are kept.
@@ -581,7 +583,8 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank) {
 
 // How the work is cut; a function of the sizes alone, as the workspace is.
 struct Plan {
-    bool few;             // few rows: parts of the shared product and a join
+    bool cut;             // parts of the shared product over K and a join
+    bool sorted;          // the rows are sorted by a launch of their own
     int64_t parts, k_per_part, low_parts, low_k_per_part;
     uint64_t low_at, cut_at, ex_at, seat_at, bytes;  // workspace: parts, low, its FP16 rows, their powers, the seats
 };
@@ -589,8 +592,14 @@ struct Plan {
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t rank) {
     Plan p = {};
     const int64_t kt = ceil_quot(K, 64);
-    p.few = M <= kFewRows;
-    const int64_t row_tiles = ceil_quot(M, PART_TILE);
+    const int64_t row_tiles = ceil_quot(M, PART_TILE), tiles = row_tiles * ceil_quot(N, 64);
+    p.sorted = M > kFewRows;
+    // More rows are cut too where their tiles leave the chip half empty, with a
+    // short K a little longer (us cut / not cut: 277 rows, 3023 x 410 18 / 46;
+    // 1024 rows, 4096 x 1024 33 / 41; 3946 rows, 3832 x 256 42 / 51; 320 tiles:
+    // 300 rows, 4096 x 4096 46 / 39, 1024 x 4096 23 / 25; 384: 333 rows, 1000 x
+    // 4095 28 / 31; 560: 2179 rows, 704 x 987 44 / 38).
+    p.cut = !p.sorted || tiles <= (kt <= 16 ? 384 : 256);
     auto cut = [&](int64_t tiles, int64_t want, int64_t *parts, int64_t *per) {
         int64_t n = ceil_quot(want, tiles > 0 ? tiles : 1);
         n = n > MAX_PARTS ? MAX_PARTS : n;       // the parts are read again
@@ -599,17 +608,17 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t rank) {
         *per = ceil_quot(kt, n);
         *parts = *per > 0 ? ceil_quot(kt, *per) : 1;
     };
-    if (p.few) cut(row_tiles * ceil_quot(N, 64), 512, &p.parts, &p.k_per_part);
+    if (p.cut) cut(tiles, 512, &p.parts, &p.k_per_part);
     // low has few tiles, and a workgroup of it starts slowly: slices of K as
     // for 512 workgroups, but longer ones where a few tiles hold many adapters.
-    cut(row_tiles * ceil_quot(rank, 64), p.few && row_tiles > 1 ? 4 * row_tiles : 512, &p.low_parts,
+    cut(row_tiles * ceil_quot(rank, 64), !p.sorted && row_tiles > 1 ? 4 * row_tiles : 512, &p.low_parts,
         &p.low_k_per_part);
     auto up16 = [](uint64_t n) { return (n + 15) / 16 * 16; };
-    p.low_at = p.few ? up16((uint64_t)p.parts * M * N * 4) : 0;
+    p.low_at = p.cut ? up16((uint64_t)p.parts * M * N * 4) : 0;
     p.cut_at = p.low_at + up16((uint64_t)p.low_parts * M * rank * 4);
-    p.ex_at = p.cut_at + (p.few ? 0 : (uint64_t)M * 2 * up16(rank) * 2);
-    p.seat_at = p.ex_at + (p.few ? 0 : up16((uint64_t)M * 4));
-    p.bytes = p.seat_at + (p.few ? 0 : up16((uint64_t)M * 8));
+    p.ex_at = p.cut_at + (p.cut ? 0 : (uint64_t)M * 2 * up16(rank) * 2);
+    p.seat_at = p.ex_at + (p.cut ? 0 : up16((uint64_t)M * 4));
+    p.bytes = p.seat_at + (p.sorted ? up16((uint64_t)M * 8) : 0);
     return p;
 }
 
@@ -663,7 +672,7 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     p.part = (float *)workspace, p.low = (float *)((unsigned char *)workspace + plan.low_at);
     p.cut = (_Float16 *)((unsigned char *)workspace + plan.cut_at);
     p.ex = (int32_t *)((unsigned char *)workspace + plan.ex_at);
-    p.seat = plan.few ? nullptr : (int2 *)((unsigned char *)workspace + plan.seat_at);
+    p.seat = plan.sorted ? (int2 *)((unsigned char *)workspace + plan.seat_at) : nullptr;
     p.rank16 = (int)((rank + 15) / 16 * 16);
     p.lda = lda * 2, p.ldb = ldb * 2, p.ldc = ldc * 4;
     p.ld_down = ld_down * 2, p.stride_down = stride_down * 2, p.ld_up = ld_up * 2, p.stride_up = stride_up * 2;
@@ -693,7 +702,7 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     const int64_t low_wgs = ceil_quot(low_tiles * plan.low_parts * p.low_cols * p.low_lanes, 8) * 8;
     const void *main_fn = nullptr, *join_fn = nullptr;
     int bm = PART_TILE, bn = PART_TILE, main_threads = 256, join_v = 1;
-    if (plan.few) {
+    if (plan.cut) {
         // (4 columns a thread: 4 x 4096 x 4096 with adapters of rank 64 20.8 us,
         // 128 rows 29.1; 2: 19.9 and 28.1.)
         join_v = N > 1 ? 2 : 1;
@@ -720,22 +729,21 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     const int64_t join_y = ceil_quot(N, (int64_t)JOIN_THREADS * join_v);
     // HIP counts a launch's threads in 32 bits (row_tiles * col_tiles fits 64).
     auto grid_ok = [](int64_t wgs, int64_t threads) { return wgs <= (int64_t)UINT32_MAX / threads; };
-    const int64_t tiles = ceil_quot(row_tiles * col_tiles * (plan.few ? plan.parts : 1), 8) * 8;
-    const int64_t parts_wgs = low_wgs + (plan.few ? tiles : 0), split_wgs = ceil_quot(M, SPLIT_THREADS / 64);
-    if (!grid_ok(parts_wgs, 256) || !grid_ok(tiles, main_threads) || (!plan.few && !grid_ok(split_wgs, SPLIT_THREADS)) ||
-        (plan.few && (join_y > 65535 || !grid_ok(M * join_y, JOIN_THREADS))))
+    const int64_t tiles = ceil_quot(row_tiles * col_tiles * (plan.cut ? plan.parts : 1), 8) * 8;
+    const int64_t parts_wgs = low_wgs + (plan.cut ? tiles : 0), split_wgs = ceil_quot(M, SPLIT_THREADS / 64);
+    if (!grid_ok(parts_wgs, 256) || !grid_ok(tiles, main_threads) || (!plan.cut && !grid_ok(split_wgs, SPLIT_THREADS)) ||
+        (plan.cut && (join_y > 65535 || !grid_ok(M * join_y, JOIN_THREADS))))
         return TDG_ERR_UNSUPPORTED;
     p.low_wgs = (int)low_wgs, p.row_tiles = (int)row_tiles, p.col_tiles = (int)col_tiles;
     rc = device_check();
     if (rc != TDG_OK) return rc;
     const void *parts_fn = ring ? (const void *)&k_lora_parts_ring : (const void *)&k_lora_parts_any;
-    if (plan.few) {
-        rc = launch(parts_fn, dim3((unsigned)parts_wgs), 256, &p, stream);
+    if (plan.sorted)
+        rc = launch((const void *)&k_lora_sort, dim3((unsigned)ceil_quot(M, SORT_ROWS)), SORT_THREADS, &p, stream);
+    if (rc == TDG_OK) rc = launch(parts_fn, dim3((unsigned)parts_wgs), 256, &p, stream);
+    if (plan.cut)
         return rc != TDG_OK ? rc
                             : launch(join_fn, dim3((unsigned)M, (unsigned)join_y), JOIN_THREADS, &p, stream);
-    }
-    rc = launch((const void *)&k_lora_sort, dim3((unsigned)ceil_quot(M, SORT_ROWS)), SORT_THREADS, &p, stream);
-    if (rc == TDG_OK) rc = launch(parts_fn, dim3((unsigned)parts_wgs), 256, &p, stream);
     if (rc == TDG_OK) rc = launch((const void *)&k_lora_split, dim3((unsigned)split_wgs), SPLIT_THREADS, &p, stream);
     return rc != TDG_OK ? rc : launch(main_fn, dim3((unsigned)tiles), main_threads, &p, stream);
 }
