@@ -424,7 +424,8 @@ def test_grouped_tiles_at_a_page_end(lib, rows, K, N, pad):
 
 @pytest.mark.parametrize("M,K,N,rank", [(3, 64, 67, 8), (20, 128, 129, 9), (70, 192, 131, 33), (256, 65, 7, 3),
                                         (300, 64, 129, 16), (257, 128, 3, 1), (400, 72, 1001, 40), (600, 130, 5001, 9),
-                                        (1100, 64, 6601, 17), (1100, 71, 6603, 65)])
+                                        (1100, 64, 6601, 17), (1100, 71, 6603, 65), (700, 64, 2305, 17),
+                                        (700, 71, 2303, 65)])
 @pytest.mark.parametrize("pad", [0, 3, 8])
 def test_lora_tiles_at_a_page_end(lib, M, K, N, rank, pad):
     r = rng(30, M, K, pad)
@@ -615,10 +616,11 @@ def test_lora(lib, M, K, N, n, rank, run, pad, skip, gap, scaled):
 
 
 @pytest.mark.parametrize("M,run", [(24, 1), (300, 7), (600, 200)])
-def test_adapters_do_not_touch_each_other(lib, M, run):
+@pytest.mark.parametrize("N", [160, 4100])
+def test_adapters_do_not_touch_each_other(lib, M, N, run):
     """NaN in one adapter, infinities in another: only their rows see them."""
     r = rng(14, M)
-    K, N, n, rank = 96, 160, 4, 16
+    K, n, rank = 96, 4, 16
     a, b = normal(r, M, K), normal(r, K, N)
     down, up = normal(r, n, K, rank), normal(r, n, rank, N)
     pick = torch.from_numpy(np.repeat(r.integers(-1, n, -(-M // run)), run)[:M]).to(torch.int32)
@@ -637,10 +639,11 @@ def test_adapters_do_not_touch_each_other(lib, M, run):
 
 @pytest.mark.parametrize("M,far", [(5, 8388352), (200, 8388352), (255, 8388352), (256, 8388352), (5, 9000000),
                                    (200, 9000000), (600, 9000000), (1000, 2147483), (1000, 2147484)])
-def test_lora_operands_far_apart(lib, M, far):
+@pytest.mark.parametrize("N", [56, 3000])
+def test_lora_operands_far_apart(lib, M, N, far):
     """Leading dimensions around and past what a lane's 32-bit offsets reach."""
     r = rng(24, M)
-    K, N, n, rank = 40, 56, 2, 6
+    K, n, rank = 40, 2, 6
     a, b, down, up = whole(r, M, K, most=2), whole(r, K, N), whole(r, n, K, rank, most=1), whole(r, n, rank, N)
     pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
     want, _, _ = lora64(a, b, down, up, pick, None)
@@ -668,15 +671,17 @@ def test_lora_few_columns(lib, M):
         assert (buf[:, 0] == -7.0).all() and (buf[:, N + 1:] == -7.0).all()
 
 
-def test_lora_many_adapters_and_one_workspace(lib):
+@pytest.mark.parametrize("N", [72, 200])
+def test_lora_many_adapters_and_one_workspace(lib, N):
     """More adapters than the sort has counters, rows over several of its
     blocks, and one workspace for calls of different sizes on one stream."""
     r = rng(25)
-    K, N, n, rank = 48, 72, 3000, 8
+    K, n, rank = 48, 3000, 8
     down, up = whole(r, n, K, rank, most=1), whole(r, n, rank, N, most=2)
     b = whole(r, K, N)
-    ws = torch.empty(lib.tdg_lora_workspace(9000, N, K, n, rank), dtype=torch.uint8, device="cuda")
-    for M in (9000, 300, 100, 4097, 20):
+    rows = (9000, 300, 100, 4097, 20)
+    ws = torch.empty(max(lib.tdg_lora_workspace(M, N, K, n, rank) for M in rows), dtype=torch.uint8, device="cuda")
+    for M in rows:
         a = whole(r, M, K, most=2)
         pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
         x, at = a.double(), pick.clamp(min=0).long()
@@ -686,13 +691,13 @@ def test_lora_many_adapters_and_one_workspace(lib):
         near(got, want, torch.zeros_like(want))
 
 
-@pytest.mark.parametrize("M", [3, 400])
+@pytest.mark.parametrize("M,N", [(3, 96), (400, 96), (400, 4000), (1000, 4000), (2200, 3900)])
 @pytest.mark.parametrize("size", [2.0 ** -20, 1.0, 2.0 ** 14])
-def test_lora_low_products_of_any_size(lib, M, size):
+def test_lora_low_products_of_any_size(lib, M, N, size):
     """A . down beyond FP16's range on both sides keeps its bits: rows of very
     different sizes, with whole numbers small enough to be exact."""
     r = rng(15, M)
-    K, N, n, rank = 64, 96, 2, 8
+    K, n, rank = 64, 2, 8
     a = whole(r, M, K, most=2).float()
     a[::2] *= 256.0
     a = a.to(F16)
@@ -824,12 +829,12 @@ def test_no_large_tile_is_read_before_it_lands(lib, rows, K, N):
 
 def test_lora_in_a_graph(lib):
     r = rng(18)
-    for M in (4, 300):
-        a, b = normal(r, M, 128).cuda(), normal(r, 128, 96).cuda()
-        down, up = normal(r, 3, 128, 8).cuda(), normal(r, 3, 8, 96).cuda()
+    for M, N in ((4, 96), (300, 96), (500, 4096)):
+        a, b = normal(r, M, 128).cuda(), normal(r, 128, N).cuda()
+        down, up = normal(r, 3, 128, 8).cuda(), normal(r, 3, 8, N).cuda()
         pick = torch.from_numpy(r.integers(-1, 3, M)).to(torch.int32).cuda()
-        ws = torch.empty(lib.tdg_lora_workspace(M, 96, 128, 3, 8), dtype=torch.uint8, device="cuda")
-        C = torch.empty(M, 96, device="cuda")
+        ws = torch.empty(lib.tdg_lora_workspace(M, N, 128, 3, 8), dtype=torch.uint8, device="cuda")
+        C = torch.empty(M, N, device="cuda")
         lib.gemm_f16f32_lora(a, b, down, up, pick, C=C, workspace=ws)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()

@@ -879,7 +879,8 @@ def gemm_f16f32_grouped_tn(A, B, offsets, C=None):
 
 
 def tdg_lora_workspace(M: int, N: int, K: int, adapters: int, rank: int) -> int:
-    """Bytes of workspace that gemm_f16f32_lora needs."""
+    """Bytes of workspace that gemm_f16f32_lora needs (not growing with M
+    throughout: for several sizes take the largest)."""
     need = ctypes.c_size_t()
     rc = _fn("tdg_lora_workspace")(M, N, K, adapters, rank, ctypes.byref(need))
     if rc != TDG_OK:
