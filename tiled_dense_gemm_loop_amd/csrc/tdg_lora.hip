@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) k_lora_main_any(LoraArgs p) {
     lora_main<E, BM, BN, WM, WN>(p, smem);
 }
 
-// The second launch for few rows: C[t][n] = the shared product's parts, in
+// The last launch where the product is cut in K: C[t][n] = its parts, in
 // order, plus scale * sum_c low[t][c] * up[c][n].  A workgroup has one row, a
 // thread V <= N of its columns; where V does not divide N the last thread's
 // begin earlier, and it and the one before make the same values for those that
