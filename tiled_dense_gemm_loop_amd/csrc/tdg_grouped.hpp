@@ -466,21 +466,9 @@ struct GroupedRing {
             uint64_t p;
             const bool in = chunk_of(kt, d, p) && p + 16 <= (d < CA ? a_stop : b_stop);
             const uint64_t src = in ? p : (uint64_t)(uintptr_t)tdg_zero16;
-            asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+            copy_to_lds(src, m0);
         } else {
-            // The base may have been written to its scalar registers by a
-            // vector instruction just before (v_readlane, where the compiler
-            // reloads spilled ones).  A vector-memory instruction may read
-            // them five wait states later at the earliest, which the compiler
-            // does not count for inline assembly; a scalar one may read them
-            // at once, and what it writes is safe.
-            const unsigned char *base = base_of(kt, d);
-            const uint32_t off = off_of(d);
-            uint64_t safe;
-            asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
-                         : "=&s"(safe)
-                         : "v"(off), "s"(base), "{m0}"(m0)
-                         : "memory");
+            copy_to_lds(base_of(kt, d), off_of(d), m0);
         }
     }
 

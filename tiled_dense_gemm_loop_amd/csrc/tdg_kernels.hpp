@@ -249,6 +249,24 @@ __device__ static __forceinline__ u32x4 load16_global(const unsigned char *p) {
     return *(const __attribute__((address_space(1))) u32x4_ua *)p;
 }
 
+// Copies 16 bytes per lane from global memory to LDS (global_load_lds_dwordx4),
+// from any byte address: lane l's land at the LDS address m0 + 16 l.  Inline
+// assembly, for which the compiler adds no waits, so they stand here: a copy
+// may read M0 one wait state after a scalar instruction has written it, and a
+// scalar base five after a vector instruction has (v_readlane, where the
+// compiler reloads spilled registers).  A scalar instruction may read the base
+// at once, and what it writes is safe; it also spaces M0 from the copy.
+__device__ static __forceinline__ void copy_to_lds(uint64_t src, uint32_t m0) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+__device__ static __forceinline__ void copy_to_lds(const unsigned char *base, uint32_t off, uint32_t m0) {
+    uint64_t safe;
+    asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+                 : "=&s"(safe)
+                 : "v"(off), "s"(base), "{m0}"(m0)
+                 : "memory");
+}
+
 // One bounds-checked 16-byte chunk of a register-staged tile.  Rows outside
 // the operand (A rows >= M, B rows k >= K) and, with ZERO_TAIL, elements at
 // and beyond `valid` must read as zero: a k >= K would add to every sum.
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) tdg_gemm_kernel(GemmArgs args
                 src = ok ? p : zero_addr;
                 m0v = wbase + (uint32_t)(G::A_BYTES + i * G::NT * 16);
             }
-            asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0v) : "memory");
+            copy_to_lds(src, m0v);
             return;
         }
         // the tile index is wave-uniform; the bounds-checked kernels' uniformity
@@ -583,15 +601,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) tdg_gemm_kernel(GemmArgs args
         if constexpr (GUARD) kt = __builtin_amdgcn_readfirstlane(kt);
         if (d < G::CA) {
             const uint32_t m0v = wbase + (uint32_t)(d * G::NT * 16);
-            asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(a_voff), "s"(a_ptr(kt, d)),
-                         "{m0}"(m0v)
-                         : "memory");
+            copy_to_lds(a_ptr(kt, d), a_voff, m0v);
         } else {
             const int i = d - G::CA;
             const uint32_t m0v = wbase + (uint32_t)(G::A_BYTES + i * G::NT * 16);
-            asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(b_voff), "s"(b_ptr(kt, i)),
-                         "{m0}"(m0v)
-                         : "memory");
+            copy_to_lds(b_ptr(kt, i), b_voff, m0v);
         }
     };
     auto issue_direct = [&](uint32_t st_off, int kt, auto checked) __attribute__((always_inline)) {
