@@ -501,8 +501,8 @@ int gemm_f16f32_grouped_tn(int64_t groups, const int32_t *offsets, int64_t rows,
  * a = adapter[t]; a row whose a lies outside [0, adapters) (say -1) gets the
  * shared product alone, and no row is touched by another's adapter.
  * down[a] is K x rank at down + a * stride_down, up[a] rank x N at
- * up + a * stride_up; scale may be NULL (1 for all); A . down is kept to at
- * least 21 bits.  0 <= rank <= TDG_LORA_MAX_RANK.  The workspace
+ * up + a * stride_up; scale may be NULL (1 for all); every element of A . down
+ * is kept to at least 21 bits.  0 <= rank <= TDG_LORA_MAX_RANK.  The workspace
  * (tdg_lora_workspace) is 16-byte aligned; its contents on return are
  * unspecified.  Its size does not grow with M throughout: one for calls of
  * several sizes is as large as the largest that they need.  Elements of up are

@@ -709,6 +709,72 @@ def test_lora_low_products_of_any_size(lib, M, N, size):
     near(got, want, torch.zeros_like(want))
 
 
+# few rows; many rows cut in K; and each of the tiles that add low . up
+LOW_SHAPES = [(3, 96), (400, 96), (400, 4000), (1000, 4000), (2200, 3900)]
+
+
+def columns_of_any_size(r, K, n, rank, first, last):
+    """down and up of whole numbers, down's columns scaled by powers of two
+    from 2^first to 2^last and up's rows so that products are multiples of
+    2^-10."""
+    size = torch.tensor([2.0 ** round(first + (last - first) * c / (rank - 1)) for c in range(rank)])
+    down = whole(r, n, K, rank, most=1).float() * size
+    up = whole(r, n, rank, 1, most=1).float() / size[:, None] / 1024
+    assert down.abs().max() < 65504 and up.abs().max() < 65504 / 2
+    return down.to(F16), up.to(F16)
+
+
+@pytest.mark.parametrize("M,N", LOW_SHAPES)
+@pytest.mark.parametrize("first,last", [(0, -20), (-18, 14), (14, -24)])
+def test_lora_elements_of_any_size_in_a_row(lib, M, N, first, last):
+    """A . down's elements of one row up to 2^52 apart, and an up that brings
+    them back to one size: none is lost.  Multiples of 2^-10 below 2^14, so
+    every sum is exact."""
+    r = rng(31, M)
+    K, n, rank = 64, 3, 8
+    a = whole(r, M, K, most=1000 if first == 14 else 2)
+    a[:, ::2] = 0
+    if first == 14:  # rows without the largest element too
+        a[::3, :32] = 0
+    b = torch.zeros(K, N, dtype=F16)
+    down, up = columns_of_any_size(r, K, n, rank, first, last)
+    down[:, 32:, 0] = 0
+    up = up.expand(n, rank, N).contiguous() * (1 + torch.from_numpy(r.integers(0, 2, (n, 1, N)))).to(F16)
+    pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
+    want, _, _ = lora64(a, b, down, up, pick, None)
+    got = lib.gemm_f16f32_lora(a.cuda(), b.cuda(), down.cuda(), up.cuda(), pick.cuda())
+    near(got, want, torch.zeros_like(want))
+
+
+@pytest.mark.parametrize("M,N", LOW_SHAPES)
+@pytest.mark.parametrize("rank", [5, 64, 130])
+def test_lora_of_any_size_within_its_bound(lib, M, N, rank):
+    """The same with no whole numbers, ranks of several blocks and a shared
+    product: each element of A . down keeps its 21 bits.  And a row's value
+    does not depend on the rows beside it, whichever way they are computed."""
+    r = rng(32, M, rank)
+    K, n = 100, 3
+    a, b = normal(r, M, K), normal(r, K, N, scale=2.0 ** -14)
+    a[::3, 0] = 0  # rows without the large elements of column 0
+    size = torch.from_numpy(2.0 ** r.integers(-14, 8, rank))
+    down = (normal(r, n, K, rank, dtype=torch.float64) * size / size.max()).to(F16)
+    up = (normal(r, n, rank, N, dtype=torch.float64) / size[:, None] * 2.0 ** -2).to(F16)
+    assert torch.isfinite(up).all()
+    down[:, :, 0] = 0
+    down[:, 0, 0] = 60000.0
+    up[:, 0] = 0
+    pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
+    scale = normal(r, n, dtype=F32)
+    want, mag, side = lora64(a, b, down, up, pick, scale)
+    args = (b.cuda(), down.cuda(), up.cuda())
+    got = lib.gemm_f16f32_lora(a.cuda(), *args, pick.cuda(), scale.cuda())
+    near(got, want, (K + 2) * U2 * mag + side + want.abs() * 2 * U2)
+    other = a.clone()
+    other[::2] = normal(r, other[::2].shape[0], K)
+    again = lib.gemm_f16f32_lora(other.cuda(), *args, pick.cuda(), scale.cuda())
+    assert torch.equal(again[1::2], got[1::2])
+
+
 # ------------------------------------------------------------------ together
 
 def layer_on(lib, x, ids, w, w1, w2, dy):

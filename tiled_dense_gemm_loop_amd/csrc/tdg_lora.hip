@@ -9,12 +9,13 @@
 // first, so that there are few.
 //   * Many rows: k_lora_sort sorts each 4096 rows; k_lora_parts_* makes low;
 //     k_lora_split sums its parts and cuts each row into two FP16 rows, high
-//     and rest, scaled by a power of two to just under 2^14: 21 bits or more
-//     at any size.  k_lora_main_* then makes the shared product's tiles over
-//     the sorted rows, and on each wave's 32-row blocks low . up on the matrix
-//     cores, one pass per distinct adapter of the block, added to the
-//     accumulators of that adapter's rows alone: C is written once, and no row
-//     sees another's adapter.
+//     and rest: 21 bits or more of every element.  k_lora_main_* then makes the
+//     shared product's tiles over the sorted rows, and on each wave's 32-row
+//     blocks low . up on the matrix cores, one pass per distinct adapter of the
+//     block, added to the accumulators of that adapter's rows alone: C is
+//     written once, and no row sees another's adapter.  A row whose elements
+//     differ too much in size for two FP16 rows takes its sums from an FP32
+//     product instead.
 //   * Few rows or few tiles: the shared product is bound by reading B, or by
 //     the latency of its K loop, and has too few tiles to do it at full rate.
 //     Its parts over K are made in the same launch as low's, and a second
@@ -35,9 +36,9 @@ struct LoraArgs {
     const float *scale;
     float *C;
     float *part;  // parts x M x N: the shared product over slices of K (cut in K)
-    float *low;   // low_parts x M x rank
+    float *low;   // low_parts x M x rank; many rows: k_lora_split leaves their sum in the first
     _Float16 *cut;  // M rows of low's high part and rest, rank16 each (many rows)
-    int32_t *ex;    // M: their rows' power of two
+    int32_t *ex;    // M: their rows' power of two, or kWide
     int rank16;     // the rank, rounded up to 16
     int2 *seat;     // M: row and adapter, sorted by adapter (more than kFewRows)
     int64_t lda, ldb, ldc, ld_down, stride_down, ld_up, stride_up;  // bytes
@@ -247,9 +248,14 @@ __global__ void __launch_bounds__(256, 1) k_lora_parts_any(LoraArgs p) {
 
 // Between the launches for many rows: a wave per row sums low's parts, finds
 // the row's largest finite magnitude and writes the row as two FP16 rows,
-// x 2^-ex = high + rest, |x 2^-ex| < 2^14.  A value that is not finite goes
-// into the high part alone.
+// x 2^-ex = high + rest 2^-12 with |x 2^-ex| < 2^14.  Their products are summed
+// apart, so that rest has a grid of its own: an element down to about 2^-30 of
+// the row's largest keeps 21 bits or more.  A row with one that does not (or
+// with one that is not finite) is marked kWide, and its sums come from FP32
+// products of the row as it is, which is left where the first part was.
 constexpr int SPLIT_THREADS = 256;
+constexpr float REST_SIZE = 4096.0f;
+constexpr int32_t kWide = INT32_MAX;
 __global__ void __launch_bounds__(SPLIT_THREADS) k_lora_split(LoraArgs p) {
     const int row = blockIdx.x * (SPLIT_THREADS / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (row >= p.M || adapter_of(p, row) < 0) return;
@@ -275,16 +281,27 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_lora_split(LoraArgs p) {
     }
     for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
     const int ex = most > 0.0f ? ilogbf(most) - 13 : 0;
-    if (lane == 0) p.ex[row] = ex;
     _Float16 *hi = p.cut + (int64_t)row * 2 * p.rank16, *rest = hi + p.rank16;
+    bool kept = true;
 #pragma unroll
     for (int q = 0; q < PER; q++) {
         const int c = q * 64 + lane;
         if (c >= p.rank16) break;
         const float v = ldexpf(x[q], -ex);
         const _Float16 h = (_Float16)v;
+        const float left = (v - (float)h) * REST_SIZE;
+        const _Float16 r = (_Float16)left;
         hi[c] = h;
-        rest[c] = fabsf(v) <= 65504.0f ? (_Float16)(v - (float)h) : (_Float16)0.0f;
+        rest[c] = r;
+        // |v - high - rest 2^-12| <= 2^-21 |v|, and v not rounded to 0 (never
+        // so for what is not finite)
+        kept &= fabsf(left - (float)r) <= fabsf(v) * (REST_SIZE * 0x1p-21f) && (v != 0.0f || x[q] == 0.0f);
+        if (c < p.rank && p.low_parts > 1) p.low[(int64_t)row * p.rank + c] = x[q];
+    }
+    if (__ballot(!kept)) {
+        if (lane == 0) p.ex[row] = kWide;
+    } else if (lane == 0) {
+        p.ex[row] = ex;
     }
 }
 
@@ -308,6 +325,7 @@ struct TileRows {
 // LDS of its own, one distinct adapter of its 32-row block after the other.
 // The wave's rows begin at r0, its columns at col0.  Chunks of up are read whole,
 // as the DMA reads those of B, unless one of them would leave up's last page.
+// Rows marked kWide are left to add_wide_rows.
 template <int MI, int NI, int BM, int WAVES>
 __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
                                              unsigned char *smem, f32x16 (&acc)[MI][NI]) {
@@ -365,7 +383,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
         u32x4 v[PER];
 #pragma unroll
         for (int i = 0; i < PER; i++) {
-            const int q = i * WAVES * 64 + tid, part = q / IL::CHUNKS, r = q / IL::CPR % BM;
+            const int q = i * WAVES * 64 + thread_again(), part = q / IL::CHUNKS, r = q / IL::CPR % BM;
             const int c = c0 + ((q % IL::CPR) ^ IL::swz(r)) * 8;
             // rows without an adapter read what is there: their sums are not used
             const _Float16 *src = p.cut + ((int64_t)rows.row[r] * 2 + part) * p.rank16 + c;
@@ -378,9 +396,12 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
 #pragma unroll
         for (int mi = 0; mi < MI; mi++) {
             const int at = r0 + mi * 32;
+            // (offsets made anew for each block leave the registers to the sums)
+            const int lane = thread_again() & 63;
             const int id = rows.id[at + (lane & 31)];
             uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
             if (!left) continue;
+            const uint32_t wide = (uint32_t)__ballot(id >= 0 && rows.ex[at + (lane & 31)] == kWide);
             int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
             if (early && MI > 1 && staged != a && loaded != a) load_up(a, 0, u);  // (one block: loaded above)
             for (;;) {
@@ -403,9 +424,10 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                 if (early && next != a) load_up(next, 0, u);
                 loaded = -1;
                 const float scale = p.scale ? p.scale[a] : 1.0f;
-                f32x16 sum[NI];
+                const uint32_t fit = mine & ~wide;
+                f32x16 sum[NI], fine[NI];  // of high, and of rest
 #pragma unroll
-                for (int ni = 0; ni < NI; ni++) sum[ni] = f32x16{};
+                for (int ni = 0; ni < NI; ni++) sum[ni] = fine[ni] = f32x16{};
 #pragma unroll
                 for (int s = 0; s < 4; s++) {
                     if (c0 + s * 16 >= p.rank) break;
@@ -414,7 +436,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                     for (int ni = 0; ni < NI; ni++) {
                         const u32x4 b = IU::read(up_at, lane, ni * 32, s);
                         sum[ni] = Mfma<DT_F16>::mac_sub(hi, b, sum[ni], 0);
-                        sum[ni] = Mfma<DT_F16>::mac_sub(rest, b, sum[ni], 0);
+                        fine[ni] = Mfma<DT_F16>::mac_sub(rest, b, fine[ni], 0);
                     }
                 }
                 __builtin_amdgcn_wave_barrier();
@@ -425,17 +447,69 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                     const i32x4 e = *(const i32x4 *)&rows.ex[at + r];
 #pragma unroll
                     for (int w = 0; w < 4; w++) {
-                        const bool on = (mine >> (r + w)) & 1;
+                        const bool on = (fit >> (r + w)) & 1;
 #pragma unroll
                         for (int ni = 0; ni < NI; ni++) {
                             const float c = acc[mi][ni][q * 4 + w];
-                            const float more = c + scale * ldexpf(sum[ni][q * 4 + w], e[w]);
+                            const float x = fmaf(fine[ni][q * 4 + w], 1.0f / REST_SIZE, sum[ni][q * 4 + w]);
+                            const float more = c + scale * ldexpf(x, e[w]);
                             acc[mi][ni][q * 4 + w] = on ? more : c;
                         }
                     }
                 }
                 if (!left) break;
                 a = next;
+            }
+        }
+    }
+}
+
+// C += scale * low . up for the wave's rows that are marked kWide, once the
+// rest of C is stored: v_mfma_f32_32x32x2_f32 on low as it is, one distinct
+// adapter of each 32-row block after the other, its up straight from memory.
+// Each lane adds to elements that it has stored itself.  Few rows come here, so
+// it is kept small rather than fast, and outside the registers and the
+// instructions of all others (4096 rows, K = N = 4096, rank 64: 154 us with no
+// such row, 165 with one in 500, 256 with all).  A row's sums depend on the row and its adapter
+// alone, and so does whether they come from here: its values are the same
+// whatever block it lies in.
+template <int MI, int NI, int BM>
+__device__ __forceinline__ void add_wide_rows(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll 1
+    for (int at = r0; at < r0 + MI * 32; at += 32) {
+        const int id = rows.ex[at + (lane & 31)] == kWide ? rows.id[at + (lane & 31)] : -1;
+        const float *low = p.low + (int64_t)rows.row[at + (lane & 31)] * p.rank;
+        uint32_t left = (uint32_t)__ballot(id >= 0);
+#pragma unroll 1
+        while (left) {
+            const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
+            const uint32_t mine = (uint32_t)__ballot(id == a);
+            left &= ~mine;
+            const float scale = p.scale ? p.scale[a] : 1.0f;
+#pragma unroll 1
+            for (int ni = 0; ni < NI && col0 + ni * 32 < p.N; ni++) {
+                const int col = col0 + ni * 32 + (lane & 31);
+                const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col * 2;
+                f32x16 sum = {};
+#pragma unroll 1
+                for (int c0 = 0; c0 < p.rank; c0 += 8) {
+                    // the lane's four of the step's eight k: the same for both operands
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int c = c0 + (lane >> 5) * 4 + i;
+                        const float x = c < p.rank ? low[c] : 0.0f;
+                        const float u = c < p.rank && col < p.N ? (float)*(const _Float16 *)(up + (int64_t)c * p.ld_up) : 0.0f;
+                        sum = __builtin_amdgcn_mfma_f32_32x32x2f32(x, u, sum, 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 16; v++) {
+                    const int r = (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+                    if (!((mine >> r) & 1) || col >= p.N) continue;
+                    float *dst = (float *)((unsigned char *)p.C + (int64_t)rows.row[at + r] * p.ldc) + col;
+                    *dst += scale * sum[v];
+                }
             }
         }
     }
@@ -489,6 +563,7 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     if (inside && lines) store(std::false_type{}, std::true_type{});
     else if (inside) store(std::false_type{}, std::false_type{});
     else store(std::true_type{}, std::false_type{});
+    add_wide_rows<E::MI, E::NI>(p, rows, r0, col0);
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
