@@ -505,8 +505,7 @@ int gemm_f16f32_grouped_tn(int64_t groups, const int32_t *offsets, int64_t rows,
  * is kept to at least 21 bits.  0 <= rank <= TDG_LORA_MAX_RANK.  The workspace
  * (tdg_lora_workspace) is 16-byte aligned; its contents on return are
  * unspecified.  Its size does not grow with M throughout: one for calls of
- * several sizes is as large as the largest that they need.  Elements of up are
- * finite: an infinity gives infinities or NaN in the rows of its adapter. */
+ * several sizes is as large as the largest that they need. */
 #define TDG_LORA_MAX_RANK 256
 int tdg_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank, size_t *bytes);
 int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda, const uint16_t *B,

@@ -775,6 +775,33 @@ def test_lora_of_any_size_within_its_bound(lib, M, N, rank):
     assert torch.equal(again[1::2], got[1::2])
 
 
+@pytest.mark.parametrize("M,N", LOW_SHAPES + [(2200, 3901)])
+@pytest.mark.parametrize("rank", [3, 70])
+def test_lora_infinities_and_nan(lib, M, N, rank):
+    """Infinities and NaN in up and down give the definition's infinities and
+    NaN, the same for few rows and many, in their own columns and rows alone."""
+    r = rng(33, M, rank)
+    K, n = 40, 4
+    a, b = whole(r, M, K, most=2), whole(r, K, N)
+    down, up = whole(r, n, K, rank, most=1), whole(r, n, rank, N, most=2)
+    for e, c, at, x in ((0, 0, 5, float("inf")), (0, rank - 1, 5, float("-inf")), (0, 1, 6, float("-inf")),
+                        (1, rank - 1, N - 1, float("inf")), (1, 2, 40, float("nan")), (1, 0, 41, float("inf"))):
+        up[e, c, at] = x
+    down[2, 7, 1], down[2, 8, 2] = float("inf"), float("-inf")
+    pick = torch.from_numpy(r.integers(-1, n, M)).to(torch.int32)
+    scale = torch.tensor([1.0, -2.0, 0.5, 0.0])
+    want = a.double() @ b.double()
+    for t in range(M):
+        e = int(pick[t])
+        if e >= 0:
+            low = (a[t].double()[:, None] * down[e].double()).sum(dim=0)
+            want[t] += float(scale[e]) * (low[:, None] * up[e].double()).sum(dim=0)
+    got = lib.gemm_f16f32_lora(a.cuda(), b.cuda(), down.cuda(), up.cuda(), pick.cuda(), scale.cuda()).cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    there = ~torch.isnan(want)
+    assert torch.isinf(want).any() and torch.equal(got[there], want[there])
+
+
 # ------------------------------------------------------------------ together
 
 def layer_on(lib, x, ids, w, w1, w2, dy):

@@ -325,14 +325,26 @@ struct TileRows {
 // LDS of its own, one distinct adapter of its 32-row block after the other.
 // The wave's rows begin at r0, its columns at col0.  Chunks of up are read whole,
 // as the DMA reads those of B, unless one of them would leave up's last page.
-// Rows marked kWide are left to add_wide_rows.
+// Rows marked kWide are left to add_exact, and elements whose column of up holds
+// an infinity or NaN (the parts' products with it are not low's).  Returns which
+// of the wave's 32-row blocks have such (the bits of `odd`).
 template <int MI, int NI, int BM, int WAVES>
-__device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
+__device__ __forceinline__ uint32_t add_adapters(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
                                              unsigned char *smem, f32x16 (&acc)[MI][NI]) {
     typedef Image<true, BM> IL;        // the tile's rows by 64 of the rank
     typedef Image<false, NI * 32> IU;  // 64 of the rank by the wave's columns
     const int tid = thread_again(), lane = tid & 63;
     unsigned char *up_at = smem + 2 * IL::BYTES + (tid >> 6) * IU::BYTES;
+    uint32_t odd = 0;    // bits mi, mi + 16: the wave's block mi has such rows, such elements
+    float probe = 0.0f;  // NaN: what the lane has staged of up is not all finite
+    auto look_at = [&](const u32x4 &v) __attribute__((always_inline)) {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t word = v[i];
+            probe = __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, word), h2{0, 0}, probe, false);
+        }
+    };
     for (int c0 = 0; c0 < p.rank; c0 += 64) {
         if (c0) __syncthreads();  // every wave is done with the block before
         // Chunks of up[a]'s rows c0 + q / CPR: U of them per lane at a time.
@@ -354,13 +366,18 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
         };
         auto store_up = [&](int a, int q0, const u32x4 (&u)[U]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < U; i++) lds_write16(up_at + (q0 + i * 64 + lane) * 16, u[i]);
+            for (int i = 0; i < U; i++) {
+                lds_write16(up_at + (q0 + i * 64 + lane) * 16, u[i]);
+                look_at(u[i]);
+            }
             if (up_on && !up_whole) {  // (zeros so far)
 #pragma unroll 1
                 for (int q = q0; q < q0 + U * 64; q += 64) {
                     const int r = c0 + q / IU::CPR + up_r;
                     const unsigned char *src = p.up + (int64_t)a * p.stride_up + (int64_t)r * p.ld_up;
-                    lds_write16(up_at + (q + lane) * 16, load_chunk(src, r < p.rank, col0 + up_c, p.N));
+                    const u32x4 v = load_chunk(src, r < p.rank, col0 + up_c, p.N);
+                    lds_write16(up_at + (q + lane) * 16, v);
+                    look_at(v);
                 }
             }
         };
@@ -402,12 +419,14 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
             uint32_t left = (uint32_t)__ballot(id >= 0);  // both halves of the wave hold the same rows
             if (!left) continue;
             const uint32_t wide = (uint32_t)__ballot(id >= 0 && rows.ex[at + (lane & 31)] == kWide);
+            if (wide) odd |= 1u << mi;
             int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
             if (early && MI > 1 && staged != a && loaded != a) load_up(a, 0, u);  // (one block: loaded above)
             for (;;) {
                 const uint32_t mine = (uint32_t)__ballot(id == a);
                 left &= ~mine;
                 if (staged != a) {
+                    probe = 0.0f;
                     if (early) {
                         store_up(a, 0, u);
                     } else {
@@ -440,47 +459,61 @@ __device__ __forceinline__ void add_adapters(const LoraArgs &p, const TileRows<B
                     }
                 }
                 __builtin_amdgcn_wave_barrier();
-                // an accumulator's rows 4 q .. 4 q + 3 follow each other
+                // an accumulator's rows 4 q .. 4 q + 3 follow each other; `checked`
+                // where up's block has an infinity or NaN somewhere
+                auto add = [&](auto checked) __attribute__((always_inline)) {
+                    bool out = false;
 #pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const int r = q * 8 + (lane >> 5) * 4;
-                    const i32x4 e = *(const i32x4 *)&rows.ex[at + r];
+                    for (int q = 0; q < 4; q++) {
+                        const int r = q * 8 + (lane >> 5) * 4;
+                        const i32x4 e = *(const i32x4 *)&rows.ex[at + r];
 #pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        const bool on = (fit >> (r + w)) & 1;
+                        for (int w = 0; w < 4; w++) {
+                            const bool on = (fit >> (r + w)) & 1;
 #pragma unroll
-                        for (int ni = 0; ni < NI; ni++) {
-                            const float c = acc[mi][ni][q * 4 + w];
-                            const float x = fmaf(fine[ni][q * 4 + w], 1.0f / REST_SIZE, sum[ni][q * 4 + w]);
-                            const float more = c + scale * ldexpf(x, e[w]);
-                            acc[mi][ni][q * 4 + w] = on ? more : c;
+                            for (int ni = 0; ni < NI; ni++) {
+                                const float c = acc[mi][ni][q * 4 + w];
+                                const float x = fmaf(fine[ni][q * 4 + w], 1.0f / REST_SIZE, sum[ni][q * 4 + w]);
+                                const float more = c + scale * ldexpf(x, e[w]);
+                                const bool fits = !decltype(checked)::value || fabsf(x) <= 3.402823466e38f;
+                                acc[mi][ni][q * 4 + w] = on && fits ? more : c;
+                                out |= on && !fits && col0 + ni * 32 + (lane & 31) < p.N;
+                            }
                         }
                     }
-                }
+                    if (decltype(checked)::value && __ballot(out)) odd |= 0x10000u << mi;
+                };
+                if (__ballot(!(probe == 0.0f))) add(std::true_type{});
+                else add(std::false_type{});
                 if (!left) break;
                 a = next;
             }
         }
     }
+    return odd;
 }
 
-// C += scale * low . up for the wave's rows that are marked kWide, once the
-// rest of C is stored: v_mfma_f32_32x32x2_f32 on low as it is, one distinct
-// adapter of each 32-row block after the other, its up straight from memory.
-// Each lane adds to elements that it has stored itself.  Few rows come here, so
-// it is kept small rather than fast, and outside the registers and the
-// instructions of all others (4096 rows, K = N = 4096, rank 64: 154 us with no
-// such row, 165 with one in 500, 256 with all).  A row's sums depend on the row and its adapter
-// alone, and so does whether they come from here: its values are the same
-// whatever block it lies in.
-template <int MI, int NI, int BM>
-__device__ __forceinline__ void add_wide_rows(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0) {
+// C += scale * low . up where add_adapters has left it out, once the rest of C
+// is stored: v_mfma_f32_32x32x2_f32 on low as it is, one distinct adapter of
+// each 32-row block after the other, its up straight from memory.  Each lane
+// adds to elements that it has stored itself.  Few come here, so it is kept
+// small rather than fast, and outside the registers and the instructions of all
+// others (4096 rows, K = N = 4096, rank 64: 156 us with no row marked kWide, 169
+// with one in 500, 265 with all).  An element's value depends on its row, its
+// adapter and its column of up alone, and so does whether it comes from here:
+// it is the same whatever block the row lies in.
+template <int NI, int BM>
+__device__ __forceinline__ void add_exact(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
+                                          uint32_t odd) {
     const int lane = threadIdx.x & 63;
 #pragma unroll 1
-    for (int at = r0; at < r0 + MI * 32; at += 32) {
-        const int id = rows.ex[at + (lane & 31)] == kWide ? rows.id[at + (lane & 31)] : -1;
+    for (int at = r0; odd; at += 32, odd >>= 1) {
+        if (!(odd & 0x10001)) continue;
+        const int id = rows.id[at + (lane & 31)];
         const float *low = p.low + (int64_t)rows.row[at + (lane & 31)] * p.rank;
+        const uint32_t wide = (uint32_t)__ballot(rows.ex[at + (lane & 31)] == kWide);
         uint32_t left = (uint32_t)__ballot(id >= 0);
+        if (!(odd & 0x10000)) left &= wide;
 #pragma unroll 1
         while (left) {
             const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
@@ -492,6 +525,7 @@ __device__ __forceinline__ void add_wide_rows(const LoraArgs &p, const TileRows<
                 const int col = col0 + ni * 32 + (lane & 31);
                 const unsigned char *up = p.up + (int64_t)a * p.stride_up + (int64_t)col * 2;
                 f32x16 sum = {};
+                bool whole = true;  // the lane's half of the column is finite
 #pragma unroll 1
                 for (int c0 = 0; c0 < p.rank; c0 += 8) {
                     // the lane's four of the step's eight k: the same for both operands
@@ -500,13 +534,17 @@ __device__ __forceinline__ void add_wide_rows(const LoraArgs &p, const TileRows<
                         const int c = c0 + (lane >> 5) * 4 + i;
                         const float x = c < p.rank ? low[c] : 0.0f;
                         const float u = c < p.rank && col < p.N ? (float)*(const _Float16 *)(up + (int64_t)c * p.ld_up) : 0.0f;
+                        whole &= fabsf(u) <= 65504.0f;
                         sum = __builtin_amdgcn_mfma_f32_32x32x2f32(x, u, sum, 0, 0, 0);
                     }
                 }
+                const uint64_t halves = __ballot(whole);
+                const uint32_t columns = (uint32_t)halves & (uint32_t)(halves >> 32);
+                const uint32_t take = (columns >> (lane & 31)) & 1 ? mine & wide : mine;
 #pragma unroll
                 for (int v = 0; v < 16; v++) {
                     const int r = (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-                    if (!((mine >> r) & 1) || col >= p.N) continue;
+                    if (!((take >> r) & 1) || col >= p.N) continue;
                     float *dst = (float *)((unsigned char *)p.C + (int64_t)rows.row[at + r] * p.ldc) + col;
                     *dst += scale * sum[v];
                 }
@@ -534,7 +572,7 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     __syncthreads();  // every wave is done with the tiles in LDS
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r0 = (wave % WM) * E::WTM, x0 = tm * BM + r0, col0 = tn * BN + (wave / WM) * E::WTN;
-    add_adapters<E::MI, E::NI, BM, WM * WN>(p, rows, r0, col0, smem, acc);
+    const uint32_t odd = add_adapters<E::MI, E::NI, BM, WM * WN>(p, rows, r0, col0, smem, acc);
     // whole 128-byte lines past the caches, as in store_tile
     auto store = [&](auto masked, auto streaming) __attribute__((always_inline)) {
 #pragma unroll
@@ -563,7 +601,7 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     if (inside && lines) store(std::false_type{}, std::true_type{});
     else if (inside) store(std::false_type{}, std::false_type{});
     else store(std::true_type{}, std::false_type{});
-    add_wide_rows<E::MI, E::NI>(p, rows, r0, col0);
+    add_exact<E::NI>(p, rows, r0, col0, odd);
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
