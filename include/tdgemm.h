@@ -422,9 +422,11 @@ int64_t tdg_lds_probe_bytes(int mode, int64_t iters);
  * are TDG_ERR_UNSUPPORTED.  Results are the same from run to run, and the
  * calls can be captured into a graph.  Ids, slots and offsets are read on the
  * device and never lead a read or write outside the arrays as described here,
- * whatever they hold.  The products read A, B, down and up to the end of the
- * 16-byte piece that holds their last element, within its 4 KiB page; what is
- * read there is not used.  Calls that may run at the same time (on several
+ * whatever they hold.  Each matrix is one allocation, rows and the gaps
+ * between them, as above; the matrices of a stack need not be.  The products
+ * read a matrix to the end of the 16-byte piece that holds its last element
+ * (and from the start of the 4-byte word that holds its first), within its 4
+ * KiB pages; what is read there is not used.  Calls that may run at the same time (on several
  * streams, or in graphs that are replayed side by side) need a workspace
  * each; calls that follow each other on one stream can share it. */
 

@@ -439,6 +439,44 @@ def test_lora_tiles_at_a_page_end(lib, M, K, N, rank, pad):
         near(lib.gemm_f16f32_lora(*args, pick.cuda()), want, torch.zeros_like(want))
 
 
+def apart_at_page_ends(t, pad):
+    """A stack whose matrices each end with a page, with a page of NaN or more
+    before the next one; rows of `pad` elements more."""
+    n, r, c = t.shape
+    span = (r - 1) * (c + pad) + c
+    stride = (span + 2047) // 2048 * 2048 + 2048
+    buf = torch.full((n * stride + 4096,), float("nan"), dtype=t.dtype, device="cuda")
+    skip = (-(buf.data_ptr() + span * 2)) % 4096 // 2
+    v = torch.as_strided(buf, (n, r, c), (stride, c + pad, 1), skip)
+    assert all((v[g].data_ptr() + span * 2) % 4096 == 0 for g in range(n))
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("rows,K,N", PAGE_ENDS)
+@pytest.mark.parametrize("pad", [0, 3])
+def test_grouped_weights_apart_at_page_ends(lib, rows, K, N, pad):
+    r = rng(34, K, N, pad)
+    off, R = groups_of(rows, 0, 0)
+    a, b = whole(r, R, K), whole(r, len(rows), K, N)
+    want, _ = grouped64(a, b, off)
+    near(lib.gemm_f16f32_grouped(a.cuda(), apart_at_page_ends(b, pad), off.cuda()), want, torch.zeros_like(want))
+    bt = b.transpose(1, 2).contiguous()
+    near(lib.gemm_f16f32_grouped_nt(a.cuda(), apart_at_page_ends(bt, pad), off.cuda()), want, torch.zeros_like(want))
+
+
+@pytest.mark.parametrize("M,K,N,rank", [(3, 64, 67, 8), (20, 128, 129, 9), (70, 192, 131, 33), (256, 65, 7, 3),
+                                        (300, 64, 129, 17), (400, 72, 1001, 41), (1100, 71, 6603, 65),
+                                        (700, 64, 2305, 17), (700, 71, 2303, 5)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_lora_adapters_apart_at_page_ends(lib, M, K, N, rank, pad):
+    r = rng(35, M, K, pad)
+    a, b, down, up = whole(r, M, K, most=2), whole(r, K, N), whole(r, 3, K, rank, most=1), whole(r, 3, rank, N, most=2)
+    pick = torch.from_numpy(r.integers(-1, 3, M)).to(torch.int32)
+    want, _, _ = lora64(a, b, down, up, pick, None)
+    got = lib.gemm_f16f32_lora(a.cuda(), b.cuda(), apart_at_page_ends(down, pad), apart_at_page_ends(up, pad), pick.cuda())
+    near(got, want, torch.zeros_like(want))
+
+
 @pytest.mark.parametrize("K,N", [(128, 128), (72, 100), (65, 67)])
 def test_groups_do_not_touch_each_other(lib, K, N):
     """Infinities and NaN in one group's rows and weights stay in that group."""

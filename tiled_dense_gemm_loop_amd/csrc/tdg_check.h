@@ -1,6 +1,6 @@
 // tdg_check.h -- argument checks shared by the operators whose rows pick
-// their weights (routed rows, grouped products, adapters).  Host code only;
-// nothing here calls HIP.
+// their weights (routed rows, grouped products, adapters).  Nothing here
+// calls HIP.
 #pragma once
 
 #include <stdint.h>
@@ -47,16 +47,29 @@ inline bool overlaps(const void *a, uint64_t alen, const void *b, uint64_t blen)
 inline bool aligned_to(const void *p, uintptr_t bytes) { return (uintptr_t)p % bytes == 0; }
 
 // Chunks of 16 bytes sit on a 16-byte grid from each row's start, and the last
-// one of an operand can reach past its last element.  Where it would reach into
-// another 4 KiB page, which need not be mapped: that page's address, so that
-// the kernels load what they need of it element by element.  kNoStop: nowhere.
+// one of a matrix, whose last row (`cols` 2-byte elements) is at `row`, can reach
+// past its last element.  Where it would reach into another 4 KiB page, which
+// need not be mapped: that page's address, so that the kernels load what they
+// need of it element by element.  kNoStop: nowhere.  (The kernels call it too.)
 constexpr uint64_t kNoStop = ~(uint64_t)0;
+constexpr uint64_t page_stop(uint64_t row, int64_t cols) {
+    const uint64_t last = row + (uint64_t)cols * 2 - 1, end = row + (uint64_t)((cols - 1) / 8 * 16 + 15);
+    return last >> 12 == end >> 12 ? kNoStop : ((last >> 12) + 1) << 12;
+}
+
+// The same of a matrix, or of the last of a stack.
 inline uint64_t chunk_stop(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t count = 1,
                            int64_t stride = 0) {
     if (rows <= 0 || cols <= 0 || count <= 0) return kNoStop;
-    const uintptr_t row = (uintptr_t)p + (uintptr_t)((count - 1) * stride + (rows - 1) * ld) * 2;
-    const uintptr_t last = row + (uintptr_t)cols * 2 - 1, end = row + (uintptr_t)((cols - 1) / 8 * 16 + 15);
-    return last >> 12 == end >> 12 ? kNoStop : (uint64_t)((last >> 12) + 1) << 12;
+    return page_stop((uint64_t)(uintptr_t)p + (uint64_t)((count - 1) * stride + (rows - 1) * ld) * 2, cols);
+}
+
+// Whether a stack's matrices need a stop each: their last chunks can reach past
+// them, into a page that neither they nor the next matrix has a byte of.  (Where
+// the next one begins less than a page behind, it has.)
+inline bool stops_each(int64_t rows, int64_t cols, int64_t ld, int64_t count, int64_t stride) {
+    if (rows <= 0 || cols <= 0 || count <= 1 || cols % 8 == 0) return false;
+    return stride - ((rows - 1) * ld + cols) >= 2048;
 }
 
 inline int64_t ceil_quot(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -57,14 +57,14 @@ struct Variant {
                           : (const void *)&tdg::KERNEL<tdg::LAY_TN, __VA_ARGS__>)
 
 Variant choose(int lay, int64_t groups, int64_t rows, int64_t M, int64_t N, int64_t lda, int64_t ldb,
-               uint64_t a_stop, uint64_t b_stop) {
+               bool a_stops, bool b_stops) {
     const bool tn = lay == tdg::LAY_TN;
     // The DMA's lanes reach a tile's rows with 32-bit byte offsets.  Where
     // an operand's rows lie at one k each and its last chunk must not be copied
-    // (a_stop, b_stop), the rows have to be long enough for no other row's
+    // (a_stops, b_stops), the rows have to be long enough for no other row's
     // chunk to reach as far.
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
-    const bool thin = (tn && lda < 8 && a_stop != tdg::kNoStop) || (lay != tdg::LAY_NT && ldb < 8 && b_stop != tdg::kNoStop);
+    const bool thin = (tn && lda < 8 && a_stops) || (lay != tdg::LAY_NT && ldb < 8 && b_stops);
     if (thin || lda > far || ldb > far) return {TDG_BY_LAYOUT(tdg_grouped_any, 128, 128, 2, 2), 128, 128, 256, INT32_MAX};
     // Tiles that the product is expected to have: half a row tile more per
     // group that can have rows than the rows fill, one at the least.
@@ -125,9 +125,11 @@ int run_grouped(int lay, int64_t groups, const int32_t *offsets, int64_t rows, i
     GroupedArgs a;
     const bool tn = lay == tdg::LAY_TN;
     a.a_stop = tdg::chunk_stop(A, rows, tn ? M : K, lda);
-    a.b_stop = tn ? tdg::chunk_stop(B, rows, N, ldb)
-                  : tdg::chunk_stop(B, lay == tdg::LAY_NN ? K : N, lay == tdg::LAY_NN ? N : K, ldb, groups, stride_b);
-    const Variant v = choose(lay, groups, rows, M, N, lda, ldb, a.a_stop, a.b_stop);
+    const int64_t br = lay == tdg::LAY_NN ? K : N, bc = lay == tdg::LAY_NN ? N : K;  // of a group's B
+    a.b_stop = tn ? tdg::chunk_stop(B, rows, N, ldb) : tdg::chunk_stop(B, br, bc, ldb, groups, stride_b);
+    a.b_each = !tn && tdg::stops_each(br, bc, ldb, groups, stride_b);
+    const Variant v = choose(lay, groups, rows, M, N, lda, ldb, a.a_stop != tdg::kNoStop,
+                             a.b_each || a.b_stop != tdg::kNoStop);
     a.A = (const unsigned char *)A, a.B = (const unsigned char *)B, a.C = (unsigned char *)C;
     a.lda = lda * 2, a.ldb = ldb * 2, a.ldc = ldc * 4;
     a.stride_b = stride_b * 2, a.stride_c = stride_c * 4;

@@ -18,6 +18,7 @@
 // of bank conflicts.
 #pragma once
 
+#include "tdg_check.h"
 #include "tdg_kernels.hpp"
 
 namespace tdg {
@@ -38,6 +39,7 @@ struct GroupedArgs {
     int tiles_n;   // ceil(N / BN)
     int tiles_most;  // no tile has this number or a higher one
     uint64_t a_stop, b_stop;  // chunks end at this address or below (chunk_stop)
+    int b_each;      // NN, NT: each group's B has a stop of its own (stops_each)
     int warm;        // read A and B once at the start (tdg_grouped_tn_loop)
     int flags;       // TDG_DEBUG_* bits
 };
@@ -667,6 +669,11 @@ struct GroupedWork {
     __device__ __forceinline__ const unsigned char *B(const GroupedArgs &a) const {
         return a.B + (LAY == LAY_TN ? 0 : (int64_t)t.g * a.stride_b);
     }
+    __device__ __forceinline__ uint64_t b_stop(const GroupedArgs &a) const {
+        if (LAY == LAY_TN || !a.b_each) return a.b_stop;
+        const int rows = LAY == LAY_NN ? a.K : a.N, cols = LAY == LAY_NN ? a.N : a.K;
+        return page_stop((uint64_t)(uintptr_t)B(a) + (uint64_t)((int64_t)(rows - 1) * a.ldb), cols);
+    }
     __device__ __forceinline__ int k_lo() const { return LAY == LAY_TN ? t.lo : 0; }
     __device__ __forceinline__ int k_hi(const GroupedArgs &a) const { return LAY == LAY_TN ? t.hi : a.K; }
     template <class E, int WM>
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_any(GroupedArgs a)
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
     E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
-           a.a_stop, a.b_stop, smem, acc);
+           a.a_stop, w.b_stop(a), smem, acc);
     w.template store<E, WM>(a, acc);
 }
 
@@ -701,7 +708,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_ring(GroupedArgs a
     f32x16 acc[E::MI][E::NI];
     clear_acc(acc);
     E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(), w.k_hi(a),
-           a.a_stop, a.b_stop, smem, acc);
+           a.a_stop, w.b_stop(a), smem, acc);
     w.template store<E, WM>(a, acc);
 }
 
@@ -720,13 +727,13 @@ __global__ void __launch_bounds__(512, 1) tdg_grouped_cut(GroupedArgs a) {
         f32x16 acc[E::MI][E::NI];
         clear_acc(acc);
         E::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(),
-               w.k_hi(a), a.a_stop, a.b_stop, smem, acc);
+               w.k_hi(a), a.a_stop, w.b_stop(a), smem, acc);
         w.template store<E, 2>(a, acc);
     } else {
         f32x16 acc[H::MI][H::NI];
         clear_acc(acc);
         H::run(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(),
-               min(a.N, w.y0() + 128), w.k_lo(), w.k_hi(a), a.a_stop, a.b_stop, smem, acc);
+               min(a.N, w.y0() + 128), w.k_lo(), w.k_hi(a), a.a_stop, w.b_stop(a), smem, acc);
         w.template store<H, 4>(a, acc);
     }
 }
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 1) tdg_grouped_tn_loop(GroupedArg
         E r;
         auto start = [&]() __attribute__((always_inline)) {
             r.aim(w.A(a), a.lda, RowsFrom{w.t.x0, a.lda}, w.B(a), a.ldb, w.t.x0, w.x_end(a), w.y0(), a.N, w.k_lo(),
-                  w.k_hi(a), a.a_stop, a.b_stop, smem);
+                  w.k_hi(a), a.a_stop, w.b_stop(a), smem);
             r.start();
         };
         start();

@@ -43,7 +43,8 @@ struct LoraArgs {
     int2 *seat;     // M: row and adapter, sorted by adapter (more than kFewRows)
     int64_t lda, ldb, ldc, ld_down, stride_down, ld_up, stride_up;  // bytes
     uint64_t a_stop, b_stop, down_stop;  // chunks end at this address or below (chunk_stop)
-    int up_apart;  // up's rows' last chunks are loaded element by element
+    int down_each;  // each adapter's down has a stop of its own (stops_each)
+    int up_apart;   // up's rows' last chunks are loaded element by element
     int M, N, K, adapters, rank;
     int row_tiles, col_tiles;           // of the shared product
     int parts, k_per_part;              // K tiles of each slice
@@ -217,8 +218,12 @@ __device__ __forceinline__ void lora_parts(const LoraArgs &p, unsigned char *sme
         if (threadIdx.x < BM) key[threadIdx.x] = max(row, 0);
         __syncthreads();
         clear_acc(acc);
-        E::run(p.A, p.lda, RowsBy{key, p.lda}, p.down + (int64_t)a * p.stride_down, p.ld_down, 0, rows, tc * BN,
-               p.rank, k_lo, k_hi, p.a_stop, p.down_stop, smem, acc);
+        const unsigned char *down = p.down + (int64_t)a * p.stride_down;
+        const uint64_t down_stop =
+            p.down_each ? page_stop((uint64_t)(uintptr_t)down + (uint64_t)((int64_t)(p.K - 1) * p.ld_down), p.rank)
+                        : p.down_stop;
+        E::run(p.A, p.lda, RowsBy{key, p.lda}, down, p.ld_down, 0, rows, tc * BN, p.rank, k_lo, k_hi, p.a_stop, down_stop,
+               smem, acc);
 #pragma unroll
         for (int mi = 0; mi < E::MI; mi++)
 #pragma unroll
@@ -795,14 +800,16 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
     p.low_parts = (int)plan.low_parts, p.low_k_per_part = (int)plan.low_k_per_part;
     p.a_stop = chunk_stop(A, M, K, lda), p.b_stop = chunk_stop(B, K, N, ldb);
     p.down_stop = chunk_stop(down, K, rank, ld_down, adapters, stride_down);
-    p.up_apart = chunk_stop(up, rank, N, ld_up, adapters, stride_up) != kNoStop;
+    p.down_each = stops_each(K, rank, ld_down, adapters, stride_down);
+    p.up_apart = stops_each(rank, N, ld_up, adapters, stride_up) ||
+                 chunk_stop(up, rank, N, ld_up, adapters, stride_up) != kNoStop;
     // The DMA's lanes reach a tile's rows with 32-bit byte offsets; and rows of
     // B and down whose last chunk must not be copied have to be long enough for
     // no other row's chunk to reach as far.
     const int64_t far = (int64_t)UINT32_MAX / 2 / 256 - 256;
     const bool ring_main = lda <= far && ldb <= far && M * lda <= (int64_t)UINT32_MAX / 2 &&
                            (ldb >= 8 || p.b_stop == kNoStop);
-    const bool ring = ring_main && ld_down <= far && (ld_down >= 8 || p.down_stop == kNoStop);
+    const bool ring = ring_main && ld_down <= far && (ld_down >= 8 || (!p.down_each && p.down_stop == kNoStop));
 
     const int64_t low_tiles = ceil_quot(M, PART_TILE);
     p.low_cols = (int)ceil_quot(rank, 64);
