@@ -536,6 +536,57 @@ def test_offsets_that_make_no_sense_stay_inside(lib, offsets):
     assert bool(torch.isfinite(dw).all()) and float(dw.max()) <= 64
 
 
+def wild_offsets(r, kind, groups, R):
+    if kind == "descending":
+        off = np.sort(r.integers(0, R + 1, groups + 1))[::-1]
+    elif kind == "around":
+        off = r.integers(-R, 2 * R + 1, groups + 1)
+    elif kind == "anywhere":
+        off = r.integers(-2 ** 31, 2 ** 31, groups + 1)
+    else:  # the whole range again and again
+        off = np.where(np.arange(groups + 1) % 2 == 0, -2 ** 31, 2 ** 31 - 1)
+    return torch.from_numpy(off.copy()).to(torch.int32)
+
+
+@pytest.mark.parametrize("rows,K,N", GROUPED[2:3] + GROUPED[6:8] + GROUPED[16:] + [([2, 260], 1001, 7)])
+@pytest.mark.parametrize("kind", ["descending", "around", "anywhere", "all"])
+def test_wild_offsets_in_every_tile(lib, rows, K, N, kind):
+    """Offsets that do not ascend or lie outside the rows, for each of the tiles
+    (the last shape's weights end with a page: the register path).  They count
+    as clamped to the rows.  A row of several groups has the product of one of
+    them, or none where there are more tiles than the rows can make; a row of
+    no group stays as it was, and so does all around C."""
+    r = rng(36, K, N, len(rows))
+    G, R = len(rows), sum(rows)
+    a, b, dy = whole(r, R, K, most=1), whole(r, G, K, N, most=1), whole(r, R, N, most=1)
+    off = wild_offsets(r, kind, G, R)
+    at = off.long().clamp(0, R).tolist()
+    end = at_page_end if N == 7 else (lambda t: t.cuda())
+    for fn, w in ((lib.gemm_f16f32_grouped, b), (lib.gemm_f16f32_grouped_nt, b.transpose(1, 2).contiguous())):
+        buf = torch.full((R + 16, N), -7.5, device="cuda")
+        fn(a.cuda(), end(w), off.cuda(), buf[8:R + 8])
+        got = buf.cpu()
+        assert (got[:8] == -7.5).all() and (got[R + 8:] == -7.5).all()
+        got = got[8:R + 8]
+        fine = got == -7.5
+        for g in range(G):
+            if at[g + 1] > at[g]:
+                s = slice(at[g], at[g + 1])
+                fine[s] |= got[s] == a[s].float() @ b[g].float()
+        assert fine.all()
+        ascending = [g for g in range(G) if at[g + 1] > at[g]]
+        if len(ascending) == 1:  # and then every row of it has its product
+            s = slice(at[ascending[0]], at[ascending[0] + 1])
+            assert not (got[s] == -7.5).any()
+    buf = torch.full((G + 2, K, N), -7.5, device="cuda")
+    lib.gemm_f16f32_grouped_tn(a.cuda(), end(dy), off.cuda(), buf[1:G + 1])
+    got = buf.cpu()
+    assert (got[0] == -7.5).all() and (got[G + 1] == -7.5).all()
+    for g in range(G):
+        s = slice(at[g], max(at[g], at[g + 1]))
+        assert torch.equal(got[g + 1], a[s].float().t() @ dy[s].float())
+
+
 def test_grouped_past_32_bits(lib):
     """Weights and rows whose byte offsets pass 2^32."""
     r = rng(12)
