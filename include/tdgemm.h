@@ -418,17 +418,20 @@ int64_t tdg_lds_probe_bytes(int mode, int64_t iters);
  * any HIP call, TDG_ERR_NO_DEVICE off gfx950, thread-safe.  Outputs (and a
  * workspace) may not overlap each other or an input; sizes are 0 .. 2^31 -
  * 2^16; leading dimensions and strides are in elements; every array is aligned
- * to its element.  Shapes past one launch's grid (over 16 million workgroups)
- * are TDG_ERR_UNSUPPORTED.  Results are the same from run to run, and the
- * calls can be captured into a graph.  Ids, slots and offsets are read on the
- * device and never lead a read or write outside the arrays as described here,
- * whatever they hold.  Each matrix is one allocation, rows and the gaps
- * between them, as above; the matrices of a stack need not be.  The products
- * read a matrix to the end of the 16-byte piece that holds its last element
- * (and from the start of the 4-byte word that holds its first), within its 4
- * KiB pages; what is read there is not used.  Calls that may run at the same time (on several
- * streams, or in graphs that are replayed side by side) need a workspace
- * each; calls that follow each other on one stream can share it. */
+ * to its element.  Shapes past one launch's grid are TDG_ERR_UNSUPPORTED: a
+ * launch has fewer than 2^32 threads (16 million workgroups of 256), and the
+ * combine's gradient takes top_k up to 524280, the adapters N up to 33553920
+ * where they join parts (M <= 256, or few tiles).  Results are the same from
+ * run to run, and the calls can be captured into a graph.  Ids, slots and
+ * offsets are read on the device and never lead a read or write outside the
+ * arrays as described here, whatever they hold.  Each matrix is one
+ * allocation, rows and the gaps between them, as above; the matrices of a
+ * stack need not be.  The products read a matrix to the end of the 16-byte
+ * piece that holds its last element (and from the start of the 4-byte word
+ * that holds its first), within its 4 KiB pages; what is read there is not
+ * used.  Calls that may run at the same time (on several streams, or in graphs
+ * that are replayed side by side) need a workspace each; calls that follow
+ * each other on one stream can share it. */
 
 /* Element of the rows that tdg_rows_* move. */
 typedef enum { TDG_ELEM_F16 = 0, TDG_ELEM_F32 = 1 } tdg_elem;
@@ -487,7 +490,8 @@ int tdg_rows_combine_grad(int row_elem, int token_elem, int64_t tokens, int64_t 
  *   grouped_tn   C_g = A[g]^T . B[g]   A: rows x M, B: rows x N, C_g: M x N:
  *                the gradient of its B; zeros for a group without rows.
  * B_g is at B + g * stride_b, C_g at C + g * stride_c.  Rows of C that belong
- * to no group are left as they were. */
+ * to no group are left as they were.  Where offsets do not ascend, a row that
+ * lies in several groups gets one of their products, or none. */
 int gemm_f16f32_grouped(int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, const uint16_t *A,
                         int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b, float *C, int64_t ldc,
                         void *stream);

@@ -135,6 +135,20 @@ def test_grids_past_one_launch_are_refused():
                     **more) == TOO_BIG
 
 
+@no_device_only
+def test_the_limits_that_the_header_states():
+    """The largest top_k and N are taken, the next ones refused."""
+    far = [i << 50 for i in range(1, 8)]
+    grad = dict(tokens=1, cols=1, ldy=1, ldz=1, lddz=1, rows=1, dy=far[0], z=far[1], slots=far[2], weights=far[3],
+                dz=far[4], dweights=far[5])
+    for top_k, rc in ((524280, NODEV), (524281, TOO_BIG)):
+        assert call("tdg_rows_combine_grad", GRAD, **grad, top_k=top_k, ld_weights=top_k, ld_dweights=top_k) == rc
+    for n, rc in ((33553920, NODEV), (33553921, TOO_BIG)):
+        assert call("gemm_f16f32_lora", LORA, M=1, N=n, K=1, rank=1, a=far[0], lda=1, b=far[1], ldb=n, down=far[2],
+                    ld_down=1, stride_down=1, up=far[3], ld_up=n, stride_up=n, adapter=far[4], c=far[5], ldc=n,
+                    ws=far[6], ws_bytes=1 << 45) == rc
+
+
 def test_workspace_sizes():
     assert tdg.tdg_route_workspace(0, 1, 8) == 0
     assert tdg.tdg_route_workspace(512, 8, 1024) == 0
