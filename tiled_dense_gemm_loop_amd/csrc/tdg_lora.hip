@@ -341,6 +341,7 @@ __device__ __forceinline__ uint32_t add_adapters(const LoraArgs &p, const TileRo
     const int tid = thread_again(), lane = tid & 63;
     unsigned char *up_at = smem + 2 * IL::BYTES + (tid >> 6) * IU::BYTES;
     uint32_t odd = 0;    // bits mi, mi + 16: the wave's block mi has such rows, such elements
+    static_assert(MI <= 16, "a bit per block");
     float probe = 0.0f;  // NaN: what the lane has staged of up is not all finite
     auto look_at = [&](const u32x4 &v) __attribute__((always_inline)) {
         typedef _Float16 h2 __attribute__((ext_vector_type(2)));
@@ -507,18 +508,19 @@ __device__ __forceinline__ uint32_t add_adapters(const LoraArgs &p, const TileRo
 // with one in 500, 265 with all).  An element's value depends on its row, its
 // adapter and its column of up alone, and so does whether it comes from here:
 // it is the same whatever block the row lies in.
-template <int NI, int BM>
+template <int MI, int NI, int BM>
 __device__ __forceinline__ void add_exact(const LoraArgs &p, const TileRows<BM> &rows, int r0, int col0,
                                           uint32_t odd) {
     const int lane = threadIdx.x & 63;
 #pragma unroll 1
-    for (int at = r0; odd; at += 32, odd >>= 1) {
-        if (!(odd & 0x10001)) continue;
+    for (int mi = 0; mi < MI; mi++) {
+        if (!((odd >> mi) & 0x10001)) continue;
+        const int at = r0 + mi * 32;
         const int id = rows.id[at + (lane & 31)];
         const float *low = p.low + (int64_t)rows.row[at + (lane & 31)] * p.rank;
         const uint32_t wide = (uint32_t)__ballot(rows.ex[at + (lane & 31)] == kWide);
         uint32_t left = (uint32_t)__ballot(id >= 0);
-        if (!(odd & 0x10000)) left &= wide;
+        if (!((odd >> mi) & 0x10000)) left &= wide;
 #pragma unroll 1
         while (left) {
             const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(__ffs(left) - 1));
@@ -606,7 +608,7 @@ __device__ __forceinline__ void lora_main(const LoraArgs &p, unsigned char *smem
     if (inside && lines) store(std::false_type{}, std::true_type{});
     else if (inside) store(std::false_type{}, std::false_type{});
     else store(std::true_type{}, std::false_type{});
-    add_exact<E::NI>(p, rows, r0, col0, odd);
+    if (odd) add_exact<E::MI, E::NI>(p, rows, r0, col0, odd);
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES>
