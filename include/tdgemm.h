@@ -520,6 +520,82 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
                      const int32_t *adapter, const float *scale, float *C, int64_t ldc, void *workspace,
                      size_t workspace_bytes, void *stream);
 
+/* ---- 4-bit weights with group scales.  The rules of the operators above
+ * hold (pointers, streams, errors, captures, overlaps, sizes).  A K x N matrix
+ * is kept as
+ *   codes   ceil(K / 128) x N pieces of 64 bytes, 16-byte aligned, a leading
+ *           dimension (ld_codes >= N) in pieces: the code of k = 128 b + 32 j +
+ *           8 q + i (j, q < 4, i < 8) of column n is the 4 bits from bit
+ *           4 (i / 2) + 16 (i % 2) on of the little-endian 32-bit word 4 q + j
+ *           of piece (b, n).  Codes of k >= K are not used, whatever they hold;
+ *   scales  ceil(K / group) x N FP16: `group`, a multiple of 32, is how many
+ *           values of k of a column share one (K or more: the whole column);
+ *   zeros   uint8 like scales, or NULL: 8 for all.
+ * The weight is (code - zero) * scale.  A stack of `count` matrices has
+ * stride_codes pieces, stride_scales and stride_zeros elements between two.
+ *
+ *   quantize    of a stack of K x N FP16 matrices.  Without zeros a group's
+ *               scale is max |w| / 7 and the code rint(w / scale) + 8 in 0 .. 15;
+ *               with zeros (written then) lo = min(0, min w), hi = max(0, max
+ *               w), the scale is (hi - lo) / 15, the zero rint(-lo / scale) in
+ *               0 .. 15, the code rint(w / scale) + zero in 0 .. 15.  Each step
+ *               is rounded in FP32, the scale then to FP16.  NaN widens no
+ *               range; a weight without a place (NaN, infinite under an infinite
+ *               scale, any under a scale of 0) gets the zero's code.  Codes of
+ *               k >= K are 0.
+ *   dequantize  W = (code - zero) * scale, rounded once: FP16 or FP32
+ *               (out_elem).
+ *
+ * The products, FP16 rows -> FP32:
+ *   gemm_f16w4f32          C[m][n] = sum over groups G of scale[G][n] * sum over
+ *                          k in G of A[m][k] * (code[k][n] - zero[G][n]), the
+ *                          inner sums over the group or over pieces of it of 32 k
+ *                          or more.  No weight is rounded.
+ *   gemm_f16w4f32_grouped  the same with matrix g for rows offsets[g] ..
+ *                          offsets[g + 1] - 1, as gemm_f16f32_grouped (where
+ *                          offsets do not ascend, each element of a row of
+ *                          several groups is one of their products, or stays). */
+int tdg_w4_quantize(int64_t count, int64_t K, int64_t N, int64_t group, const uint16_t *W, int64_t ldw,
+                    int64_t stride_w, uint8_t *codes, int64_t ld_codes, int64_t stride_codes, uint16_t *scales,
+                    int64_t ld_scales, int64_t stride_scales, uint8_t *zeros, int64_t ld_zeros, int64_t stride_zeros,
+                    void *stream);
+int tdg_w4_dequantize(int out_elem, int64_t count, int64_t K, int64_t N, int64_t group, const uint8_t *codes,
+                      int64_t ld_codes, int64_t stride_codes, const uint16_t *scales, int64_t ld_scales,
+                      int64_t stride_scales, const uint8_t *zeros, int64_t ld_zeros, int64_t stride_zeros, void *W,
+                      int64_t ldw, int64_t stride_w, void *stream);
+int gemm_f16w4f32(int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *A, int64_t lda,
+                  const uint8_t *codes, int64_t ld_codes, const uint16_t *scales, int64_t ld_scales,
+                  const uint8_t *zeros, int64_t ld_zeros, float *C, int64_t ldc, void *stream);
+int gemm_f16w4f32_grouped(int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, int64_t group,
+                          const uint16_t *A, int64_t lda, const uint8_t *codes, int64_t ld_codes,
+                          int64_t stride_codes, const uint16_t *scales, int64_t ld_scales, int64_t stride_scales,
+                          const uint8_t *zeros, int64_t ld_zeros, int64_t stride_zeros, float *C, int64_t ldc,
+                          void *stream);
+
+/* ---- A whole layer of experts for a few tokens, without a plan or sorted
+ * rows: y[t] = sum over j of weights[t][j] * (h . down[e]) with e = ids[t][j]
+ * and h = silu(x[t] . up[e] left) * (x[t] . up[e] right), silu(g) = g / (1 +
+ * exp(-g)).  x is tokens x cols FP16; up[e] is cols x 2 inner at up + e *
+ * stride_up, its left half the gate; down[e] inner x cols; y tokens x cols in
+ * FP16 or FP32 (out_elem).  Products and h are kept in FP32, y is summed in the
+ * order of j and rounded once; weights NULL means 1.  Entries whose id lies
+ * outside [0, experts) add nothing (a token without an expert gets zeros), and
+ * no weight of an expert that a token did not pick reaches it.  The same expert
+ * may be named twice.  1 <= experts <= 1024; cols and inner up to 2^30 - 2^15;
+ * more than TDG_LAYER_MAX_TOKENS tokens or TDG_LAYER_MAX_TOP_K choices are
+ * TDG_ERR_UNSUPPORTED: sorted rows and grouped products are for those.  The
+ * workspace (tdg_expert_layer_workspace) is 16-byte aligned; its contents on
+ * return are unspecified. */
+#define TDG_LAYER_MAX_TOKENS 64
+#define TDG_LAYER_MAX_TOP_K 32
+int tdg_expert_layer_workspace(int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int64_t inner,
+                               size_t *bytes);
+int tdg_expert_layer(int out_elem, int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int64_t inner,
+                     const uint16_t *x, int64_t ldx, const int32_t *ids, int64_t ld_ids, const float *weights,
+                     int64_t ld_weights, const uint16_t *up, int64_t ld_up, int64_t stride_up, const uint16_t *down,
+                     int64_t ld_down, int64_t stride_down, void *y, int64_t ldy, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -56,6 +56,8 @@ EXPORTED = (
     "tdg_route_workspace", "tdg_route_plan", "tdg_rows_dispatch", "tdg_rows_combine",
     "tdg_rows_combine_grad", "gemm_f16f32_grouped", "gemm_f16f32_grouped_nt",
     "gemm_f16f32_grouped_tn", "tdg_lora_workspace", "gemm_f16f32_lora",
+    "tdg_w4_quantize", "tdg_w4_dequantize", "gemm_f16w4f32", "gemm_f16w4f32_grouped",
+    "tdg_expert_layer_workspace", "tdg_expert_layer",
 )
 
 
@@ -183,6 +185,12 @@ def load_library(path: str = LIB_PATH):
         "tdg_lora_workspace": [i64] * 5 + [size_p],
         "gemm_f16f32_lora": [i64] * 3 + [vp, i64, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp,
                                          i64, vp, size_t, vp],
+        "tdg_w4_quantize": [i64] * 4 + [vp, i64, i64] * 4 + [vp],
+        "tdg_w4_dequantize": [c_int] + [i64] * 4 + [vp, i64, i64] * 4 + [vp],
+        "gemm_f16w4f32": [i64] * 4 + [vp, i64] * 5 + [vp],
+        "gemm_f16w4f32_grouped": [i64, vp] + [i64] * 4 + [vp, i64] + [vp, i64, i64] * 3 + [vp, i64, vp],
+        "tdg_expert_layer_workspace": [i64] * 5 + [size_p],
+        "tdg_expert_layer": [c_int] + [i64] * 5 + [vp, i64] * 3 + [vp, i64, i64] * 2 + [vp, i64, vp, size_t, vp],
     }.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = c_int
@@ -603,17 +611,17 @@ TDG_ELEM_F32 = 1
 TDG_LORA_MAX_RANK = 256
 
 
-_FLOATS = _HALF = _SINGLE = _INT = None  # dtype tuples, once torch is loaded
+_FLOATS = _HALF = _SINGLE = _BYTE = _INT = None  # dtype tuples, once torch is loaded
 
 
 def _types():
     """Loads torch's names that the calls below use, once."""
-    global _FLOATS, _HALF, _SINGLE, _INT, _empty, _device_now
+    global _FLOATS, _HALF, _SINGLE, _BYTE, _INT, _empty, _device_now
     torch = _torch()
     _empty = torch.empty_strided  # a microsecond less than torch.empty with a device
     _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _FLOATS, _HALF = (torch.float16, torch.float32), (torch.float16, torch.int16)
-    _SINGLE = (torch.float32,)
+    _SINGLE, _BYTE = (torch.float32,), (torch.uint8,)
     _INT = (torch.int32,)  # the last: callers in other threads look at it
 
 
@@ -922,3 +930,210 @@ def gemm_f16f32_lora(A, B, down, up, adapter, scale=None, C=None, workspace=None
     _launch("gemm_f16f32_lora", dev, M, N, K, pa, lda, pb, ldb, n, rank, pd, ldd, sd, pu, ldu, su, p_ad, p_sc, pc,
             ldc, p_ws, ws_bytes)
     return C
+
+
+# ------------------------------------------------------ 4-bit weights with group scales
+
+def _codes_of(t, dev, stack):
+    """Checks the codes of a matrix (blocks x N x 64) or of a stack of them:
+    (count, blocks, N, address, ld, stride)."""
+    shape = t.shape
+    if len(shape) != 3 + stack or shape[-1] != 64:
+        raise ValueError("codes must be %sblocks x N x 64, got shape %s" % ("count x " * stack, tuple(shape)))
+    if t.dtype not in _BYTE:
+        raise TypeError("codes has dtype %s; expected torch.uint8" % t.dtype)
+    if t.get_device() != dev:
+        raise ValueError("codes must be a device tensor on device %d" % dev)
+    count = shape[0] if stack else 1
+    blocks, N = shape[-3:-1]
+    if count == 0 or blocks == 0 or N == 0:
+        return count, blocks, N, t.data_ptr(), N or 1, blocks * (N or 1)
+    st = t.stride()
+    ld, stride = st[-3] if blocks > 1 else N * 64, st[0] if count > 1 else 0
+    if st[-1] != 1 or (st[-2] != 64 and N > 1) or ld % 64 or stride % 64:
+        raise ValueError("codes: a block's columns must be contiguous, and strides whole pieces of 64")
+    return count, blocks, N, t.data_ptr(), ld // 64, stride // 64
+
+
+def _group_values(t, types, what, dev, count, groups, N):
+    """Checks scales or zeros, groups x N or a stack of them (`count` not
+    None): (address, ld, stride)."""
+    if count is None:
+        rows, cols, p, ld, _ = _mat(t, types, what, dev)
+        stride = 0
+    else:
+        n, rows, cols, p, ld, stride = _stack(t, types, what, dev)
+    if rows != groups or cols != N or (count is not None and n != count):
+        raise ValueError("%s has shape %s, expected %s" % (
+            what, tuple(t.shape), (groups, N) if count is None else (count, groups, N)))
+    return p, ld, stride
+
+
+def _w4(codes, scales, zeros, K, group, dev, stack):
+    """The checked arguments of 4-bit weights: (count, N, their addresses, leading
+    dimensions and strides)."""
+    count, blocks, N, pc, ldc, sc = _codes_of(codes, dev, stack)
+    group = int(group)
+    if group < 32 or group % 32:
+        raise ValueError("group must be a multiple of 32, got %d" % group)
+    if blocks != (K + 127) // 128:
+        raise ValueError("codes have %d blocks, K = %d needs %d" % (blocks, K, (K + 127) // 128))
+    of, groups = count if stack else None, (K + group - 1) // group
+    ps, lds, ss = _group_values(scales, _HALF, "scales", dev, of, groups, N)
+    pz, ldz, sz = (None, N or 1, 0) if zeros is None else _group_values(zeros, _BYTE, "zeros", dev, of, groups, N)
+    return count, N, (pc, ldc, sc, ps, lds, ss, pz, ldz, sz)
+
+
+def tdg_w4_quantize(W, group: int = 128, zeros=False, codes=None, scales=None):
+    """4-bit weights of W (K x N, or count x K x N; float16): (codes, scales,
+    zeros), with zero points where `zeros` is True or a uint8 tensor for them,
+    else None.  codes: ceil(K / 128) x N x 64 uint8 in the layout that the
+    products take; scales (float16) and zeros: ceil(K / group) x N; a stack's
+    have its count in front."""
+    if _INT is None:
+        _types()
+    stack = len(W.shape) == 3
+    if stack:
+        dev = W.get_device()
+        if dev < 0:
+            raise ValueError("W must be a device tensor")
+        count, K, N, pw, ldw, sw = _stack(W, _HALF, "W", dev)
+    else:
+        K, N, pw, ldw, dev = _mat(W, _HALF, "W")
+        count, sw = 1, 0
+    group = int(group)
+    if group < 32 or group % 32:
+        raise ValueError("group must be a multiple of 32, got %d" % group)
+    front, groups, blocks = (count,) if stack else (), (K + group - 1) // group, (K + 127) // 128
+
+    def new(rows, cols, dtype):
+        strides = (rows * cols, cols, 1) if stack else (cols, 1)
+        return _empty(front + (rows, cols), strides, dtype=dtype, device=W.device)
+
+    if codes is None:
+        codes = new(blocks, N * 64, _BYTE[0]).view(front + (blocks, N, 64))
+    if scales is None:
+        scales = new(groups, N, _HALF[0])
+    if zeros is False:
+        zeros = None
+    elif zeros is True:
+        zeros = new(groups, N, _BYTE[0])
+    n, cols, places = _w4(codes, scales, zeros, K, group, dev, stack)
+    if n != count or cols != N:
+        raise ValueError("codes have shape %s, W %s" % (tuple(codes.shape), tuple(W.shape)))
+    _launch("tdg_w4_quantize", dev, count, K, N, group, pw, ldw, sw, *places)
+    return codes, scales, zeros
+
+
+def tdg_w4_dequantize(codes, scales, zeros=None, K=None, group: int = 128, out=None, out_dtype=None):
+    """The weights (code - zero) * scale, K x N or a stack of them, rounded
+    once to `out`'s type (out_dtype, else float16, when allocated here).  K is
+    128 times the codes' blocks, and not more, when not given."""
+    if _INT is None:
+        _types()
+    stack = len(codes.shape) == 4
+    dev = codes.get_device()
+    if dev < 0:
+        raise ValueError("codes must be a device tensor")
+    if K is None:
+        K = codes.shape[-3] * 128 if len(codes.shape) > 2 else 0
+    K, group = int(K), int(group)
+    count, N, places = _w4(codes, scales, zeros, K, group, dev, stack)
+    if out is None:
+        shape, strides = ((count, K, N), (K * N, N, 1)) if stack else ((K, N), (N, 1))
+        out = _empty(shape, strides, dtype=out_dtype or _HALF[0], device=codes.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out has dtype %s, out_dtype is %s" % (out.dtype, out_dtype))
+    if stack:
+        n, rows, cols, po, ldo, so = _stack(out, _FLOATS, "out", dev)
+    else:
+        rows, cols, po, ldo, _ = _mat(out, _FLOATS, "out", dev)
+        n, so = 1, 0
+    if (n, rows, cols) != (count, K, N):
+        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), (count,) * stack + (K, N)))
+    _launch("tdg_w4_dequantize", dev, _FLOATS.index(out.dtype), count, K, N, group, *places, po, ldo, so)
+    return out
+
+
+def gemm_f16w4f32(A, codes, scales, zeros=None, group: int = 128, C=None):
+    """C (float32) = A (M x K, float16) times 4-bit weights as tdg_w4_quantize
+    makes them (zeros None: 8)."""
+    if _INT is None:
+        _types()
+    M, K, pa, lda, dev = _mat(A, _HALF, "A")
+    _, N, (pc, ldc, _, ps, lds, _, pz, ldz, _) = _w4(codes, scales, zeros, K, group, dev, False)
+    if C is None:
+        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
+    Mc, Nc, p_out, ld_out, _ = _mat(C, _SINGLE, "C", dev)
+    if Mc != M or Nc != N:
+        raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
+    _launch("gemm_f16w4f32", dev, M, N, K, int(group), pa, lda, pc, ldc, ps, lds, pz, ldz, p_out, ld_out)
+    return C
+
+
+def gemm_f16w4f32_grouped(A, codes, scales, offsets, zeros=None, group: int = 128, C=None):
+    """C[i] (float32) = A[i] times 4-bit matrix g for the rows offsets[g] <= i <
+    offsets[g + 1] of A (M x K, float16); codes, scales and zeros are stacks.
+    Rows of no group are left as they are."""
+    if _INT is None:
+        _types()
+    M, K, pa, lda, dev = _mat(A, _HALF, "A")
+    count, N, places = _w4(codes, scales, zeros, K, group, dev, True)
+    n_off, p_off = _offsets_of(offsets, dev)
+    if n_off != count:
+        raise ValueError("offsets name %d groups, codes have %d" % (n_off, count))
+    if C is None:
+        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
+    Mc, Nc, p_out, ld_out, _ = _mat(C, _SINGLE, "C", dev)
+    if Mc != M or Nc != N:
+        raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
+    _launch("gemm_f16w4f32_grouped", dev, count, p_off, M, N, K, int(group), pa, lda, *places, p_out, ld_out)
+    return C
+
+
+# ------------------------------------------------------ a layer of experts for a few tokens
+
+TDG_LAYER_MAX_TOKENS = 64
+TDG_LAYER_MAX_TOP_K = 32
+
+
+def tdg_expert_layer_workspace(tokens: int, top_k: int, experts: int, cols: int, inner: int) -> int:
+    """Bytes of workspace that tdg_expert_layer needs."""
+    need = ctypes.c_size_t()
+    rc = _fn("tdg_expert_layer_workspace")(tokens, top_k, experts, cols, inner, ctypes.byref(need))
+    if rc != TDG_OK:
+        raise TdgError(rc, "tdg_expert_layer_workspace")
+    return need.value
+
+
+def tdg_expert_layer(x, ids, weights, up, down, out=None, out_dtype=None, workspace=None):
+    """y[t] = sum over j of weights[t, j] * (h . down[e]), e = ids[t, j], h =
+    silu(x[t] . up[e][:, :inner]) * (x[t] . up[e][:, inner:]).  x: tokens x cols
+    (float16), ids: tokens x top_k (int32; one outside the experts adds nothing),
+    weights: float32 or None (1), up: experts x cols x 2 inner, down: experts x
+    inner x cols (float16); `out` is float16 or float32 (out_dtype, else float16,
+    when allocated here).  Up to 64 tokens with 32 choices each.  The workspace is
+    allocated here when not given."""
+    if _INT is None:
+        _types()
+    tokens, cols, px, ldx, dev = _mat(x, _HALF, "x")
+    rows, top_k, p_ids, ld_ids, _ = _mat(ids, _INT, "ids", dev)
+    if rows != tokens:
+        raise ValueError("x has %d rows, ids %d" % (tokens, rows))
+    pw, ldw = (None, top_k) if weights is None else _weights_of(weights, ids, "weights", dev)
+    n, ku, nu, p_up, ld_up, s_up = _stack(up, _HALF, "up", dev)
+    nd, inner, cd, p_down, ld_down, s_down = _stack(down, _HALF, "down", dev)
+    if ku != cols or cd != cols or nu != 2 * inner or nd != n:
+        raise ValueError("up is %s and down %s; expected experts x %d x 2 inner and experts x inner x %d"
+                         % (tuple(up.shape), tuple(down.shape), cols, cols))
+    if out is None:
+        out = _empty((tokens, cols), (cols, 1), dtype=out_dtype or _HALF[0], device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out has dtype %s, out_dtype is %s" % (out.dtype, out_dtype))
+    orow, oc, po, ldo, _ = _mat(out, _FLOATS, "out", dev)
+    if orow != tokens or oc != cols:
+        raise ValueError("out has shape %s, expected %s" % ((orow, oc), (tokens, cols)))
+    ws, p_ws, ws_bytes = _workspace(workspace, tdg_expert_layer_workspace(tokens, top_k, n, cols, inner), x)
+    _launch("tdg_expert_layer", dev, _FLOATS.index(out.dtype), tokens, top_k, n, cols, inner, px, ldx, p_ids, ld_ids,
+            pw, ldw, p_up, ld_up, s_up, p_down, ld_down, s_down, po, ldo, p_ws, ws_bytes)
+    return out

@@ -1,8 +1,8 @@
 """Build libtdgemm.so, the gfx950 GEMM library, in-tree with hipcc.
 
 The kernel tables for the three dtypes are separate translation units and are
-compiled in parallel with the host API, the copy/transpose ladder and the
-products whose rows pick their own weights.  All
+compiled in parallel with the host API, the copy/transpose ladder, the
+products whose rows pick their own weights, and those of 4-bit weights.  All
 HIP code is compiled for gfx950 only, with packed-FP32 instruction selection
 turned off.
 """
@@ -38,6 +38,8 @@ UNITS = [
     ("tdg_route.hip", [], "tdg_route.o"),
     ("tdg_grouped.hip", [], "tdg_grouped.o"),
     ("tdg_lora.hip", [], "tdg_lora.o"),
+    ("tdg_w4.hip", [], "tdg_w4.o"),
+    ("tdg_layer.hip", [], "tdg_layer.o"),
 ]
 
 

@@ -1,0 +1,436 @@
+// tdg_w4.hip -- 4-bit weights with group scales: quantizing, reading back, and
+// the products that multiply FP16 rows by them, for one matrix and for a stack
+// of experts' matrices whose rows are sorted.
+//
+// A K x N matrix is kept as codes, 4 bits a weight, and for every `group`
+// values of k of a column an FP16 scale s and a zero point z (8 where none are
+// given); the weight is (code - z) * s.  The product is
+//   C[m][n] = sum over groups G of s[G][n] * sum over k in G of A[m][k] * (code[k][n] - z[G][n]).
+// code - z is a whole number of at most 255 and exact in FP16, so the matrix
+// instructions multiply it as it is; the scale joins in FP32, once for each
+// group's (or each 32 k's) sum: no weight is rounded.
+//
+// Codes are laid out for v_mfma_f32_16x16x32_f16, whose lane l takes column l %
+// 16 at k = 8 (l / 16) .. + 7: a column's 128 k are 64 bytes, of which lane
+// group q = l / 16 takes 16: the words of its k in each of four instructions.
+// The nibbles of a word stand so that four masks give them in pairs, two
+// neighbours in k in the halves of a register.
+#include "tdg_kernels.hpp"
+
+#include "tdg_check.h"
+#include "tdg_internal.h"
+
+namespace {
+
+using namespace tdg;
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int BLOCK = 128;  // k in one block of codes: 64 bytes of a column
+
+// Strides in bytes; `codes`' row is a block of k.
+struct Weights4 {
+    const unsigned char *codes, *scales, *zeros;
+    int64_t ld_codes, ld_scales, ld_zeros;              // between blocks, groups
+    int64_t stride_codes, stride_scales, stride_zeros;  // between matrices
+};
+
+// Where bit 0 of k's nibble stands in its word, k = 0 .. 7.
+__device__ __forceinline__ constexpr int nibble_at(int k) { return 4 * (k >> 1) + 16 * (k & 1); }
+
+// ------------------------------------------------------------------ quantizing
+
+struct QuantArgs {
+    const unsigned char *W;
+    int64_t ldw, stride_w;  // bytes
+    Weights4 q;             // written
+    int K, N, group, groups, blocks;
+};
+
+struct ScaleZero {
+    float s, z;
+};
+
+// Scale and zero point of a group that holds values from lo to hi (symmetric:
+// of a magnitude up to hi).  Each step is one correctly rounded FP32 operation.
+template <bool ZEROS>
+__device__ __forceinline__ ScaleZero scale_of(float lo, float hi) {
+    const float s = (float)(_Float16)(ZEROS ? (hi - lo) / 15.0f : hi / 7.0f);
+    if constexpr (!ZEROS) return {s, 8.0f};
+    const float z = rintf(-lo / s);  // s == 0, or infinities: NaN may come out
+    return {s, s > 0.0f && z >= 0.0f ? fminf(z, 15.0f) : 0.0f};
+}
+
+// The code of w: the nearest of the 16 values; the zero point where the scale
+// is 0, and for a weight that has no place (NaN, or infinite under an infinite
+// scale).
+__device__ __forceinline__ uint32_t code_of(float w, ScaleZero g) {
+    const float q = rintf(w / g.s);
+    if (!(g.s > 0.0f) || q != q) return (uint32_t)g.z;
+    return (uint32_t)fminf(fmaxf(q + g.z, 0.0f), 15.0f);
+}
+
+__device__ __forceinline__ float load_weight(const unsigned char *p) { return (float)*(const _Float16 *)p; }
+
+template <bool ZEROS>
+__device__ __forceinline__ void widen(float w, float &lo, float &hi) {  // (a NaN changes nothing)
+    if constexpr (ZEROS) lo = fminf(lo, w), hi = fmaxf(hi, w);
+    else hi = fmaxf(hi, fabsf(w));
+}
+
+template <bool ZEROS>
+__device__ __forceinline__ void store_scale(const QuantArgs &a, int64_t e, int g, int n, ScaleZero v) {
+    *(_Float16 *)(a.q.scales + e * a.q.stride_scales + g * a.q.ld_scales + (int64_t)n * 2) = (_Float16)v.s;
+    if constexpr (ZEROS)
+        *(unsigned char *)(a.q.zeros + e * a.q.stride_zeros + g * a.q.ld_zeros + n) = (unsigned char)v.z;
+}
+
+// Scales of groups of any length: a workgroup has 64 columns of one group, its
+// four waves every fourth k.
+template <bool ZEROS>
+__global__ void __launch_bounds__(256) k_w4_scales(QuantArgs a) {
+    __shared__ float low[4][64], high[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = min((int)blockIdx.x * 64 + lane, a.N - 1), g = blockIdx.y;
+    const int64_t e = blockIdx.z;
+    const int k1 = (int)min((int64_t)a.K, (int64_t)(g + 1) * a.group);
+    const unsigned char *w = a.W + e * a.stride_w + (int64_t)n * 2;
+    float lo = 0.0f, hi = 0.0f;
+#pragma unroll 8
+    for (int64_t k = (int64_t)g * a.group + wave; k < k1; k += 4) widen<ZEROS>(load_weight(w + k * a.ldw), lo, hi);
+    low[wave][lane] = lo, high[wave][lane] = hi;
+    __syncthreads();
+    if (wave || (int)blockIdx.x * 64 + lane >= a.N) return;
+    for (int i = 1; i < 4; i++) lo = fminf(lo, low[i][lane]), hi = fmaxf(hi, high[i][lane]);
+    store_scale<ZEROS>(a, e, g, n, scale_of<ZEROS>(lo, hi));
+}
+
+// Codes under scales that are there: a thread has a column of a block.
+template <bool ZEROS>
+__global__ void __launch_bounds__(256) k_w4_codes(QuantArgs a) {
+    const int n = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+    const int64_t e = blockIdx.z;
+    if (n >= a.N) return;
+    const unsigned char *w = a.W + e * a.stride_w + (int64_t)b * BLOCK * a.ldw + (int64_t)n * 2;
+    u32x4 word[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {  // 32 k: all in one group
+        if (b * BLOCK + 32 * j >= a.K) break;
+        const int g = (b * BLOCK + 32 * j) / a.group;
+        ScaleZero v;
+        v.s = load_weight(a.q.scales + e * a.q.stride_scales + g * a.q.ld_scales + (int64_t)n * 2);
+        v.z = ZEROS ? (float)a.q.zeros[e * a.q.stride_zeros + g * a.q.ld_zeros + n] : 8.0f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int k = 32 * j + 8 * q + i;
+                if (b * BLOCK + k < a.K) bits |= code_of(load_weight(w + k * a.ldw), v) << nibble_at(i);
+            }
+            word[q][j] = bits;
+        }
+    }
+    u32x4 *out = (u32x4 *)(a.q.codes + e * a.q.stride_codes + b * a.q.ld_codes + (int64_t)n * 64);
+#pragma unroll
+    for (int q = 0; q < 4; q++) out[q] = word[q];
+}
+
+// Weights from codes: a thread has a column of a block.
+template <typename T, bool ZEROS>
+__global__ void __launch_bounds__(256) k_w4_values(QuantArgs a) {
+    const int n = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+    const int64_t e = blockIdx.z;
+    if (n >= a.N) return;
+    unsigned char *w = (unsigned char *)a.W + e * a.stride_w + (int64_t)b * BLOCK * a.ldw + (int64_t)n * sizeof(T);
+    const u32x4 *in = (const u32x4 *)(a.q.codes + e * a.q.stride_codes + b * a.q.ld_codes + (int64_t)n * 64);
+    u32x4 word[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) word[q] = in[q];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (b * BLOCK + 32 * j >= a.K) break;
+        const int g = (b * BLOCK + 32 * j) / a.group;
+        const float s = load_weight(a.q.scales + e * a.q.stride_scales + g * a.q.ld_scales + (int64_t)n * 2);
+        const float z = ZEROS ? (float)a.q.zeros[e * a.q.stride_zeros + g * a.q.ld_zeros + n] : 8.0f;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int k = 32 * j + 8 * q + i;
+                if (b * BLOCK + k < a.K)
+                    *(T *)(w + k * a.ldw) = (T)(((float)(word[q][j] >> nibble_at(i) & 15) - z) * s);
+            }
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+struct W4Args {
+    const unsigned char *A;
+    float *C;
+    int64_t lda, ldc;  // bytes
+    Weights4 w;
+    const int32_t *offsets;  // groups of rows; NULL: all rows have the first matrix
+    int row_groups, rows;
+    int N, K, group, blocks;
+};
+
+// Eight codes of a word, less the zero point, as FP16 in the order of k.  1024
+// + q and 1024 + 16 q are FP16's bit patterns of nibbles set below its exponent;
+// both differences are exact.
+__device__ __forceinline__ f16x8 code_values(uint32_t word, f16x2 z1024, f16x2 z64) {
+    const uint32_t high = word >> 8;
+    f16x2 v[4];
+    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+    v[0] = __builtin_bit_cast(f16x2, (word & 0x000f000fu) | 0x64006400u) - z1024;
+    v[1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (word & 0x00f000f0u) | 0x64006400u), sixteenth, -z64);
+    v[2] = __builtin_bit_cast(f16x2, (high & 0x000f000fu) | 0x64006400u) - z1024;
+    v[3] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (high & 0x00f000f0u) | 0x64006400u), sixteenth, -z64);
+    return f16x8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+}
+
+// Few rows: a workgroup has 16 CT columns and up to 16 MT rows, and its eight
+// waves a part of k each, which LDS joins in order.
+constexpr int FEW_WAVES = 8;
+
+template <int MT, int CT, bool ZEROS>
+__global__ void __launch_bounds__(FEW_WAVES * 64) k_w4_few(W4Args p) {
+    __shared__ float part[FEW_WAVES][CT * 4 * 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
+    int lo = 0, hi = p.rows;
+    Weights4 w = p.w;
+    if (p.offsets) {
+        const int g = blockIdx.y;
+        lo = min(max(p.offsets[g], 0), p.rows), hi = min(max(p.offsets[g + 1], 0), p.rows);
+        w.codes += g * w.stride_codes, w.scales += g * w.stride_scales, w.zeros += g * w.stride_zeros;
+    }
+    const int per = (p.blocks + FEW_WAVES - 1) / FEW_WAVES;
+    const int b0 = min(p.blocks, wave * per), b1 = min(p.blocks, b0 + per);
+    const unsigned char *code[CT];
+    int col[CT];
+#pragma unroll
+    for (int t = 0; t < CT; t++) {
+        col[t] = min((int)blockIdx.x * 16 * CT + t * 16 + c, p.N - 1);
+        code[t] = w.codes + (int64_t)col[t] * 64 + q * 16;
+    }
+    for (int m0 = lo + (int)blockIdx.z * 16 * MT; m0 < hi; m0 += (int)gridDim.z * 16 * MT) {
+        f32x4 acc[MT][CT] = {};
+        for (int b = b0; b < b1; b++) {
+            u32x4 word[CT];
+#pragma unroll
+            for (int t = 0; t < CT; t++) word[t] = *(const u32x4 *)(code[t] + b * w.ld_codes);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int k = b * BLOCK + 32 * j;
+                if (k >= p.K) break;
+                const int g = k / p.group, kl = k + 8 * q;
+                f16x8 x[MT];
+#pragma unroll
+                for (int i = 0; i < MT; i++) {
+                    const int m = m0 + i * 16 + c;
+                    const unsigned char *at = p.A + (int64_t)m * p.lda + (int64_t)kl * 2;
+                    x[i] = f16x8{};
+                    if (m < hi && kl + 8 <= p.K) {
+                        x[i] = __builtin_bit_cast(f16x8, load16_global(at));
+                    } else if (m < hi) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            if (kl + e < p.K) x[i][e] = *(const _Float16 *)(at + e * 2);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < CT; t++) {
+                    const float s = load_weight(w.scales + g * w.ld_scales + (int64_t)col[t] * 2);
+                    const _Float16 z = ZEROS ? (_Float16)(float)w.zeros[g * w.ld_zeros + col[t]] : (_Float16)8.0f;
+                    const _Float16 z1024 = z + (_Float16)1024.0f, z64 = z + (_Float16)64.0f;
+                    const f16x8 v = code_values(word[t][j], f16x2{z1024, z1024}, f16x2{z64, z64});
+#pragma unroll
+                    for (int i = 0; i < MT; i++) {
+                        const f32x4 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[i], v, f32x4{}, 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < 4; r++) acc[i][t][r] = fmaf(s, sum[r], acc[i][t][r]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < CT; t++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) part[wave][(t * 4 + r) * 64 + lane] = acc[i][t][r];
+            __syncthreads();
+            for (int e = tid; e < CT * 256; e += FEW_WAVES * 64) {
+                float sum = part[0][e];
+#pragma unroll
+                for (int v = 1; v < FEW_WAVES; v++) sum += part[v][e];
+                const int m = m0 + i * 16 + (e >> 4 & 3) * 4 + (e >> 6 & 3);
+                const int n = (int)blockIdx.x * 16 * CT + (e >> 8) * 16 + (e & 15);
+                if (m < hi && n < p.N) *(float *)((unsigned char *)p.C + (int64_t)m * p.ldc + (int64_t)n * 4) = sum;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+int launch(const void *fn, dim3 grid, int threads, void *args, void *stream) {
+    void *kargs[] = {args};
+    if (hipLaunchKernel(fn, grid, dim3((unsigned)threads), kargs, 0, (hipStream_t)stream) != hipSuccess)
+        return TDG_ERR_LAUNCH;
+    if (hipGetLastError() != hipSuccess) return TDG_ERR_LAUNCH;
+    return TDG_OK;
+}
+
+// A stack of 4-bit matrices as a caller names it, and its checks.
+struct Named4 {
+    int64_t count, K, N, group;
+    const void *codes;
+    int64_t ld_codes, stride_codes;
+    const void *scales;
+    int64_t ld_scales, stride_scales;
+    const void *zeros;
+    int64_t ld_zeros, stride_zeros;
+
+    int64_t blocks() const { return ceil_quot(K, BLOCK); }
+    int64_t groups() const { return ceil_quot(K, group); }
+    bool ok(bool written) const {
+        if (count < 0 || !size_ok(count) || !size_ok(K) || !size_ok(N) || group < 32 || group % 32 || !size_ok(group))
+            return false;
+        return stack_ok(codes, count, stride_codes, blocks(), N, ld_codes, 64, written) && aligned_to(codes, 16) &&
+               stack_ok(scales, count, stride_scales, groups(), N, ld_scales, 2, written) && aligned_to(scales, 2) &&
+               (!zeros || stack_ok(zeros, count, stride_zeros, groups(), N, ld_zeros, 1, written));
+    }
+    uint64_t bytes(int i) const {
+        return i == 0   ? span_bytes(blocks(), N, ld_codes, 64, count, stride_codes)
+               : i == 1 ? span_bytes(groups(), N, ld_scales, 2, count, stride_scales)
+                        : span_bytes(groups(), N, ld_zeros, 1, count, stride_zeros);
+    }
+    const void *array(int i) const { return i == 0 ? codes : i == 1 ? scales : zeros; }
+    bool apart_from(const void *p, uint64_t len) const {
+        for (int i = 0; i < 3; i++)
+            if (overlaps(array(i), bytes(i), p, len)) return false;
+        return true;
+    }
+    Weights4 device() const {
+        Weights4 w;
+        w.codes = (const unsigned char *)codes, w.scales = (const unsigned char *)scales;
+        w.zeros = (const unsigned char *)zeros;
+        w.ld_codes = ld_codes * 64, w.ld_scales = ld_scales * 2, w.ld_zeros = ld_zeros;
+        w.stride_codes = stride_codes * 64, w.stride_scales = stride_scales * 2, w.stride_zeros = stride_zeros;
+        return w;
+    }
+};
+
+QuantArgs quant_args(const Named4 &q, const void *W, int64_t ldw, int64_t stride_w, int64_t es) {
+    QuantArgs a;
+    a.W = (const unsigned char *)W, a.ldw = ldw * es, a.stride_w = stride_w * es, a.q = q.device();
+    a.K = (int)q.K, a.N = (int)q.N, a.group = (int)q.group, a.groups = (int)q.groups(), a.blocks = (int)q.blocks();
+    return a;
+}
+
+bool grid_ok(const dim3 &g, int64_t threads) {
+    return g.y <= 65535 && g.z <= 65535 && (uint64_t)g.x * g.y * g.z <= (uint64_t)UINT32_MAX / threads;
+}
+
+dim3 grid_of(int64_t x, int64_t y, int64_t z) {  // (what does not fit is refused by grid_ok)
+    auto cap = [](int64_t v) { return (unsigned)(v < 65536 ? v : 65536); };
+    return dim3((unsigned)x, cap(y), cap(z));
+}
+
+int run_product(int64_t row_groups, const int32_t *offsets, int64_t M, const Named4 &q, const void *A, int64_t lda,
+                float *C, int64_t ldc, void *stream) {
+    if (!q.ok(false) || row_groups > 1024 || !size_ok(M) || !matrix_ok(A, M, q.K, lda, 2) ||
+        !matrix_ok(C, M, q.N, ldc, 4) || !aligned_to(A, 2) || !aligned_to(C, 4) || !aligned_to(offsets, 4))
+        return TDG_ERR_INVALID_ARG;
+    const uint64_t c_len = span_bytes(M, q.N, ldc, 4);
+    if (!q.apart_from(C, c_len) || overlaps(C, c_len, A, span_bytes(M, q.K, lda, 2)) ||
+        (offsets && overlaps(C, c_len, offsets, (uint64_t)(row_groups + 1) * 4)))
+        return TDG_ERR_INVALID_ARG;
+    if (M == 0 || q.N == 0 || row_groups == 0) return TDG_OK;
+    W4Args p;
+    p.A = (const unsigned char *)A, p.C = C, p.lda = lda * 2, p.ldc = ldc * 4, p.w = q.device();
+    p.offsets = offsets, p.row_groups = (int)row_groups, p.rows = (int)M;
+    p.N = (int)q.N, p.K = (int)q.K, p.group = (int)q.group, p.blocks = (int)q.blocks();
+    const int64_t most = offsets ? 1 : ceil_quot(M, 64);
+    dim3 grid = grid_of(ceil_quot(q.N, 32), row_groups, most > 65535 ? 65535 : most);
+    if (!grid_ok(grid, FEW_WAVES * 64)) return TDG_ERR_UNSUPPORTED;
+    const int rc = device_check();
+    if (rc != TDG_OK) return rc;
+    const void *fn = q.zeros ? (const void *)&k_w4_few<4, 2, true> : (const void *)&k_w4_few<4, 2, false>;
+    return launch(fn, grid, FEW_WAVES * 64, &p, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int tdg_w4_quantize(int64_t count, int64_t K, int64_t N, int64_t group, const uint16_t *W, int64_t ldw,
+                    int64_t stride_w, uint8_t *codes, int64_t ld_codes, int64_t stride_codes, uint16_t *scales,
+                    int64_t ld_scales, int64_t stride_scales, uint8_t *zeros, int64_t ld_zeros, int64_t stride_zeros,
+                    void *stream) {
+    const Named4 q = {count, K, N, group, codes, ld_codes, stride_codes, scales, ld_scales, stride_scales,
+                      zeros, ld_zeros, stride_zeros};
+    if (!q.ok(true) || !stack_ok(W, count, stride_w, K, N, ldw, 2, false) || !aligned_to(W, 2) ||
+        !q.apart_from(W, span_bytes(K, N, ldw, 2, count, stride_w)) || overlaps(codes, q.bytes(0), scales, q.bytes(1)) ||
+        overlaps(codes, q.bytes(0), zeros, q.bytes(2)) || overlaps(scales, q.bytes(1), zeros, q.bytes(2)))
+        return TDG_ERR_INVALID_ARG;
+    if (count == 0 || K == 0 || N == 0) return TDG_OK;
+    QuantArgs a = quant_args(q, W, ldw, stride_w, 2);
+    const dim3 scale_grid = grid_of(ceil_quot(N, 64), q.groups(), count);
+    const dim3 code_grid = grid_of(ceil_quot(N, 256), q.blocks(), count);
+    if (!grid_ok(scale_grid, 256) || !grid_ok(code_grid, 256)) return TDG_ERR_UNSUPPORTED;
+    int rc = device_check();
+    if (rc != TDG_OK) return rc;
+    rc = launch(zeros ? (const void *)&k_w4_scales<true> : (const void *)&k_w4_scales<false>, scale_grid, 256, &a,
+                stream);
+    if (rc != TDG_OK) return rc;
+    return launch(zeros ? (const void *)&k_w4_codes<true> : (const void *)&k_w4_codes<false>, code_grid, 256, &a,
+                  stream);
+}
+
+int tdg_w4_dequantize(int out_elem, int64_t count, int64_t K, int64_t N, int64_t group, const uint8_t *codes,
+                      int64_t ld_codes, int64_t stride_codes, const uint16_t *scales, int64_t ld_scales,
+                      int64_t stride_scales, const uint8_t *zeros, int64_t ld_zeros, int64_t stride_zeros, void *W,
+                      int64_t ldw, int64_t stride_w, void *stream) {
+    if (out_elem != TDG_ELEM_F16 && out_elem != TDG_ELEM_F32) return TDG_ERR_INVALID_ARG;
+    const bool half = out_elem == TDG_ELEM_F16;
+    const int64_t es = half ? 2 : 4;
+    const Named4 q = {count, K, N, group, codes, ld_codes, stride_codes, scales, ld_scales, stride_scales,
+                      zeros, ld_zeros, stride_zeros};
+    if (!q.ok(false) || !stack_ok(W, count, stride_w, K, N, ldw, es, true) || !aligned_to(W, es) ||
+        !q.apart_from(W, span_bytes(K, N, ldw, es, count, stride_w)))
+        return TDG_ERR_INVALID_ARG;
+    if (count == 0 || K == 0 || N == 0) return TDG_OK;
+    QuantArgs a = quant_args(q, W, ldw, stride_w, es);
+    const dim3 grid = grid_of(ceil_quot(N, 256), q.blocks(), count);
+    if (!grid_ok(grid, 256)) return TDG_ERR_UNSUPPORTED;
+    const int rc = device_check();
+    if (rc != TDG_OK) return rc;
+    const void *fn = half ? (zeros ? (const void *)&k_w4_values<_Float16, true> : (const void *)&k_w4_values<_Float16, false>)
+                          : (zeros ? (const void *)&k_w4_values<float, true> : (const void *)&k_w4_values<float, false>);
+    return launch(fn, grid, 256, &a, stream);
+}
+
+int gemm_f16w4f32(int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *A, int64_t lda,
+                  const uint8_t *codes, int64_t ld_codes, const uint16_t *scales, int64_t ld_scales,
+                  const uint8_t *zeros, int64_t ld_zeros, float *C, int64_t ldc, void *stream) {
+    const Named4 q = {1, K, N, group, codes, ld_codes, 0, scales, ld_scales, 0, zeros, ld_zeros, 0};
+    return run_product(1, nullptr, M, q, A, lda, C, ldc, stream);
+}
+
+int gemm_f16w4f32_grouped(int64_t groups, const int32_t *offsets, int64_t M, int64_t N, int64_t K, int64_t group,
+                          const uint16_t *A, int64_t lda, const uint8_t *codes, int64_t ld_codes,
+                          int64_t stride_codes, const uint16_t *scales, int64_t ld_scales, int64_t stride_scales,
+                          const uint8_t *zeros, int64_t ld_zeros, int64_t stride_zeros, float *C, int64_t ldc,
+                          void *stream) {
+    const Named4 q = {groups, K, N, group, codes, ld_codes, stride_codes, scales, ld_scales, stride_scales,
+                      zeros, ld_zeros, stride_zeros};
+    if (groups > 0 && !offsets) return TDG_ERR_INVALID_ARG;
+    return run_product(groups, offsets, M, q, A, lda, C, ldc, stream);
+}
+
+}  // extern "C"
