@@ -15,7 +15,7 @@
 // group q = l / 16 takes 16: the words of its k in each of four instructions.
 // The nibbles of a word stand so that four masks give them in pairs, two
 // neighbours in k in the halves of a register.
-#include "tdg_kernels.hpp"
+#include "tdg_grouped.hpp"
 
 #include "tdg_check.h"
 #include "tdg_internal.h"
@@ -175,6 +175,8 @@ struct W4Args {
     const int32_t *offsets;  // groups of rows; NULL: all rows have the first matrix
     int row_groups, rows;
     int N, K, group, blocks;
+    int tiles_m, tiles_n;  // k_w4_tile
+    int flags;             // TDG_DEBUG_* bits
 };
 
 // Eight codes of a word, less the zero point, as FP16 in the order of k.  1024
@@ -275,6 +277,185 @@ __global__ void __launch_bounds__(FEW_WAVES * 64) k_w4_few(W4Args p) {
     }
 }
 
+// Many rows: a workgroup of four waves has 16 MT rows and 64 CT columns, each
+// wave all the rows and a fourth of the columns, so that no weight is unpacked
+// twice in a workgroup.  A ring of LDS buffers is filled by the global-to-LDS
+// DMA, one block of 128 k each: A's rows (256 bytes each, 16-byte pieces at
+// piece ^ (row % 16)), the waves' codes (64 bytes a column, pieces at piece ^
+// (column / 4 % 4); both keep fragment reads free of bank conflicts) and their
+// scales and zero points, a word for each column.  A block's codes become
+// fragments in registers; then row by row of 16 the instructions of SPAN * 32 k
+// run on a sum of their own, which joins the accumulators times the scale.
+template <int MT_, int CT_, int SPAN_, bool ZEROS_, int STAGES_>
+struct W4Tile {
+    static constexpr int MT = MT_, CT = CT_, SPAN = SPAN_, STAGES = STAGES_;
+    static constexpr bool ZEROS = ZEROS_;
+    static constexpr int BM = 16 * MT, BN = 64 * CT, WAVES = 4, THREADS = 256;
+    static constexpr int SCALES = 4 / SPAN;  // scales of a column in a block
+    static constexpr int A_BYTES = BM * 256, CODE_BYTES = CT * 1024, SCALE_BYTES = SCALES * 256;
+    static constexpr int WAVE_BYTES = CODE_BYTES + SCALE_BYTES * (ZEROS ? 2 : 1);
+    static constexpr int STAGE = A_BYTES + WAVES * WAVE_BYTES;
+    static constexpr int COPIES = MT + CT + SCALES * (ZEROS ? 2 : 1);  // of a wave, for each block
+    static_assert(STAGES >= 2 && STAGES <= 4 && COPIES * (STAGES - 2) <= 63 && STAGES * STAGE <= 160 * 1024, "ring");
+};
+
+// As copy_to_lds, 2 bytes (1 byte) of each lane's address to the word at m0 + 4 lane.
+template <int BYTES>
+__device__ __forceinline__ void copy_word_to_lds(uint64_t src, uint32_t m0) {
+    static_assert(BYTES == 1 || BYTES == 2, "what a word is made of");
+    if constexpr (BYTES == 2)
+        asm volatile("s_nop 0\n\tglobal_load_lds_ushort %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+    else
+        asm volatile("s_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+}
+
+template <class T>
+__device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int x0, int hi, int y0,
+                                        unsigned char *smem) {
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t lds = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)smem;
+    const int n0 = y0 + wave * 16 * T::CT;
+    // A's copies: rows 16 i + tid / 16, of which the last one stands for all behind it.
+    const int piece = (tid & 15) ^ (tid >> 4 & 15);
+    uint32_t a_off[T::MT];
+#pragma unroll
+    for (int i = 0; i < T::MT; i++)
+        a_off[i] = (uint32_t)((int64_t)min(i * 16 + (tid >> 4), hi - 1 - x0) * p.lda + piece * 16);
+    const unsigned char *a_base = p.A + (int64_t)x0 * p.lda;
+    const int own = min(n0 + (T::CT == 4 ? lane : lane % (16 * T::CT)), p.N - 1);  // the lane's column of scales
+
+    auto issue = [&](int b) {
+        const uint32_t at = lds + (uint32_t)(b % T::STAGES) * T::STAGE, mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
+        const unsigned char *base = a_base + (int64_t)b * 256;
+        const int left = p.K - b * BLOCK;
+        if (left >= BLOCK) {
+#pragma unroll
+            for (int i = 0; i < T::MT; i++) copy_to_lds(base, a_off[i], at + i * 4096 + wave * 1024);
+        } else {
+            // The last block, which the end of k cuts: pieces behind it are zeros,
+            // and the one that it cuts is written element by element.
+            const int have = left - piece * 8;
+#pragma unroll
+            for (int i = 0; i < T::MT; i++) {
+                const unsigned char *src = base + a_off[i];
+                if (have >= 8 || have <= 0) {
+                    copy_to_lds(have > 0 ? (uint64_t)(uintptr_t)src : (uint64_t)(uintptr_t)tdg_zero16,
+                                at + i * 4096 + wave * 1024);
+                } else {
+                    f16x8 v = {};
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (e < have) v[e] = *(const _Float16 *)(src + e * 2);
+                    lds_write16(smem + (b % T::STAGES) * T::STAGE + i * 4096 + tid * 16, __builtin_bit_cast(u32x4, v));
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < T::CT; t++) {
+            const int col = min(n0 + t * 16 + (lane >> 2), p.N - 1), from = (lane & 3) ^ (lane >> 4 & 3);
+            copy_to_lds((uint64_t)(uintptr_t)(w.codes + b * w.ld_codes + (int64_t)col * 64 + from * 16),
+                        mine + t * 1024);
+        }
+#pragma unroll
+        for (int g = 0; g < T::SCALES; g++) {
+            const int k = min(b * BLOCK + g * 32 * T::SPAN, p.K - 1);
+            const int64_t row = k / p.group;
+            copy_word_to_lds<2>((uint64_t)(uintptr_t)(w.scales + row * w.ld_scales + (int64_t)own * 2),
+                                mine + T::CODE_BYTES + g * 256);
+            if constexpr (T::ZEROS)
+                copy_word_to_lds<1>((uint64_t)(uintptr_t)(w.zeros + row * w.ld_zeros + own),
+                                    mine + T::CODE_BYTES + T::SCALE_BYTES + g * 256);
+        }
+    };
+
+    f32x4 acc[T::MT][T::CT] = {};
+#pragma unroll
+    for (int b = 0; b < T::STAGES - 1; b++)
+        if (b < p.blocks) issue(b);
+    uint32_t a_at[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) a_at[j] = (uint32_t)(c * 256 + (((4 * j + q) ^ c) << 4));
+    for (int b = 0; b < p.blocks; b++) {
+        const int later = min(T::STAGES - 2, p.blocks - 1 - b);  // blocks whose copies may stay in flight
+        if (T::STAGES >= 4 && later == 2) wait_vmcnt<(T::STAGES >= 4 ? 2 : 0) * T::COPIES>();
+        else if (T::STAGES >= 3 && later >= 1) wait_vmcnt<(T::STAGES >= 3 ? 1 : 0) * T::COPIES>();
+        else wait_vmcnt<0>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (b + T::STAGES - 1 < p.blocks) issue(b + T::STAGES - 1);
+        const unsigned char *at = smem + (b % T::STAGES) * T::STAGE, *mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
+        f16x8 v[T::CT][4];
+        float scale[T::CT][T::SCALES];
+#pragma unroll
+        for (int t = 0; t < T::CT; t++) {
+            const u32x4 word = lds_read16(mine + t * 1024 + c * 64 + ((q ^ (c >> 2)) << 4));
+#pragma unroll
+            for (int g = 0; g < T::SCALES; g++) {
+                const uint32_t bits = *(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + g * 256 + (t * 16 + c) * 4);
+                scale[t][g] = b * BLOCK + g * 32 * T::SPAN < p.K ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits) : 0.0f;
+                f16x2 z1024 = {(_Float16)1032.0f, (_Float16)1032.0f}, z64 = {(_Float16)72.0f, (_Float16)72.0f};
+                if constexpr (T::ZEROS) {
+                    const float z = (float)*(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + T::SCALE_BYTES + g * 256 +
+                                                                       (t * 16 + c) * 4);
+                    z1024[0] = z1024[1] = (_Float16)(z + 1024.0f), z64[0] = z64[1] = (_Float16)(z + 64.0f);
+                }
+#pragma unroll
+                for (int j = g * T::SPAN; j < (g + 1) * T::SPAN; j++) v[t][j] = code_values(word[j], z1024, z64);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < T::MT; i++) {
+            f16x8 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) x[j] = __builtin_bit_cast(f16x8, lds_read16(at + i * 4096 + a_at[j]));
+#pragma unroll
+            for (int g = 0; g < T::SCALES; g++) {
+                f32x4 sum[T::CT] = {};
+#pragma unroll
+                for (int j = g * T::SPAN; j < (g + 1) * T::SPAN; j++)
+#pragma unroll
+                    for (int t = 0; t < T::CT; t++)
+                        sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], v[t][j], sum[t], 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < T::CT; t++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++) acc[i][t][r] = fmaf(scale[t][g], sum[t][r], acc[i][t][r]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < T::MT; i++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int m = x0 + i * 16 + q * 4 + r;
+            if (m >= hi) continue;
+            float *out = (float *)((unsigned char *)p.C + (int64_t)m * p.ldc) + n0 + c;
+#pragma unroll
+            for (int t = 0; t < T::CT; t++)
+                if (n0 + t * 16 + c < p.N) out[t * 16] = acc[i][t][r];
+        }
+}
+
+template <int MT, int CT, int SPAN, bool ZEROS, int STAGES>
+__global__ void __launch_bounds__(256) k_w4_tile(W4Args p) {
+    typedef W4Tile<MT, CT, SPAN, ZEROS, STAGES> T;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[STAGES * T::STAGE];
+    poison_lds<STAGES * T::STAGE, T::THREADS>(p.flags, smem);
+    Weights4 w = p.w;
+    if (!p.offsets) {
+        int tm, tn;
+        map_tile(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+        w4_tile<T>(p, w, tm * T::BM, p.rows, tn * T::BN, smem);
+        return;
+    }
+    GroupedArgs a;
+    a.offsets = p.offsets, a.groups = p.row_groups, a.rows = p.rows, a.tiles_n = p.tiles_n;
+    const GroupedTile t = find_tile<LAY_NN, T::BM, false>(a, blockIdx.x);
+    if (!t.ok) return;
+    w.codes += t.g * w.stride_codes, w.scales += t.g * w.stride_scales, w.zeros += t.g * w.stride_zeros;
+    w4_tile<T>(p, w, t.x0, t.hi, t.tn * T::BN, smem);
+}
+
 // ------------------------------------------------------------------ host side
 
 int launch(const void *fn, dim3 grid, int threads, void *args, void *stream) {
@@ -341,6 +522,47 @@ dim3 grid_of(int64_t x, int64_t y, int64_t z) {  // (what does not fit is refuse
     return dim3((unsigned)x, cap(y), cap(z));
 }
 
+struct Variant4 {
+    const void *fn;
+    dim3 grid;
+    int threads;
+};
+
+template <int MT, int CT, int SPAN, bool ZEROS>
+const void *tile_fn() {
+    // Three buffers where they fit.
+    constexpr int three = 3 * W4Tile<MT, CT, SPAN, ZEROS, 2>::STAGE <= 160 * 1024 ? 3 : 2;
+    return (const void *)&k_w4_tile<MT, CT, SPAN, ZEROS, three>;
+}
+
+template <int MT, int CT>
+const void *tile_fn(int64_t group, bool zeros) {
+    if (group % 128 == 0) return zeros ? tile_fn<MT, CT, 4, true>() : tile_fn<MT, CT, 4, false>();
+    if (group % 64 == 0) return zeros ? tile_fn<MT, CT, 2, true>() : tile_fn<MT, CT, 2, false>();
+    return zeros ? tile_fn<MT, CT, 1, true>() : tile_fn<MT, CT, 1, false>();
+}
+
+Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
+    const int64_t live = p.offsets ? (p.row_groups < p.rows ? p.row_groups : p.rows) : 1;
+    // The DMA's lanes reach a tile's rows with 32-bit byte offsets.
+    const bool far = lda > (int64_t)UINT32_MAX / 2 / 128 - 256;
+    if (p.rows <= 64 * live || far || p.blocks == 0) {
+        const int64_t most = p.offsets ? 1 : ceil_quot(p.rows, 64);
+        return {q.zeros ? (const void *)&k_w4_few<4, 2, true> : (const void *)&k_w4_few<4, 2, false>,
+                grid_of(ceil_quot(q.N, 32), p.row_groups, most > 65535 ? 65535 : most), FEW_WAVES * 64};
+    }
+    auto tiles = [&](int64_t bm, int64_t bn) {
+        const int64_t m = p.offsets ? p.rows / bm + live : ceil_quot(p.rows, bm);
+        return m * ceil_quot(q.N, bn);
+    };
+    const bool wide = tiles(128, 256) >= 256;
+    const int bn = wide ? 256 : 128;
+    p.tiles_m = (int)ceil_quot(p.rows, 128), p.tiles_n = (int)ceil_quot(q.N, bn);
+    const int64_t grid = p.offsets ? ceil_quot(tiles(128, bn), 8) * 8 : tiles(128, bn);
+    return {wide ? tile_fn<8, 4>(q.group, q.zeros) : tile_fn<8, 2>(q.group, q.zeros),
+            dim3((unsigned)(grid > UINT32_MAX ? UINT32_MAX : grid)), 256};
+}
+
 int run_product(int64_t row_groups, const int32_t *offsets, int64_t M, const Named4 &q, const void *A, int64_t lda,
                 float *C, int64_t ldc, void *stream) {
     if (!q.ok(false) || row_groups > 1024 || !size_ok(M) || !matrix_ok(A, M, q.K, lda, 2) ||
@@ -355,13 +577,12 @@ int run_product(int64_t row_groups, const int32_t *offsets, int64_t M, const Nam
     p.A = (const unsigned char *)A, p.C = C, p.lda = lda * 2, p.ldc = ldc * 4, p.w = q.device();
     p.offsets = offsets, p.row_groups = (int)row_groups, p.rows = (int)M;
     p.N = (int)q.N, p.K = (int)q.K, p.group = (int)q.group, p.blocks = (int)q.blocks();
-    const int64_t most = offsets ? 1 : ceil_quot(M, 64);
-    dim3 grid = grid_of(ceil_quot(q.N, 32), row_groups, most > 65535 ? 65535 : most);
-    if (!grid_ok(grid, FEW_WAVES * 64)) return TDG_ERR_UNSUPPORTED;
+    p.flags = debug_flags_now();
+    const Variant4 v = choose(p, q, lda);
+    if (!grid_ok(v.grid, v.threads)) return TDG_ERR_UNSUPPORTED;
     const int rc = device_check();
     if (rc != TDG_OK) return rc;
-    const void *fn = q.zeros ? (const void *)&k_w4_few<4, 2, true> : (const void *)&k_w4_few<4, 2, false>;
-    return launch(fn, grid, FEW_WAVES * 64, &p, stream);
+    return launch(v.fn, v.grid, v.threads, &p, stream);
 }
 
 }  // namespace
