@@ -433,6 +433,58 @@ def test_grouped_one_matrix_for_all_groups(lib):
     near(lib.gemm_f16w4f32_grouped(x.cuda(), codes, scales, off, z, 96), x.double() @ w.value, bound(x, w.value, 200))
 
 
+# ------------------------------------------------------------------ every tile
+
+# (rows, matrices or 0 for the plain product, N, K): 128 x 512, 64 x 256, 64 x 128,
+# 32 x 128 and 32 x 64 tiles and the kernels of few rows, by the rule that picks them.
+TILES = [(1030, 0, 13000, 130), (1100, 0, 6000, 155), (700, 0, 3000, 256), (70, 0, 8200, 300), (130, 0, 3900, 200),
+         (40, 0, 4100, 129), (24, 0, 4100, 384), (9, 0, 300, 8200), (2100, 2, 6600, 70), (2000, 6, 3300, 257),
+         (1000, 5, 2000, 128), (700, 40, 800, 200), (300, 20, 300, 391), (150, 30, 500, 140)]
+
+
+@pytest.mark.parametrize("rows,groups,N,K", TILES)
+@pytest.mark.parametrize("group", [32, 64, 128, 96])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_every_tile_is_exact_on_whole_numbers(lib, rows, groups, N, K, group, zeros):
+    """Whole numbers against 64 bits; and the same with LDS full of NaN first,
+    which a read of a buffer that is not filled yet would show."""
+    r = rng(rows, groups, N, K, group)
+    ws = [Weights(r, K, N, group, zeros, whole=True) for _ in range(min(groups, 3) or 1)]
+    x = torch.from_numpy(r.integers(-3, 4, (rows, K))).to(F16)
+    X = x.cuda()
+    if groups:
+        ws = [ws[g % len(ws)] for g in range(groups)]
+        off = offsets_of(r, rows, groups)
+        codes, scales, z = stacked(ws)
+        d = torch.tensor(off, dtype=torch.int32).cuda()
+        run = lambda: lib.gemm_f16w4f32_grouped(X, codes, scales, d, z, group)  # noqa: E731
+        want = torch.cat([x[off[g]:off[g + 1]].double() @ ws[g].value for g in range(groups)])
+    else:
+        run = lambda: lib.gemm_f16w4f32(X, *ws[0].all, group=group)  # noqa: E731
+        want = x.double() @ ws[0].value
+    assert torch.equal(run().cpu().double(), want)
+    old = lib.tdg_set_debug_flags(lib.TDG_DEBUG_POISON_LDS)
+    try:
+        assert torch.equal(run().cpu().double(), want)
+    finally:
+        lib.tdg_set_debug_flags(old)
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 8200, 261), (700, 3000, 133), (1100, 6000, 100), (1030, 13000, 135)])
+def test_tiles_of_strided_rows_that_end_with_their_page(lib, M, N, K):
+    """Rows off any grid, NaN between them and behind the last; C's
+    surroundings stay."""
+    r = rng(M, N, K)
+    w, x = Weights(r, K, N, 64, True), normal(r, M, K)
+    wide = torch.full((M, K + 3), float("nan"), dtype=F16)
+    wide[:, 3:] = x
+    C = torch.full((M + 1, N + 2), -5.0, device="cuda")
+    lib.gemm_f16w4f32(at_page_end(wide)[:, 3:], *w.all, group=64, C=C[:M, 1:1 + N])
+    near(C[:M, 1:1 + N], x.double() @ w.value, bound(x, w.value, K))
+    C[:M, 1:1 + N] = -5
+    assert (C == -5).all()
+
+
 # ------------------------------------------------------------------ together, streams, graphs
 
 def test_a_routed_layer_with_quantized_experts(lib):

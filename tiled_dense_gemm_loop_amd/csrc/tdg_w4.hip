@@ -184,23 +184,30 @@ struct W4Args {
 // both differences are exact.
 __device__ __forceinline__ f16x8 code_values(uint32_t word, f16x2 z1024, f16x2 z64) {
     const uint32_t high = word >> 8;
+    uint32_t above = 0x64006400u;
+    asm("" : "+v"(above));  // a register: and-or is one instruction, and takes no two literals
     f16x2 v[4];
     const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
-    v[0] = __builtin_bit_cast(f16x2, (word & 0x000f000fu) | 0x64006400u) - z1024;
-    v[1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (word & 0x00f000f0u) | 0x64006400u), sixteenth, -z64);
-    v[2] = __builtin_bit_cast(f16x2, (high & 0x000f000fu) | 0x64006400u) - z1024;
-    v[3] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (high & 0x00f000f0u) | 0x64006400u), sixteenth, -z64);
+    v[0] = __builtin_bit_cast(f16x2, (word & 0x000f000fu) | above) - z1024;
+    v[1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (word & 0x00f000f0u) | above), sixteenth, -z64);
+    v[2] = __builtin_bit_cast(f16x2, (high & 0x000f000fu) | above) - z1024;
+    v[3] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (high & 0x00f000f0u) | above), sixteenth, -z64);
     return f16x8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
 }
 
-// Few rows: a workgroup has 16 CT columns and up to 16 MT rows, and its eight
-// waves a part of k each, which LDS joins in order.
-constexpr int FEW_WAVES = 8;
-
-template <int MT, int CT, bool ZEROS>
-__global__ void __launch_bounds__(FEW_WAVES * 64) k_w4_few(W4Args p) {
-    __shared__ float part[FEW_WAVES][CT * 4 * 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
+// Few rows: a workgroup has 16 CT columns and up to 16 MT rows, and each of its
+// NW waves a run of k's blocks, which LDS joins in order.  Rows, codes and scales
+// go to registers as the matrix instructions take them; the waves share nothing
+// but the rows.  The loads in flight are those of many waves: a wave that loads
+// two or four blocks at a time, or the next one's codes early, holds so many
+// registers that it loses more (1 x 4096 x 4096: 4.3 us with one block, 5.0 with
+// two or four; 16 x 8192 x 8192: 13.1, 13.7, 14.3).
+template <int MT, int CT, int NW, int SPAN, bool ZEROS>
+__global__ void __launch_bounds__(NW * 64) k_w4_few(W4Args p) {
+    constexpr int SCALES = 4 / SPAN;  // scales of a column in a block
+    __shared__ float part[NW][CT * 4 * 64];
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lo = 0, hi = p.rows;
     Weights4 w = p.w;
     if (p.offsets) {
@@ -208,105 +215,147 @@ __global__ void __launch_bounds__(FEW_WAVES * 64) k_w4_few(W4Args p) {
         lo = min(max(p.offsets[g], 0), p.rows), hi = min(max(p.offsets[g + 1], 0), p.rows);
         w.codes += g * w.stride_codes, w.scales += g * w.stride_scales, w.zeros += g * w.stride_zeros;
     }
-    const int per = (p.blocks + FEW_WAVES - 1) / FEW_WAVES;
+    const int per = (p.blocks + NW - 1) / NW;
     const int b0 = min(p.blocks, wave * per), b1 = min(p.blocks, b0 + per);
-    const unsigned char *code[CT];
     int col[CT];
 #pragma unroll
-    for (int t = 0; t < CT; t++) {
-        col[t] = min((int)blockIdx.x * 16 * CT + t * 16 + c, p.N - 1);
-        code[t] = w.codes + (int64_t)col[t] * 64 + q * 16;
-    }
+    for (int t = 0; t < CT; t++) col[t] = min((int)blockIdx.x * 16 * CT + t * 16 + c, p.N - 1);
     for (int m0 = lo + (int)blockIdx.z * 16 * MT; m0 < hi; m0 += (int)gridDim.z * 16 * MT) {
+        const unsigned char *row[MT];  // a lane behind the last row takes that one: its sums are not stored
+#pragma unroll
+        for (int i = 0; i < MT; i++) row[i] = p.A + (int64_t)min(m0 + i * 16 + c, hi - 1) * p.lda + q * 16;
         f32x4 acc[MT][CT] = {};
         for (int b = b0; b < b1; b++) {
+            const int k = b * BLOCK;
             u32x4 word[CT];
+            _Float16 scale[SCALES][CT];
+            unsigned char zero[SCALES][CT];
+            const unsigned char *code = w.codes + b * w.ld_codes + q * 16;
 #pragma unroll
-            for (int t = 0; t < CT; t++) word[t] = *(const u32x4 *)(code[t] + b * w.ld_codes);
+            for (int t = 0; t < CT; t++) word[t] = *(const u32x4 *)(code + (int64_t)col[t] * 64);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int k = b * BLOCK + 32 * j;
-                if (k >= p.K) break;
-                const int g = k / p.group, kl = k + 8 * q;
-                f16x8 x[MT];
-#pragma unroll
-                for (int i = 0; i < MT; i++) {
-                    const int m = m0 + i * 16 + c;
-                    const unsigned char *at = p.A + (int64_t)m * p.lda + (int64_t)kl * 2;
-                    x[i] = f16x8{};
-                    if (m < hi && kl + 8 <= p.K) {
-                        x[i] = __builtin_bit_cast(f16x8, load16_global(at));
-                    } else if (m < hi) {
-#pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            if (kl + e < p.K) x[i][e] = *(const _Float16 *)(at + e * 2);
-                    }
-                }
+            for (int g = 0; g < SCALES; g++) {
+                const int64_t at = min(k + g * 32 * SPAN, p.K - 1) / p.group;
 #pragma unroll
                 for (int t = 0; t < CT; t++) {
-                    const float s = load_weight(w.scales + g * w.ld_scales + (int64_t)col[t] * 2);
-                    const _Float16 z = ZEROS ? (_Float16)(float)w.zeros[g * w.ld_zeros + col[t]] : (_Float16)8.0f;
-                    const _Float16 z1024 = z + (_Float16)1024.0f, z64 = z + (_Float16)64.0f;
-                    const f16x8 v = code_values(word[t][j], f16x2{z1024, z1024}, f16x2{z64, z64});
+                    scale[g][t] = *(const _Float16 *)(w.scales + at * w.ld_scales + (int64_t)col[t] * 2);
+                    if constexpr (ZEROS) zero[g][t] = w.zeros[at * w.ld_zeros + col[t]];
+                }
+            }
+            f16x8 x[4][MT];
+            if (k + BLOCK <= p.K) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int i = 0; i < MT; i++)
+                        x[j][i] = __builtin_bit_cast(f16x8, load16_global(row[i] + (int64_t)(k + 32 * j) * 2));
+            } else {  // the end of k cuts the block: zeros behind it
+#pragma unroll
+                for (int j = 0; j < 4; j++)
 #pragma unroll
                     for (int i = 0; i < MT; i++) {
-                        const f32x4 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[i], v, f32x4{}, 0, 0, 0);
+                        const int have = p.K - k - 32 * j - 8 * q;
+                        const unsigned char *at = row[i] + (int64_t)(k + 32 * j) * 2;
+                        x[j][i] = f16x8{};
+                        if (have >= 8) {
+                            x[j][i] = __builtin_bit_cast(f16x8, load16_global(at));
+                        } else {
 #pragma unroll
-                        for (int r = 0; r < 4; r++) acc[i][t][r] = fmaf(s, sum[r], acc[i][t][r]);
+                            for (int e = 0; e < 8; e++)
+                                if (e < have) x[j][i][e] = *(const _Float16 *)(at + e * 2);
+                        }
                     }
+            }
+#pragma unroll
+            for (int g = 0; g < SCALES; g++) {
+                if (k + g * 32 * SPAN >= p.K) break;
+#pragma unroll
+                for (int t = 0; t < CT; t++) {
+                    f16x2 z1024 = {(_Float16)1032.0f, (_Float16)1032.0f}, z64 = {(_Float16)72.0f, (_Float16)72.0f};
+                    if constexpr (ZEROS) {
+                        const float z = (float)zero[g][t];
+                        z1024[0] = z1024[1] = (_Float16)(z + 1024.0f), z64[0] = z64[1] = (_Float16)(z + 64.0f);
+                    }
+                    f32x4 sum[MT] = {};
+#pragma unroll
+                    for (int j = g * SPAN; j < (g + 1) * SPAN; j++) {
+                        const f16x8 v = code_values(word[t][j], z1024, z64);
+#pragma unroll
+                        for (int i = 0; i < MT; i++)
+                            sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j][i], v, sum[i], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; i++)
+#pragma unroll
+                        for (int r = 0; r < 4; r++)
+                            acc[i][t][r] = fmaf((float)scale[g][t], sum[i][r], acc[i][t][r]);
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < MT; i++) {
+            if (m0 + i * 16 >= hi) break;
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < CT; t++)
 #pragma unroll
                 for (int r = 0; r < 4; r++) part[wave][(t * 4 + r) * 64 + lane] = acc[i][t][r];
             __syncthreads();
-            for (int e = tid; e < CT * 256; e += FEW_WAVES * 64) {
-                float sum = part[0][e];
-#pragma unroll
-                for (int v = 1; v < FEW_WAVES; v++) sum += part[v][e];
+            for (int e = tid; e < CT * 256; e += NW * 64) {
                 const int m = m0 + i * 16 + (e >> 4 & 3) * 4 + (e >> 6 & 3);
                 const int n = (int)blockIdx.x * 16 * CT + (e >> 8) * 16 + (e & 15);
-                if (m < hi && n < p.N) *(float *)((unsigned char *)p.C + (int64_t)m * p.ldc + (int64_t)n * 4) = sum;
+                if (m >= hi || n >= p.N) continue;
+                float sum = part[0][e];
+#pragma unroll
+                for (int v = 1; v < NW; v++) sum += part[v][e];
+                *(float *)((unsigned char *)p.C + (int64_t)m * p.ldc + (int64_t)n * 4) = sum;
             }
         }
     }
 }
 
-// Many rows: a workgroup of four waves has 16 MT rows and 64 CT columns, each
-// wave all the rows and a fourth of the columns, so that no weight is unpacked
-// twice in a workgroup.  A ring of LDS buffers is filled by the global-to-LDS
-// DMA, one block of 128 k each: A's rows (256 bytes each, 16-byte pieces at
-// piece ^ (row % 16)), the waves' codes (64 bytes a column, pieces at piece ^
-// (column / 4 % 4); both keep fragment reads free of bank conflicts) and their
-// scales and zero points, a word for each column.  A block's codes become
-// fragments in registers; then row by row of 16 the instructions of SPAN * 32 k
-// run on a sum of their own, which joins the accumulators times the scale.
-template <int MT_, int CT_, int SPAN_, bool ZEROS_, int STAGES_>
+// Many rows: a workgroup has 16 MT rows and 16 CT columns for each of its waves,
+// and every wave all the rows, so that no weight is unpacked twice in a
+// workgroup.  Two LDS buffers are filled by the global-to-LDS DMA, one block of
+// 128 k each: A's rows (256 bytes each, 16-byte pieces at piece ^ (row % 16)), the
+// waves' codes (64 bytes a column, pieces at piece ^ (column / 4 % 4); both keep
+// fragment reads free of bank conflicts), and their scales and zero points, a word
+// for each column.  A block's codes become fragments in registers; then row by row
+// of 16 the instructions of SPAN * 32 k run on a sum of their own, which joins the
+// accumulators times the scale.  What bounds it: the copies' rate from L2, which
+// tall and wide tiles spare, and the vector instructions that unpack and scale, so
+// that tiles small enough for two or three workgroups to a CU do better than a
+// third buffer (8192 rows, 16 matrices of 4096 x 4096: 64 x 256 tiles 291 us,
+// with three buffers 319 and more).
+template <int MT_, int CT_, int WAVES_, int SPAN_, bool ZEROS_>
 struct W4Tile {
-    static constexpr int MT = MT_, CT = CT_, SPAN = SPAN_, STAGES = STAGES_;
+    static constexpr int MT = MT_, CT = CT_, WAVES = WAVES_, SPAN = SPAN_;
     static constexpr bool ZEROS = ZEROS_;
-    static constexpr int BM = 16 * MT, BN = 64 * CT, WAVES = 4, THREADS = 256;
-    static constexpr int SCALES = 4 / SPAN;  // scales of a column in a block
+    static constexpr int BM = 16 * MT, BN = 16 * CT * WAVES, THREADS = 64 * WAVES;
+    static constexpr int ROWS = 4 * WAVES, COPIES = BM / ROWS;  // rows of A that all waves copy at once, how often
+    static constexpr int SCALES = 4 / SPAN;                     // scales of a column in a block
     static constexpr int A_BYTES = BM * 256, CODE_BYTES = CT * 1024, SCALE_BYTES = SCALES * 256;
     static constexpr int WAVE_BYTES = CODE_BYTES + SCALE_BYTES * (ZEROS ? 2 : 1);
     static constexpr int STAGE = A_BYTES + WAVES * WAVE_BYTES;
-    static constexpr int COPIES = MT + CT + SCALES * (ZEROS ? 2 : 1);  // of a wave, for each block
-    static_assert(STAGES >= 2 && STAGES <= 4 && COPIES * (STAGES - 2) <= 63 && STAGES * STAGE <= 160 * 1024, "ring");
+    static_assert(BM % ROWS == 0 && ROWS % 16 == 0, "A's rows must split evenly, and their swizzle repeat");
+    static_assert(2 * STAGE <= 160 * 1024, "two buffers");
 };
 
-// As copy_to_lds, 2 bytes (1 byte) of each lane's address to the word at m0 + 4 lane.
+// As copy_to_lds, 2 bytes (1 byte) at each lane's address to the word at m0 + 4 lane.
 template <int BYTES>
-__device__ __forceinline__ void copy_word_to_lds(uint64_t src, uint32_t m0) {
+__device__ __forceinline__ void copy_word_to_lds(const unsigned char *base, uint32_t off, uint32_t m0) {
     static_assert(BYTES == 1 || BYTES == 2, "what a word is made of");
+    uint64_t safe;
     if constexpr (BYTES == 2)
-        asm volatile("s_nop 0\n\tglobal_load_lds_ushort %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+        asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_ushort %1, %0"
+                     : "=&s"(safe)
+                     : "v"(off), "s"(base), "{m0}"(m0)
+                     : "memory");
     else
-        asm volatile("s_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(src), "{m0}"(m0) : "memory");
+        asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_ubyte %1, %0"
+                     : "=&s"(safe)
+                     : "v"(off), "s"(base), "{m0}"(m0)
+                     : "memory");
 }
 
 template <class T>
@@ -316,74 +365,76 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t lds = (uint32_t)(uintptr_t)(TDG_LDS unsigned char *)smem;
     const int n0 = y0 + wave * 16 * T::CT;
-    // A's copies: rows 16 i + tid / 16, of which the last one stands for all behind it.
+    // A's copies: rows ROWS i + tid / 16, of which the last one stands for all behind it.
     const int piece = (tid & 15) ^ (tid >> 4 & 15);
-    uint32_t a_off[T::MT];
+    uint32_t a_off[T::COPIES];
 #pragma unroll
-    for (int i = 0; i < T::MT; i++)
-        a_off[i] = (uint32_t)((int64_t)min(i * 16 + (tid >> 4), hi - 1 - x0) * p.lda + piece * 16);
+    for (int i = 0; i < T::COPIES; i++)
+        a_off[i] = (uint32_t)((int64_t)min(i * T::ROWS + (tid >> 4), hi - 1 - x0) * p.lda + piece * 16);
     const unsigned char *a_base = p.A + (int64_t)x0 * p.lda;
-    const int own = min(n0 + (T::CT == 4 ? lane : lane % (16 * T::CT)), p.N - 1);  // the lane's column of scales
+    // Codes and scales: columns from n0 on; the last one stands for those behind it.
+    const int first = min(n0, p.N - 1), last = p.N - 1 - first;
+    uint32_t code_off[T::CT];
+#pragma unroll
+    for (int t = 0; t < T::CT; t++)
+        code_off[t] = (uint32_t)(min(t * 16 + (lane >> 2), last) * 64 + (((lane & 3) ^ (lane >> 4)) << 4));
+    const uint32_t own = (uint32_t)min(lane % (16 * T::CT), last);
+    const unsigned char *codes = w.codes + (int64_t)first * 64, *scales = w.scales + (int64_t)first * 2;
+    const unsigned char *zeros = w.zeros + first;
+    int into = 0;  // k of the next block's first scale in its group
 
+    // (Blocks are copied in order: each moves codes, scales and zeros on.)
     auto issue = [&](int b) {
-        const uint32_t at = lds + (uint32_t)(b % T::STAGES) * T::STAGE, mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
+        const uint32_t at = lds + (uint32_t)(b & 1) * T::STAGE, mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
         const unsigned char *base = a_base + (int64_t)b * 256;
         const int left = p.K - b * BLOCK;
         if (left >= BLOCK) {
 #pragma unroll
-            for (int i = 0; i < T::MT; i++) copy_to_lds(base, a_off[i], at + i * 4096 + wave * 1024);
+            for (int i = 0; i < T::COPIES; i++) copy_to_lds(base, a_off[i], at + i * T::ROWS * 256 + wave * 1024);
         } else {
             // The last block, which the end of k cuts: pieces behind it are zeros,
             // and the one that it cuts is written element by element.
             const int have = left - piece * 8;
 #pragma unroll
-            for (int i = 0; i < T::MT; i++) {
+            for (int i = 0; i < T::COPIES; i++) {
                 const unsigned char *src = base + a_off[i];
                 if (have >= 8 || have <= 0) {
                     copy_to_lds(have > 0 ? (uint64_t)(uintptr_t)src : (uint64_t)(uintptr_t)tdg_zero16,
-                                at + i * 4096 + wave * 1024);
+                                at + i * T::ROWS * 256 + wave * 1024);
                 } else {
                     f16x8 v = {};
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         if (e < have) v[e] = *(const _Float16 *)(src + e * 2);
-                    lds_write16(smem + (b % T::STAGES) * T::STAGE + i * 4096 + tid * 16, __builtin_bit_cast(u32x4, v));
+                    lds_write16(smem + (b & 1) * T::STAGE + i * T::ROWS * 256 + tid * 16, __builtin_bit_cast(u32x4, v));
                 }
             }
         }
 #pragma unroll
-        for (int t = 0; t < T::CT; t++) {
-            const int col = min(n0 + t * 16 + (lane >> 2), p.N - 1), from = (lane & 3) ^ (lane >> 4 & 3);
-            copy_to_lds((uint64_t)(uintptr_t)(w.codes + b * w.ld_codes + (int64_t)col * 64 + from * 16),
-                        mine + t * 1024);
-        }
+        for (int t = 0; t < T::CT; t++) copy_to_lds(codes, code_off[t], mine + t * 1024);
+        codes += w.ld_codes;
 #pragma unroll
         for (int g = 0; g < T::SCALES; g++) {
-            const int k = min(b * BLOCK + g * 32 * T::SPAN, p.K - 1);
-            const int64_t row = k / p.group;
-            copy_word_to_lds<2>((uint64_t)(uintptr_t)(w.scales + row * w.ld_scales + (int64_t)own * 2),
-                                mine + T::CODE_BYTES + g * 256);
-            if constexpr (T::ZEROS)
-                copy_word_to_lds<1>((uint64_t)(uintptr_t)(w.zeros + row * w.ld_zeros + own),
-                                    mine + T::CODE_BYTES + T::SCALE_BYTES + g * 256);
+            copy_word_to_lds<2>(scales, own * 2, mine + T::CODE_BYTES + g * 256);
+            if constexpr (T::ZEROS) copy_word_to_lds<1>(zeros, own, mine + T::CODE_BYTES + T::SCALE_BYTES + g * 256);
+            into += 32 * T::SPAN;
+            if (into >= p.group && b * BLOCK + (g + 1) * 32 * T::SPAN < p.K) {
+                into = 0;
+                scales += w.ld_scales, zeros += w.ld_zeros;
+            }
         }
     };
 
     f32x4 acc[T::MT][T::CT] = {};
-#pragma unroll
-    for (int b = 0; b < T::STAGES - 1; b++)
-        if (b < p.blocks) issue(b);
+    if (p.blocks > 0) issue(0);
     uint32_t a_at[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) a_at[j] = (uint32_t)(c * 256 + (((4 * j + q) ^ c) << 4));
     for (int b = 0; b < p.blocks; b++) {
-        const int later = min(T::STAGES - 2, p.blocks - 1 - b);  // blocks whose copies may stay in flight
-        if (T::STAGES >= 4 && later == 2) wait_vmcnt<(T::STAGES >= 4 ? 2 : 0) * T::COPIES>();
-        else if (T::STAGES >= 3 && later >= 1) wait_vmcnt<(T::STAGES >= 3 ? 1 : 0) * T::COPIES>();
-        else wait_vmcnt<0>();
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (b + T::STAGES - 1 < p.blocks) issue(b + T::STAGES - 1);
-        const unsigned char *at = smem + (b % T::STAGES) * T::STAGE, *mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
+        // Block b has landed, and nobody reads the other buffer any more.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (b + 1 < p.blocks) issue(b + 1);
+        const unsigned char *at = smem + (b & 1) * T::STAGE, *mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
         f16x8 v[T::CT][4];
         float scale[T::CT][T::SCALES];
 #pragma unroll
@@ -436,11 +487,11 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
         }
 }
 
-template <int MT, int CT, int SPAN, bool ZEROS, int STAGES>
-__global__ void __launch_bounds__(256) k_w4_tile(W4Args p) {
-    typedef W4Tile<MT, CT, SPAN, ZEROS, STAGES> T;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[STAGES * T::STAGE];
-    poison_lds<STAGES * T::STAGE, T::THREADS>(p.flags, smem);
+template <int MT, int CT, int WAVES, int SPAN, bool ZEROS>
+__global__ void __launch_bounds__(WAVES * 64) k_w4_tile(W4Args p) {
+    typedef W4Tile<MT, CT, WAVES, SPAN, ZEROS> T;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * T::STAGE];
+    poison_lds<2 * T::STAGE, T::THREADS>(p.flags, smem);
     Weights4 w = p.w;
     if (!p.offsets) {
         int tm, tn;
@@ -528,39 +579,77 @@ struct Variant4 {
     int threads;
 };
 
-template <int MT, int CT, int SPAN, bool ZEROS>
-const void *tile_fn() {
-    // Three buffers where they fit.
-    constexpr int three = 3 * W4Tile<MT, CT, SPAN, ZEROS, 2>::STAGE <= 160 * 1024 ? 3 : 2;
-    return (const void *)&k_w4_tile<MT, CT, SPAN, ZEROS, three>;
+// The kernel of a shape for the group length and with or without zero points:
+// a sum takes as many matrix instructions as the groups and blocks allow.
+#define TDG_W4_FN(KERNEL, ...)                                             \
+    (q.group % 128 == 0  ? (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, 4, true>   \
+                                    : (const void *)&KERNEL<__VA_ARGS__, 4, false>) \
+     : q.group % 64 == 0 ? (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, 2, true>   \
+                                    : (const void *)&KERNEL<__VA_ARGS__, 2, false>) \
+                         : (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, 1, true>   \
+                                    : (const void *)&KERNEL<__VA_ARGS__, 1, false>))
+
+template <int MT, int CT, int NW>
+Variant4 few(const W4Args &p, const Named4 &q) {
+    const int64_t z = p.offsets ? 1 : ceil_quot(p.rows, 16 * MT);
+    return {TDG_W4_FN(k_w4_few, MT, CT, NW),
+            grid_of(ceil_quot(q.N, 16 * CT), p.row_groups, z > 65535 ? 65535 : z), NW * 64};
 }
 
-template <int MT, int CT>
-const void *tile_fn(int64_t group, bool zeros) {
-    if (group % 128 == 0) return zeros ? tile_fn<MT, CT, 4, true>() : tile_fn<MT, CT, 4, false>();
-    if (group % 64 == 0) return zeros ? tile_fn<MT, CT, 2, true>() : tile_fn<MT, CT, 2, false>();
-    return zeros ? tile_fn<MT, CT, 1, true>() : tile_fn<MT, CT, 1, false>();
+// Tiles of bm x bn that a product is expected to have: half a row tile for each
+// group that can have rows, beside those that the rows fill.
+int64_t tiles_of(const W4Args &p, int64_t live, int64_t bm, int64_t bn) {
+    const int64_t high = p.offsets ? p.rows / bm + live / 2 : ceil_quot(p.rows, bm);
+    return (high > live ? high : live) * ceil_quot(p.N, bn);
+}
+
+template <int MT, int CT, int WAVES>
+Variant4 tiled(W4Args &p, const Named4 &q, int64_t live) {
+    typedef W4Tile<MT, CT, WAVES, 4, false> T;
+    p.tiles_m = (int)ceil_quot(p.rows, T::BM), p.tiles_n = (int)ceil_quot(q.N, T::BN);
+    // (Most tiles: every group can end inside one, and needs a row for it.)
+    const int64_t most = p.offsets ? ceil_quot((p.rows / T::BM + live) * p.tiles_n, 8) * 8 : (int64_t)p.tiles_m * p.tiles_n;
+    return {TDG_W4_FN(k_w4_tile, MT, CT, WAVES), dim3(most <= INT32_MAX - 65536 ? (unsigned)most : UINT32_MAX), T::THREADS};
 }
 
 Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
     const int64_t live = p.offsets ? (p.row_groups < p.rows ? p.row_groups : p.rows) : 1;
+    // Pieces of 16 rows by 16 columns.
+    const int64_t pieces = (p.offsets ? live : ceil_quot(p.rows, 16)) * ceil_quot(q.N, 16);
     // The DMA's lanes reach a tile's rows with 32-bit byte offsets.
     const bool far = lda > (int64_t)UINT32_MAX / 2 / 128 - 256;
-    if (p.rows <= 64 * live || far || p.blocks == 0) {
-        const int64_t most = p.offsets ? 1 : ceil_quot(p.rows, 64);
-        return {q.zeros ? (const void *)&k_w4_few<4, 2, true> : (const void *)&k_w4_few<4, 2, false>,
-                grid_of(ceil_quot(q.N, 32), p.row_groups, most > 65535 ? 65535 : most), FEW_WAVES * 64};
+    // Few rows: as many columns to a workgroup as leave one or two to a CU (us,
+    // 16 / 32 / 64 columns: 16 x 4096 x 4096, 256 pieces, 6.6 / 7.2 / -; 24 rows,
+    // 512, 9.7 / 7.5 / 8.7; 64 rows, 1024, 15.0 / 12.2 / 9.2; 1 x 16384 x 4096,
+    // 1024, - / 10.6 / 10.2); then two row tiles (128 rows, 2048: 15.7 with one,
+    // 13.7 with two, 32 x 64 tiles from LDS 16.1; 192 rows, 3072: 21.0, 24.8,
+    // 18.8; 32 x 16384 x 4096, 2048: 16.9, 15.0, 21).  Groups of rows: up to 8 to a
+    // group (32 groups of 2048 x 2048, 200 rows: 17.9, tiles 19.2; 400: 22.6, 19.6).
+    const bool short_groups = p.rows <= 8 * live;
+    if (far || p.blocks == 0 || (p.offsets ? short_groups : p.rows <= 32 || pieces <= 2048)) {
+        // 16 waves where k is long or so few rows that their loads do not count
+        // (us, 8 / 16 waves: 1 x 4096 x 4096 4.9 / 4.3, 1 x 512 x 8192 6.7 / 5.4, 16 x
+        // 4096 x 4096 6.6 / 6.9).
+        if (pieces <= 384) return (p.rows <= 4 || p.blocks >= 64) && !p.offsets ? few<1, 1, 16>(p, q) : few<1, 1, 8>(p, q);
+        if (pieces <= 640) return few<1, 2, 8>(p, q);
+        if (pieces <= 1280 || p.rows <= 16 || (p.offsets && short_groups)) return few<1, 4, 8>(p, q);
+        return few<2, 4, 8>(p, q);
     }
-    auto tiles = [&](int64_t bm, int64_t bn) {
-        const int64_t m = p.offsets ? p.rows / bm + live : ceil_quot(p.rows, bm);
-        return m * ceil_quot(q.N, bn);
-    };
-    const bool wide = tiles(128, 256) >= 256;
-    const int bn = wide ? 256 : 128;
-    p.tiles_m = (int)ceil_quot(p.rows, 128), p.tiles_n = (int)ceil_quot(q.N, bn);
-    const int64_t grid = p.offsets ? ceil_quot(tiles(128, bn), 8) * 8 : tiles(128, bn);
-    return {wide ? tile_fn<8, 4>(q.group, q.zeros) : tile_fn<8, 2>(q.group, q.zeros),
-            dim3((unsigned)(grid > UINT32_MAX ? UINT32_MAX : grid)), 256};
+    // Tiles.  128 x 512, one to a CU, where its rounds of 256 are full (us, against
+    // 64 x 256: 4096 x 4096 x 4096, 256 tiles, 121 / 138; 3000 x 11008 x 2048, 528,
+    // 174 / 150; 16 groups of 1024 rows, 4096 x 4096, 1088 588 / 585).
+    const int64_t large = tiles_of(p, live, 128, 512);
+    if (large * 100 > ceil_quot(large, 256) * 256 * 85 && p.rows >= 1024 * live) return tiled<8, 4, 8>(p, q, live);
+    // A few rows of each group: 32 x 128, or 64 wide (us, against 64 x 128 / 32 x 64:
+    // 32 groups of 2048 x 2048, 600 rows 20.3, 25.2 / 21.4; 1000 rows 25.4, 26.1 /
+    // 30.1; 2000 rows -, 32.7 / -; 9 groups of 1537 x 1000, 333 rows 8.6, 9.7 / 7.9).
+    if (p.rows <= 40 * live) return tiles_of(p, live, 32, 128) >= 256 ? tiled<2, 2, 4>(p, q, live) : tiled<2, 1, 4>(p, q, live);
+    // 64 x 256, two to a CU (us, against 64 x 128: 2048 x 4096 x 4096, 512 tiles, 73
+    // / 80; 1536 rows, 384, 64 / 60; 1024 rows, 256, 44 / 42); 64 x 128, three to a
+    // CU, against 32 x 64 (512 rows, 256 tiles: 29 / 30; 192 rows, 96: 26 / 19).
+    if (tiles_of(p, live, 64, 256) > 416) return tiled<4, 2, 8>(p, q, live);
+    if (tiles_of(p, live, 64, 128) >= 256) return tiled<4, 1, 8>(p, q, live);
+    return tiled<2, 1, 4>(p, q, live);
 }
 
 int run_product(int64_t row_groups, const int32_t *offsets, int64_t M, const Named4 &q, const void *A, int64_t lda,
