@@ -29,18 +29,21 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int MAX_ENTRIES = TDG_LAYER_MAX_TOKENS * TDG_LAYER_MAX_TOP_K;
-constexpr int WAVES = 8, THREADS = WAVES * 64;
 
 struct LayerArgs {
     const unsigned char *x, *up, *down;
     const int32_t *ids;
     const float *weights;  // NULL: 1
     unsigned char *y;
-    float *h, *z;                                                 // entries x ld_h, entries x ld_z
+    // The workspace.  One part of k in the up product: h, entries x ld_h; more:
+    // parts x entries x 2 x ld_h sums of gate and up.  z: parts_z x entries x ld_z.
+    float *h, *z;
     int64_t ldx, ld_up, stride_up, ld_down, stride_down, ldy;     // bytes
     int64_t ld_ids, ld_weights;                                   // elements
     int64_t ld_h, ld_z;                                           // elements, multiples of 4
     int tokens, top_k, experts, cols, inner, entries;
+    int parts, parts_z;  // workgroups that share k: grid.z of the up and of the down product
+    int piece;           // elements of h that a wave of down joins in LDS
 };
 
 __device__ __forceinline__ int id_of(const LayerArgs &p, int entry) {
@@ -58,10 +61,13 @@ struct Mine {
 __device__ __forceinline__ Mine find_entries(const LayerArgs &p, int slot, int *list) {
     const int lane = threadIdx.x & 63;
     const bool by_entry = p.entries <= p.experts;
+    int id = id_of(p, lane);
     Mine m = {by_entry ? id_of(p, slot) : slot, 0};
+    m.expert = __builtin_amdgcn_readfirstlane(m.expert);
     if ((unsigned)m.expert >= (unsigned)p.experts) return m;
     for (int base = 0; base < p.entries; base += 64) {  // (every wave: the same values to the same places)
-        const bool hit = id_of(p, base + lane) == m.expert;
+        if (base) id = id_of(p, base + lane);
+        const bool hit = id == m.expert;
         const unsigned long long hits = __ballot(hit);
         if (hit) list[m.count + __popcll(hits & ((1ull << lane) - 1))] = base + lane;
         if (by_entry && m.count == 0 && hits && base + __ffsll((long long)hits) - 1 < slot) return m;  // not the first
@@ -93,58 +99,65 @@ __device__ __forceinline__ _Float16 element(typename Halves<V>::vec v, int i) {
     else return v[i];
 }
 
-// Joins the waves' sums of one accumulator row: `sum` of V columns and the 64
-// lanes, waves in order.
-template <int V, int SIDES>
-__device__ __forceinline__ float join_waves(const float (&part)[WAVES][SIDES][V * 64], int side, int e) {
+// V neighbouring elements of N rows of a matrix from row k on; rows from K on,
+// which the caller's `cut` says there may be, are zeros.
+template <int V, int N>
+__device__ __forceinline__ void load_rows(typename Halves<V>::vec (&w)[N], const unsigned char *base, int64_t ld, int k,
+                                          int K, bool cut) {
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+        if (!cut || k + e < K) w[e] = load_halves<V>(base + (int64_t)(k + e) * ld);
+        else w[e] = typename Halves<V>::vec{};
+    }
+}
+
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// Sums the waves' parts of one accumulator row, in order.
+template <int NW, int SIDES, int N>
+__device__ __forceinline__ float join_waves(const float (&part)[NW][SIDES][N], int side, int e) {
     float sum = part[0][side][e];
 #pragma unroll
-    for (int w = 1; w < WAVES; w++) sum += part[w][side][e];
+    for (int w = 1; w < NW; w++) sum += part[w][side][e];
     return sum;
 }
 
 // A workgroup has 16 V columns of gate and up and all of k, of which each wave
 // takes a part, 32 at a time: lane l loads V columns from 16 V (l % 16) on, at
 // k = 8 (l / 16) .. + 7.
-template <int MT, int V>
-__global__ void __launch_bounds__(THREADS) k_layer_up(LayerArgs p) {
+template <int MT, int V, int NW>
+__global__ void __launch_bounds__(NW * 64) k_layer_up(LayerArgs p) {
     __shared__ int list[MAX_ENTRIES];
-    __shared__ float part[WAVES][2][V * 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
+    __shared__ float part[NW][2][V * 64];
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Mine mine = find_entries(p, blockIdx.y, list);
     if (mine.count == 0) return;
     typedef typename Halves<V>::vec vec;
     const int want = ((int)blockIdx.x * 16 + c) * V, n = min(want, p.inner - V);
     const unsigned char *gate = p.up + mine.expert * p.stride_up + (int64_t)n * 2, *up = gate + (int64_t)p.inner * 2;
-    const int steps = (p.cols + 31) / 32, per = (steps + WAVES - 1) / WAVES;
-    const int s0 = min(steps, wave * per), s1 = min(steps, s0 + per);
+    const int steps = (p.cols + 31) / 32, runs = NW * p.parts, run = (int)blockIdx.z * NW + wave;
+    const int s0 = (int)((int64_t)steps * run / runs), s1 = (int)((int64_t)steps * (run + 1) / runs);
     __syncthreads();
     for (int r0 = 0; r0 < mine.count; r0 += 16 * MT) {
-        const unsigned char *x[MT];
+        const unsigned char *x[MT];  // a lane behind the last row takes that one: its sums are not stored
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            const int r = r0 + i * 16 + c;
-            x[i] = r < mine.count ? p.x + (int64_t)(list[r] / p.top_k) * p.ldx : nullptr;
-        }
+        for (int i = 0; i < MT; i++)
+            x[i] = p.x + (int64_t)(list[min(r0 + i * 16 + c, mine.count - 1)] / p.top_k) * p.ldx;
         f32x4 acc[2][V][MT] = {};
         for (int s = s0; s < s1; s++) {
             const int k = s * 32 + q * 8;
+            const bool cut = s * 32 + 32 > p.cols;
             vec g[8], u[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                g[e] = u[e] = vec{};
-                if (k + e < p.cols) {
-                    g[e] = load_halves<V>(gate + (int64_t)(k + e) * p.ld_up);
-                    u[e] = load_halves<V>(up + (int64_t)(k + e) * p.ld_up);
-                }
-            }
+            load_rows<V, 8>(g, gate, p.ld_up, k, p.cols, cut);
+            load_rows<V, 8>(u, up, p.ld_up, k, p.cols, cut);
             f16x8 a[MT];
 #pragma unroll
             for (int i = 0; i < MT; i++) {
-                a[i] = f16x8{};
-                if (x[i] && k + 8 <= p.cols) {
+                if (!cut || k + 8 <= p.cols) {
                     a[i] = __builtin_bit_cast(f16x8, load16_global(x[i] + (int64_t)k * 2));
-                } else if (x[i]) {
+                } else {
+                    a[i] = f16x8{};
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         if (k + e < p.cols) a[i][e] = *(const _Float16 *)(x[i] + (int64_t)(k + e) * 2);
@@ -176,97 +189,154 @@ __global__ void __launch_bounds__(THREADS) k_layer_up(LayerArgs p) {
                     part[wave][1][v * 64 + lane] = acc[1][v][i][r];
                 }
                 __syncthreads();
-                for (int e = tid; e < V * 64; e += THREADS) {  // (e % 64 == lane)
-                    const float sg = join_waves<V, 2>(part, 0, e), su = join_waves<V, 2>(part, 1, e);
+                for (int e = tid; e < V * 64; e += NW * 64) {  // (e % 64 == lane)
                     const int row = r0 + i * 16 + q * 4 + r;
-                    if (row < mine.count && want < p.inner)
-                        p.h[list[row] * p.ld_h + n + (e >> 6)] = sg / (1.0f + expf(-sg)) * su;
+                    if (row >= mine.count || want >= p.inner) continue;
+                    const float sg = join_waves(part, 0, e), su = join_waves(part, 1, e);
+                    if (p.parts == 1) {
+                        p.h[list[row] * p.ld_h + n + (e >> 6)] = gated(sg, su);
+                    } else {
+                        float *out = p.h + ((int64_t)blockIdx.z * p.entries + list[row]) * 2 * p.ld_h + n + (e >> 6);
+                        out[0] = sg, out[p.ld_h] = su;
+                    }
                 }
             }
     }
 }
 
+// A wave's piece of h from the parts of gate and up, k = k0 .. k0 + len - 1 of
+// `count` rows, to LDS: each element once for the wave, not once for each lane
+// and column that it is multiplied with.  Zeros from the end of k on.  A lane
+// takes W neighbours: four where there are many, or its gates follow each other
+// for nothing (one token: 9.8 us with one, 10.7 with four; 33 tokens 27.8, 26.8).
+template <int PARTS, int W>
+__device__ __forceinline__ void join_h(const LayerArgs &p, const int *list, int count, int k0, int len, int lane,
+                                       float *piece) {
+    typedef float vec __attribute__((ext_vector_type(W)));
+    for (int e = lane * W; e < count * len; e += 64 * W) {
+        const int r = e / len, k = k0 + (e - r * len);
+        vec v = {};
+        if (k < p.inner) {  // (rows are whole pieces of four)
+            const float *at = p.h + list[r] * 2 * p.ld_h + k;
+            vec g[PARTS], u[PARTS];
+#pragma unroll
+            for (int i = 0; i < PARTS; i++) {
+                const float *from = at + i * p.entries * 2 * p.ld_h;
+                g[i] = *(const vec *)from, u[i] = *(const vec *)(from + p.ld_h);
+            }
+#pragma unroll
+            for (int i = 1; i < PARTS; i++) g[0] += g[i], u[0] += u[i];
+#pragma unroll
+            for (int j = 0; j < W; j++) v[j] = k + j < p.inner ? gated(g[0][j], u[0][j]) : 0.0f;
+        }
+        *(vec *)(piece + e) = v;
+    }
+}
+
+// y[t][n] from the token's rows of z; eight of them travel at a time.
+template <typename T>
+__device__ __forceinline__ void join_token(const LayerArgs &p, int t, int n) {
+    constexpr int J = 8;
+    const float *z = p.z + t * p.top_k * p.ld_z + n;
+    float sum = 0.0f;
+    for (int j0 = 0; j0 < p.top_k; j0 += J) {
+        int id[J];
+        float w[J], v[J];
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            const int at = min(j0 + j, p.top_k - 1);
+            id[j] = j0 + j < p.top_k ? p.ids[t * p.ld_ids + at] : -1;
+            w[j] = p.weights ? p.weights[t * p.ld_weights + at] : 1.0f;
+            v[j] = z[at * p.ld_z];
+        }
+        for (int i = 1; i < p.parts_z; i++)
+#pragma unroll
+            for (int j = 0; j < J; j++) v[j] += z[(i * p.entries + min(j0 + j, p.top_k - 1)) * p.ld_z];
+#pragma unroll
+        for (int j = 0; j < J; j++)
+            if ((unsigned)id[j] < (unsigned)p.experts) sum = fmaf(w[j], v[j], sum);
+    }
+    *(T *)(p.y + t * p.ldy + (int64_t)n * sizeof(T)) = (T)sum;
+}
+
 // A workgroup has 16 V columns of down; lane l loads V of them at k = 4 (l / 16)
 // .. + 3, and the product's e-th step takes row e of each.
-template <int MT, int V>
-__global__ void __launch_bounds__(THREADS) k_layer_down(LayerArgs p) {
+template <int V, int NW, int PARTS>
+__global__ void __launch_bounds__(NW * 64) k_layer_down(LayerArgs p) {
     __shared__ int list[MAX_ENTRIES];
-    __shared__ float part[WAVES][1][V * 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, q = lane >> 4;
+    __shared__ float part[NW][1][V * 64];
+    constexpr bool JOIN = PARTS > 1;
+    extern __shared__ __attribute__((aligned(16))) float pieces[];  // JOIN: a piece of h for each wave
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Mine mine = find_entries(p, blockIdx.y, list);
     if (mine.count == 0) return;
     typedef typename Halves<V>::vec vec;
     const int want = ((int)blockIdx.x * 16 + c) * V, n = min(want, p.cols - V);
     const unsigned char *down = p.down + mine.expert * p.stride_down + (int64_t)n * 2;
-    const int steps = (p.inner + 15) / 16, per = (steps + WAVES - 1) / WAVES;
-    const int s0 = min(steps, wave * per), s1 = min(steps, s0 + per);
+    const int steps = (p.inner + 15) / 16, runs = NW * p.parts_z, run = (int)blockIdx.z * NW + wave;
+    const int s0 = (int)((int64_t)steps * run / runs), s1 = (int)((int64_t)steps * (run + 1) / runs);
+    float *piece = JOIN ? pieces + wave * p.piece : nullptr;
     __syncthreads();
-    for (int r0 = 0; r0 < mine.count; r0 += 16 * MT) {
-        const float *h[MT];
-#pragma unroll
-        for (int i = 0; i < MT; i++) {
-            const int r = r0 + i * 16 + c;
-            h[i] = r < mine.count ? p.h + list[r] * p.ld_h : nullptr;
+    for (int r0 = 0; r0 < mine.count; r0 += 16) {
+        const int rows = min(16, mine.count - r0), row = min(c, rows - 1);  // (rows behind the last: not stored)
+        const float *h = JOIN ? piece + row * (s1 - s0) * 16 - s0 * 16 : p.h + list[r0 + row] * p.ld_h;
+        f32x4 acc[V] = {};
+        auto load = [&](vec (&w)[4], int s) {
+            load_rows<V, 4>(w, down, p.ld_down, s * 16 + q * 4, p.inner, s * 16 + 16 > p.inner);
+        };
+        vec next[4];
+        if constexpr (JOIN) {  // the first weights travel while h is joined
+            if (s0 < s1) load(next, s0);
+            const int len = (s1 - s0) * 16;
+            if (rows * len > 256) join_h<PARTS, 4>(p, list + r0, rows, s0 * 16, len, lane, piece);
+            else join_h<PARTS, 1>(p, list + r0, rows, s0 * 16, len, lane, piece);
         }
-        f32x4 acc[V][MT] = {};
         for (int s = s0; s < s1; s++) {
             const int k = s * 16 + q * 4;
             vec w[4];
+            if constexpr (JOIN) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                w[e] = vec{};
-                if (k + e < p.inner) w[e] = load_halves<V>(down + (int64_t)(k + e) * p.ld_down);
+                for (int e = 0; e < 4; e++) w[e] = next[e];
+                if (s + 1 < s1) load(next, s + 1);
+            } else {  // (one step ahead: 63.6 us for 58.6 at 16 tokens, for the waves that its registers cost)
+                load(w, s);
             }
-            f32x4 a[MT];
-#pragma unroll
-            for (int i = 0; i < MT; i++) {
-                a[i] = f32x4{};
-                if (h[i] && k < p.inner) a[i] = *(const f32x4 *)(h[i] + k);  // (rows end on 16 bytes)
+            f32x4 a = {};
+            if (JOIN || k < p.inner) a = *(const f32x4 *)(h + k);  // (rows are whole pieces of four)
+            if (!JOIN && s * 16 + 16 > p.inner) {
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    if (k + e >= p.inner) a[i][e] = 0.0f;
+                    if (k + e >= p.inner) a[e] = 0.0f;
             }
 #pragma unroll
             for (int e = 0; e < 4; e++)
 #pragma unroll
                 for (int v = 0; v < V; v++) {
-                    const float b = (float)element<V>(w[e], v);
-#pragma unroll
-                    for (int i = 0; i < MT; i++) {
-                        const float ae = a[i][e];
-                        acc[v][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(ae, b, acc[v][i], 0, 0, 0);
-                    }
+                    const float ae = a[e], be = (float)element<V>(w[e], v);
+                    acc[v] = __builtin_amdgcn_mfma_f32_16x16x4f32(ae, be, acc[v], 0, 0, 0);
                 }
         }
 #pragma unroll
-        for (int i = 0; i < MT; i++)
+        for (int r = 0; r < 4; r++) {
+            if (r >= rows) break;
+            __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                if (r0 + i * 16 + r >= mine.count) continue;
-                __syncthreads();
-#pragma unroll
-                for (int v = 0; v < V; v++) part[wave][0][v * 64 + lane] = acc[v][i][r];
-                __syncthreads();
-                for (int e = tid; e < V * 64; e += THREADS) {
-                    const float sum = join_waves<V, 1>(part, 0, e);
-                    const int row = r0 + i * 16 + q * 4 + r;
-                    if (row < mine.count && want < p.cols) p.z[list[row] * p.ld_z + n + (e >> 6)] = sum;
-                }
+            for (int v = 0; v < V; v++) part[wave][0][v * 64 + lane] = acc[v][r];
+            __syncthreads();
+            for (int e = tid; e < V * 64; e += NW * 64) {
+                const int at = q * 4 + r;
+                if (at < rows && want < p.cols)
+                    p.z[((int64_t)blockIdx.z * p.entries + list[r0 + at]) * p.ld_z + n + (e >> 6)] = join_waves(part, 0, e);
             }
+        }
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) k_layer_join(LayerArgs p) {
-    const int n = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
-    if (n >= p.cols) return;
-    float sum = 0.0f;
-    for (int j = 0; j < p.top_k; j++) {
-        if ((unsigned)p.ids[t * p.ld_ids + j] >= (unsigned)p.experts) continue;
-        const float z = p.z[(t * p.top_k + j) * p.ld_z + n];
-        sum = p.weights ? fmaf(p.weights[t * p.ld_weights + j], z, sum) : sum + z;
-    }
-    *(T *)(p.y + t * p.ldy + (int64_t)n * sizeof(T)) = (T)sum;
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n < p.cols) join_token<T>(p, blockIdx.y, n);
 }
 
 // ------------------------------------------------------------------ host side
@@ -278,9 +348,48 @@ bool sizes_ok(int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int6
 
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
-int launch(const void *fn, dim3 grid, int threads, LayerArgs *args, void *stream) {
+int64_t at_most(int64_t n, int64_t most) { return n < most ? n : most; }
+
+// How the work is cut; a function of the sizes alone, as the workspace is.
+struct Plan {
+    int64_t slots, up_x, parts, down_x, parts_z, piece;
+    bool thin_up, thin_down, narrow;  // matrices below 8 columns; 64 instead of 128 columns of down to a workgroup
+    uint64_t z_at, bytes;
+};
+
+Plan make_plan(int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int64_t inner) {
+    Plan p;
+    const int64_t entries = tokens * top_k;
+    p.slots = entries < experts ? entries : experts;
+    // down: 128 columns and eight waves, k in two parts below 512 workgroups; 64
+    // columns and sixteen waves below 192 (us, 128 whole / 128 in two / 64 whole /
+    // 64 in two: 16 tokens, 1024 workgroups of 128, 50.7 / 51.4 / 56 / 65; 33
+    // tokens of 8 experts, 256, 22.3 / 20.2 / 23.3 / -; one token, 128, 10.9 / 9.3 /
+    // 8.5 / 9.7; 2 experts of 4096 x 4096, 64, - / 27 / 28 / 17).
+    p.thin_down = cols < 8;
+    const int64_t wide = ceil_quot(cols, 128) * p.slots;
+    p.narrow = !p.thin_down && wide < 192;
+    p.down_x = ceil_quot(cols, p.thin_down ? 16 : p.narrow ? 64 : 128);
+    p.parts_z = p.thin_down ? 1 : at_most(wide < 96 || (wide >= 192 && wide < 512) ? 2 : 1, inner / 256);
+    if (p.parts_z < 1) p.parts_z = 1;
+    // A CU takes about 35 GB/s from L2, so the weights need most CUs: k is cut in
+    // two or four where there are few workgroups (us, 1 / 2 / 4 parts: one token, 8
+    // experts of 2048 x 2 768, 48 workgroups, 17.3 / 12.5 / 11.4; two tokens, 96, 21
+    // / 18.7 / 21; 33 tokens, 8 experts of 4095 x 2 1001, 64, - / 33.8 / 32.9), if LDS
+    // holds what down then joins.
+    p.thin_up = inner < 8;
+    p.up_x = ceil_quot(inner, p.thin_up ? 16 : 128);
+    const int64_t wgs = p.up_x * p.slots, waves = p.narrow ? 16 : 8;
+    p.piece = ceil_quot(ceil_quot(inner, 16), waves * p.parts_z) * 16 * at_most(entries, 16);
+    p.parts = wgs > 96 || cols < 512 || p.piece * waves * 4 > 40 * 1024 ? 1 : wgs > 64 || cols < 1024 ? 2 : 4;
+    p.z_at = (uint64_t)(entries * up4(inner) * 4 * (p.parts > 1 ? 2 * p.parts : 1));
+    p.bytes = p.z_at + (uint64_t)(p.parts_z * entries * up4(cols) * 4);
+    return p;
+}
+
+int launch(const void *fn, dim3 grid, int threads, size_t lds, LayerArgs *args, void *stream) {
     void *kargs[] = {args};
-    if (hipLaunchKernel(fn, grid, dim3((unsigned)threads), kargs, 0, (hipStream_t)stream) != hipSuccess)
+    if (hipLaunchKernel(fn, grid, dim3((unsigned)threads), kargs, lds, (hipStream_t)stream) != hipSuccess)
         return TDG_ERR_LAUNCH;
     if (hipGetLastError() != hipSuccess) return TDG_ERR_LAUNCH;
     return TDG_OK;
@@ -294,7 +403,7 @@ int tdg_expert_layer_workspace(int64_t tokens, int64_t top_k, int64_t experts, i
                                size_t *bytes) {
     if (!bytes || !sizes_ok(tokens, top_k, experts, cols, inner)) return TDG_ERR_INVALID_ARG;
     if (tokens > TDG_LAYER_MAX_TOKENS || top_k > TDG_LAYER_MAX_TOP_K) return TDG_ERR_UNSUPPORTED;
-    *bytes = (size_t)(tokens * top_k * (up4(inner) + up4(cols)) * 4);
+    *bytes = (size_t)make_plan(tokens, top_k, experts, cols, inner).bytes;
     return TDG_OK;
 }
 
@@ -331,32 +440,45 @@ int tdg_expert_layer(int out_elem, int64_t tokens, int64_t top_k, int64_t expert
     for (int i = 0; i < 5; i++)
         if (overlaps(workspace, need, in[i], in_len[i])) return TDG_ERR_INVALID_ARG;
 
+    const Plan plan = make_plan(tokens, top_k, experts, cols, inner);
     LayerArgs p;
     p.x = (const unsigned char *)x, p.up = (const unsigned char *)up, p.down = (const unsigned char *)down;
     p.ids = ids, p.weights = weights, p.y = (unsigned char *)y;
     p.entries = (int)(tokens * top_k);
     p.ld_h = up4(inner), p.ld_z = up4(cols);
-    p.h = (float *)workspace, p.z = p.h + p.entries * p.ld_h;
+    p.h = (float *)workspace, p.z = (float *)((unsigned char *)workspace + plan.z_at);
     p.ldx = ldx * 2, p.ld_up = ld_up * 2, p.stride_up = stride_up * 2, p.ld_down = ld_down * 2;
     p.stride_down = stride_down * 2, p.ldy = ldy * es, p.ld_ids = ld_ids, p.ld_weights = ld_weights;
     p.tokens = (int)tokens, p.top_k = (int)top_k, p.experts = (int)experts, p.cols = (int)cols;
     p.inner = (int)inner;
-    const int64_t slots = p.entries < experts ? p.entries : experts;
-    const int vu = inner >= 8 ? 4 : 1, vd = cols >= 8 ? 8 : 1;
-    const int64_t up_x = ceil_quot(inner, 16 * vu), down_x = ceil_quot(cols, 16 * vd), join_x = ceil_quot(cols, 256);
-    const int64_t most = (int64_t)UINT32_MAX / THREADS;
-    if (up_x * slots > most || down_x * slots > most || join_x * tokens > most) return TDG_ERR_UNSUPPORTED;
+    p.parts = (int)plan.parts, p.parts_z = (int)plan.parts_z, p.piece = (int)plan.piece;
+    const int64_t join_x = ceil_quot(cols, 256), most = (int64_t)UINT32_MAX / 1024;
+    if (plan.up_x * plan.slots * plan.parts > most || plan.down_x * plan.slots * plan.parts_z > most ||
+        join_x * tokens > most)
+        return TDG_ERR_UNSUPPORTED;
     int rc = device_check();
     if (rc != TDG_OK) return rc;
-    if (inner > 0)
-        rc = launch(vu == 4 ? (const void *)&k_layer_up<4, 4> : (const void *)&k_layer_up<4, 1>,
-                    dim3((unsigned)up_x, (unsigned)slots), THREADS, &p, stream);
-    if (rc != TDG_OK) return rc;
-    rc = launch(vd == 8 ? (const void *)&k_layer_down<1, 8> : (const void *)&k_layer_down<1, 1>,
-                dim3((unsigned)down_x, (unsigned)slots), THREADS, &p, stream);
+    if (inner > 0) {
+        // Two row tiles where many experts have more than one (us, one / two: 64
+        // tokens, 2 of 8 experts, 146 / 99; 8 of 64 experts 107.8 / 104.5; 33 tokens, 2
+        // of 8, 32.9 / 36.6).
+        const void *fn = plan.thin_up  ? (const void *)&k_layer_up<2, 1, 8>
+                         : p.entries > 10 * plan.slots ? (const void *)&k_layer_up<2, 8, 8>
+                                       : (const void *)&k_layer_up<1, 8, 8>;
+        rc = launch(fn, dim3((unsigned)plan.up_x, (unsigned)plan.slots, (unsigned)plan.parts), 512, 0, &p, stream);
+        if (rc != TDG_OK) return rc;
+    }
+#define TDG_LAYER_DOWN(...)                                                  \
+    (plan.parts == 1   ? (const void *)&k_layer_down<__VA_ARGS__, 1>         \
+     : plan.parts == 2 ? (const void *)&k_layer_down<__VA_ARGS__, 2>         \
+                       : (const void *)&k_layer_down<__VA_ARGS__, 4>)
+    const void *fn = plan.thin_down ? TDG_LAYER_DOWN(1, 8) : plan.narrow ? TDG_LAYER_DOWN(4, 16) : TDG_LAYER_DOWN(8, 8);
+#undef TDG_LAYER_DOWN
+    rc = launch(fn, dim3((unsigned)plan.down_x, (unsigned)plan.slots, (unsigned)plan.parts_z), plan.narrow ? 1024 : 512,
+                p.parts > 1 ? (size_t)p.piece * 4 * (plan.narrow ? 16 : 8) : 0, &p, stream);
     if (rc != TDG_OK) return rc;
     return launch(es == 2 ? (const void *)&k_layer_join<_Float16> : (const void *)&k_layer_join<float>,
-                  dim3((unsigned)join_x, (unsigned)tokens), 256, &p, stream);
+                  dim3((unsigned)join_x, (unsigned)tokens), 256, 0, &p, stream);
 }
 
 }  // extern "C"
