@@ -393,28 +393,23 @@ struct W4Tile {
     static constexpr int BM = 16 * MT, BN = 16 * CT * WAVES, THREADS = 64 * WAVES;
     static constexpr int ROWS = 4 * WAVES, COPIES = BM / ROWS;  // rows of A that all waves copy at once, how often
     static constexpr int SCALES = 4 / SPAN;                     // scales of a column in a block
-    static constexpr int A_BYTES = BM * 256, CODE_BYTES = CT * 1024, SCALE_BYTES = SCALES * 256;
+    // One copy takes the words of 64 lanes: scales of 64 / (16 CT) groups.
+    static constexpr int AT_ONCE = 4 / CT, SCALE_COPIES = (SCALES + AT_ONCE - 1) / AT_ONCE;
+    static constexpr int A_BYTES = BM * 256, CODE_BYTES = CT * 1024, SCALE_BYTES = SCALE_COPIES * 256;
     static constexpr int WAVE_BYTES = CODE_BYTES + SCALE_BYTES * (ZEROS ? 2 : 1);
     static constexpr int STAGE = A_BYTES + WAVES * WAVE_BYTES;
     static_assert(BM % ROWS == 0 && ROWS % 16 == 0, "A's rows must split evenly, and their swizzle repeat");
     static_assert(2 * STAGE <= 160 * 1024, "two buffers");
 };
 
-// As copy_to_lds, 2 bytes (1 byte) at each lane's address to the word at m0 + 4 lane.
+// As copy_to_lds, 2 bytes (1 byte) from each lane's address to the word at m0 + 4 lane.
 template <int BYTES>
-__device__ __forceinline__ void copy_word_to_lds(const unsigned char *base, uint32_t off, uint32_t m0) {
+__device__ __forceinline__ void copy_word_to_lds(const unsigned char *src, uint32_t m0) {
     static_assert(BYTES == 1 || BYTES == 2, "what a word is made of");
-    uint64_t safe;
     if constexpr (BYTES == 2)
-        asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_ushort %1, %0"
-                     : "=&s"(safe)
-                     : "v"(off), "s"(base), "{m0}"(m0)
-                     : "memory");
+        asm volatile("s_nop 0\n\tglobal_load_lds_ushort %0, off" ::"v"((uint64_t)(uintptr_t)src), "{m0}"(m0) : "memory");
     else
-        asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_ubyte %1, %0"
-                     : "=&s"(safe)
-                     : "v"(off), "s"(base), "{m0}"(m0)
-                     : "memory");
+        asm volatile("s_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"((uint64_t)(uintptr_t)src), "{m0}"(m0) : "memory");
 }
 
 template <class T>
@@ -437,10 +432,18 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
 #pragma unroll
     for (int t = 0; t < T::CT; t++)
         code_off[t] = (uint32_t)(min(t * 16 + (lane >> 2), last) * 64 + (((lane & 3) ^ (lane >> 4)) << 4));
-    const uint32_t own = (uint32_t)min(lane % (16 * T::CT), last);
-    const unsigned char *codes = w.codes + (int64_t)first * 64, *scales = w.scales + (int64_t)first * 2;
-    const unsigned char *zeros = w.zeros + first;
-    int into = 0;  // k of the next block's first scale in its group
+    const unsigned char *codes = w.codes + (int64_t)first * 64;
+    // The lane's next scale: its column, k, and k counted from its group's start.
+    int at_k[T::SCALE_COPIES], into[T::SCALE_COPIES];
+    const unsigned char *scale[T::SCALE_COPIES], *zero[T::SCALE_COPIES];
+#pragma unroll
+    for (int i = 0; i < T::SCALE_COPIES; i++) {
+        at_k[i] = min(i * T::AT_ONCE + lane / (16 * T::CT), T::SCALES - 1) * 32 * T::SPAN;
+        const int own = min(lane % (16 * T::CT), last), g = min(at_k[i], p.K - 1) / p.group;
+        into[i] = at_k[i] - g * p.group;
+        scale[i] = w.scales + g * w.ld_scales + (int64_t)(first + own) * 2;
+        if constexpr (T::ZEROS) zero[i] = w.zeros + g * w.ld_zeros + first + own;
+    }
 
     // (Blocks are copied in order: each moves codes, scales and zeros on.)
     auto issue = [&](int b) {
@@ -473,13 +476,18 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
         for (int t = 0; t < T::CT; t++) copy_to_lds(codes, code_off[t], mine + t * 1024);
         codes += w.ld_codes;
 #pragma unroll
-        for (int g = 0; g < T::SCALES; g++) {
-            copy_word_to_lds<2>(scales, own * 2, mine + T::CODE_BYTES + g * 256);
-            if constexpr (T::ZEROS) copy_word_to_lds<1>(zeros, own, mine + T::CODE_BYTES + T::SCALE_BYTES + g * 256);
-            into += 32 * T::SPAN;
-            if (into >= p.group && b * BLOCK + (g + 1) * 32 * T::SPAN < p.K) {
-                into = 0;
-                scales += w.ld_scales, zeros += w.ld_zeros;
+        for (int i = 0; i < T::SCALE_COPIES; i++) {
+            copy_word_to_lds<2>(scale[i], mine + T::CODE_BYTES + i * 256);
+            if constexpr (T::ZEROS) copy_word_to_lds<1>(zero[i], mine + T::CODE_BYTES + T::SCALE_BYTES + i * 256);
+            // On to the group that holds k of the next block (not past the last k's).
+            at_k[i] += BLOCK, into[i] += BLOCK;
+            if (at_k[i] >= p.K) continue;
+#pragma unroll
+            for (int j = 0; j < T::SCALES; j++) {
+                const bool on = into[i] >= p.group;
+                into[i] -= on ? p.group : 0;
+                scale[i] += on ? w.ld_scales : 0;
+                if constexpr (T::ZEROS) zero[i] += on ? w.ld_zeros : 0;
             }
         }
     };
@@ -501,12 +509,12 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
             const u32x4 word = lds_read16(mine + t * 1024 + c * 64 + ((q ^ (c >> 2)) << 4));
 #pragma unroll
             for (int g = 0; g < T::SCALES; g++) {
-                const uint32_t bits = *(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + g * 256 + (t * 16 + c) * 4);
+                const uint32_t bits = *(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + ((g * T::CT + t) * 16 + c) * 4);
                 scale[t][g] = b * BLOCK + g * 32 * T::SPAN < p.K ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits) : 0.0f;
                 f16x2 z1024 = {(_Float16)1032.0f, (_Float16)1032.0f}, z64 = {(_Float16)72.0f, (_Float16)72.0f};
                 if constexpr (T::ZEROS) {
-                    const float z = (float)*(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + T::SCALE_BYTES + g * 256 +
-                                                                       (t * 16 + c) * 4);
+                    const float z = (float)*(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + T::SCALE_BYTES +
+                                                                       ((g * T::CT + t) * 16 + c) * 4);
                     z1024[0] = z1024[1] = (_Float16)(z + 1024.0f), z64[0] = z64[1] = (_Float16)(z + 64.0f);
                 }
 #pragma unroll
