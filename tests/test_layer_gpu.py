@@ -92,6 +92,29 @@ def test_layer(lib, T, k, E, cols, inner, dtype):
     near(got, *layer64(*p, dtype))
 
 
+# Every way to cut the work: k of the up product in two and four parts beside both
+# shapes of down, k of down in two, more rows than one tile with each.
+CUTS = [(3, 2, 8, 600, 200), (2, 2, 8, 1100, 600), (20, 2, 16, 1600, 520), (20, 2, 16, 1600, 500), (40, 1, 2, 1030, 100),
+        (64, 8, 64, 1100, 130), (1, 1, 1, 4096, 1100), (50, 1, 2, 520, 700), (33, 2, 8, 2050, 300), (2, 2, 4, 1025, 129)]
+
+
+@pytest.mark.parametrize("T,k,E,cols,inner", CUTS)
+def test_every_cut_of_the_work(lib, T, k, E, cols, inner):
+    p = problem(rng(T, k, E, cols, inner), T, k, E, cols, inner)
+    p = p[:1] + (torch.where(p[1] == 0, -1, p[1]).to(torch.int32) if T > 20 else p[1],) + p[2:]
+    need = lib.tdg_expert_layer_workspace(T, k, E, cols, inner)
+    work = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN, wherever it is read
+    got = lib.tdg_expert_layer(*(t.cuda() for t in p), out_dtype=F32, workspace=work)
+    near(got, *layer64(*p, F32))
+
+
+def test_no_inner_columns_give_zeros(lib):
+    x, ids, w, up, down = problem(rng(2), 3, 2, 4, 20, 8)
+    y = torch.full((3, 20), 5.0, device="cuda")
+    lib.tdg_expert_layer(x.cuda(), ids.cuda(), w.cuda(), up[:, :, :0].cuda(), down[:, :0].cuda(), out=y)
+    assert (y == 0).all()
+
+
 @pytest.mark.parametrize("T,k,E", [(1, 6, 2), (30, 3, 2), (64, 32, 2), (20, 4, 100)])
 def test_the_same_expert_twice_and_ids_outside(lib, T, k, E):
     r = rng(T, k, E)

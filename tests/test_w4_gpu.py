@@ -345,6 +345,29 @@ def test_rows_more_than_32_bits_apart(lib, M):
     near(C, x.double() @ w.value, bound(x, w.value, K))
 
 
+def test_tiles_whose_rows_pass_32_bits(lib):
+    """Rows near enough for the LDS tiles' offsets, 6 GB in all."""
+    r = rng(10)
+    M, K, N, far = 400, 140, 3000, 8 << 20
+    w, x = Weights(r, K, N, 64, False), normal(r, M, K)
+    rows = torch.empty(far * (M - 1) + K, dtype=F16, device="cuda").as_strided((M, K), (far, 1))
+    rows.copy_(x)
+    near(lib.gemm_f16w4f32(rows, *w.all, group=64), x.double() @ w.value, bound(x, w.value, K))
+
+
+@pytest.mark.parametrize("group", [64, 96])
+def test_quantizing_rows_that_pass_32_bits(lib, group):
+    K, N, far = 200, 40, 16 << 20
+    w = normal(rng(group), K, N)
+    rows = torch.empty(far * (K - 1) + N, dtype=F16, device="cuda").as_strided((K, N), (far, 1))
+    rows.copy_(w)
+    got = lib.tdg_w4_quantize(rows, group, True)
+    check_quantized(got, w, group, True)
+    out = torch.empty(far * (K - 1) + N, dtype=F16, device="cuda").as_strided((K, N), (far, 1))
+    lib.tdg_w4_dequantize(*got, K=K, group=group, out=out)
+    assert torch.equal(out.cpu(), lib.tdg_w4_dequantize(*got, K=K, group=group).cpu())
+
+
 # ------------------------------------------------------------------ the experts' products
 
 GROUPED = [(1, 1, 1, 1, 32), (4, 9, 33, 100, 64), (64, 32, 48, 256, 128), (37, 3, 130, 257, 96), (333, 9, 61, 1000, 32),

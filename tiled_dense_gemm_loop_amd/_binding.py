@@ -984,6 +984,15 @@ def _w4(codes, scales, zeros, K, group, dev, stack):
     return count, N, (pc, ldc, sc, ps, lds, ss, pz, ldz, sz)
 
 
+def _new(shape, dtype, t):
+    """A dense tensor on t's device."""
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= d or 1
+    return _empty(shape, strides[::-1], dtype=dtype, device=t.device)
+
+
 def tdg_w4_quantize(W, group: int = 128, zeros=False, codes=None, scales=None):
     """4-bit weights of W (K x N, or count x K x N; float16): (codes, scales,
     zeros), with zero points where `zeros` is True or a uint8 tensor for them,
@@ -1004,23 +1013,25 @@ def tdg_w4_quantize(W, group: int = 128, zeros=False, codes=None, scales=None):
     group = int(group)
     if group < 32 or group % 32:
         raise ValueError("group must be a multiple of 32, got %d" % group)
-    front, groups, blocks = (count,) if stack else (), (K + group - 1) // group, (K + 127) // 128
-
-    def new(rows, cols, dtype):
-        strides = (rows * cols, cols, 1) if stack else (cols, 1)
-        return _empty(front + (rows, cols), strides, dtype=dtype, device=W.device)
-
+    blocks, groups = (K + 127) // 128, (K + group - 1) // group
+    front = (count,) if stack else ()
+    fresh = codes is None and scales is None and isinstance(zeros, bool)
     if codes is None:
-        codes = new(blocks, N * 64, _BYTE[0]).view(front + (blocks, N, 64))
+        codes = _new(front + (blocks, N, 64), _BYTE[0], W)
     if scales is None:
-        scales = new(groups, N, _HALF[0])
+        scales = _new(front + (groups, N), _HALF[0], W)
     if zeros is False:
         zeros = None
     elif zeros is True:
-        zeros = new(groups, N, _BYTE[0])
-    n, cols, places = _w4(codes, scales, zeros, K, group, dev, stack)
-    if n != count or cols != N:
-        raise ValueError("codes have shape %s, W %s" % (tuple(codes.shape), tuple(W.shape)))
+        zeros = _new(front + (groups, N), _BYTE[0], W)
+    if fresh:
+        ld, sg = N or 1, groups * (N or 1)
+        places = (codes.data_ptr(), ld, blocks * ld, scales.data_ptr(), ld, sg,
+                  None if zeros is None else zeros.data_ptr(), ld, sg)
+    else:
+        n, cols, places = _w4(codes, scales, zeros, K, group, dev, stack)
+        if n != count or cols != N:
+            raise ValueError("codes have shape %s, W %s" % (tuple(codes.shape), tuple(W.shape)))
     _launch("tdg_w4_quantize", dev, count, K, N, group, pw, ldw, sw, *places)
     return codes, scales, zeros
 
@@ -1040,8 +1051,7 @@ def tdg_w4_dequantize(codes, scales, zeros=None, K=None, group: int = 128, out=N
     K, group = int(K), int(group)
     count, N, places = _w4(codes, scales, zeros, K, group, dev, stack)
     if out is None:
-        shape, strides = ((count, K, N), (K * N, N, 1)) if stack else ((K, N), (N, 1))
-        out = _empty(shape, strides, dtype=out_dtype or _HALF[0], device=codes.device)
+        out = _new((count, K, N) if stack else (K, N), out_dtype or _HALF[0], codes)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out has dtype %s, out_dtype is %s" % (out.dtype, out_dtype))
     if stack:
@@ -1055,6 +1065,18 @@ def tdg_w4_dequantize(codes, scales, zeros=None, K=None, group: int = 128, out=N
     return out
 
 
+def _result(C, M, N, A, dev):
+    """(tensor, address, ld) of a product's M x N float32 result on A's device,
+    allocated when not given."""
+    if C is None:
+        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
+        return C, C.data_ptr(), N or 1
+    Mc, Nc, p, ld, _ = _mat(C, _SINGLE, "C", dev)
+    if Mc != M or Nc != N:
+        raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
+    return C, p, ld
+
+
 def gemm_f16w4f32(A, codes, scales, zeros=None, group: int = 128, C=None):
     """C (float32) = A (M x K, float16) times 4-bit weights as tdg_w4_quantize
     makes them (zeros None: 8)."""
@@ -1062,11 +1084,7 @@ def gemm_f16w4f32(A, codes, scales, zeros=None, group: int = 128, C=None):
         _types()
     M, K, pa, lda, dev = _mat(A, _HALF, "A")
     _, N, (pc, ldc, _, ps, lds, _, pz, ldz, _) = _w4(codes, scales, zeros, K, group, dev, False)
-    if C is None:
-        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
-    Mc, Nc, p_out, ld_out, _ = _mat(C, _SINGLE, "C", dev)
-    if Mc != M or Nc != N:
-        raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
+    C, p_out, ld_out = _result(C, M, N, A, dev)
     _launch("gemm_f16w4f32", dev, M, N, K, int(group), pa, lda, pc, ldc, ps, lds, pz, ldz, p_out, ld_out)
     return C
 
@@ -1082,11 +1100,7 @@ def gemm_f16w4f32_grouped(A, codes, scales, offsets, zeros=None, group: int = 12
     n_off, p_off = _offsets_of(offsets, dev)
     if n_off != count:
         raise ValueError("offsets name %d groups, codes have %d" % (n_off, count))
-    if C is None:
-        C = _empty((M, N), (N, 1), dtype=_SINGLE[0], device=A.device)
-    Mc, Nc, p_out, ld_out, _ = _mat(C, _SINGLE, "C", dev)
-    if Mc != M or Nc != N:
-        raise ValueError("C has shape %s, expected %s" % ((Mc, Nc), (M, N)))
+    C, p_out, ld_out = _result(C, M, N, A, dev)
     _launch("gemm_f16w4f32_grouped", dev, count, p_off, M, N, K, int(group), pa, lda, *places, p_out, ld_out)
     return C
 

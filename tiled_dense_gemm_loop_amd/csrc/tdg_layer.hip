@@ -472,7 +472,9 @@ int tdg_expert_layer(int out_elem, int64_t tokens, int64_t top_k, int64_t expert
     (plan.parts == 1   ? (const void *)&k_layer_down<__VA_ARGS__, 1>         \
      : plan.parts == 2 ? (const void *)&k_layer_down<__VA_ARGS__, 2>         \
                        : (const void *)&k_layer_down<__VA_ARGS__, 4>)
-    const void *fn = plan.thin_down ? TDG_LAYER_DOWN(1, 8) : plan.narrow ? TDG_LAYER_DOWN(4, 16) : TDG_LAYER_DOWN(8, 8);
+    const void *fn = plan.thin_down ? (const void *)&k_layer_down<1, 8, 1>  // (with few columns k is not cut)
+                     : plan.narrow  ? TDG_LAYER_DOWN(4, 16)
+                                    : TDG_LAYER_DOWN(8, 8);
 #undef TDG_LAYER_DOWN
     rc = launch(fn, dim3((unsigned)plan.down_x, (unsigned)plan.slots, (unsigned)plan.parts_z), plan.narrow ? 1024 : 512,
                 p.parts > 1 ? (size_t)p.piece * 4 * (plan.narrow ? 16 : 8) : 0, &p, stream);
