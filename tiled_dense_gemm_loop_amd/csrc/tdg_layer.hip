@@ -10,8 +10,8 @@
 // workgroup works for one expert: it finds the expert's entries (e = t * top_k
 // + j) among the ids by itself, so that nothing is sorted before.
 //   * k_layer_up: FP16 products of x, FP32 sums; h in FP32 to the workspace.
-//   * k_layer_down: h stays FP32, on v_mfma_f32_16x16x4_f32, whose rate on up to
-//     16 rows is still above that of reading the weights; z = h . down in FP32.
+//   * k_layer_down: z = h . down with h as it is, on the FP32 matrix instructions:
+//     up to 16 rows at a time keep about the pace of reading the weights.
 //   * k_layer_join: y from the tokens' rows of z, in the order of j, rounded once.
 // Rows of a tile belong to one expert alone, so no token meets a weight of an
 // expert that it did not pick, whatever that holds.
@@ -259,77 +259,94 @@ __device__ __forceinline__ void join_token(const LayerArgs &p, int t, int n) {
     *(T *)(p.y + t * p.ldy + (int64_t)n * sizeof(T)) = (T)sum;
 }
 
-// A workgroup has 16 V columns of down; lane l loads V of them at k = 4 (l / 16)
-// .. + 3, and the product's e-th step takes row e of each.
+// The down product of up to 16 rows of an expert: a workgroup has 16 V columns,
+// lane l loads V of them at k = 4 q .. + 3 of each 16, q = l / 16, and the e-th
+// products take row e of those.  FOURS = 0: v_mfma_f32_16x16x4_f32, a product of 16
+// rows at the four k of the lane groups.  FOURS = 1: four rows on
+// v_mfma_f32_4x4x1_16b_f32, a quarter of its time: 16 blocks of
+// four lanes' columns, each at its own lanes' k, so that a column's sum is spread
+// over the four lane groups, and added at the end.  Most experts of a few tokens
+// have four rows or fewer, and the time of 16 rows' products shows: it is as long
+// as that of reading the weights (16 tokens, 8 of 64 experts, 2048 x 1024: 47 us
+// without loads, 47 without products, 58.6 with both; with four rows' products 55;
+// one token 10.3 and 8.0).
+template <int V, int NW, int PARTS, bool FOURS>
+__device__ __forceinline__ void down_rows(const LayerArgs &p, const unsigned char *down, const int *list, int rows,
+                                          int want, int n, int s0, int s1, float *piece,
+                                          float (&part)[NW][1][V * 64]) {
+    constexpr bool JOIN = PARTS > 1;
+    typedef typename Halves<V>::vec vec;
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    auto load = [&](vec (&w)[4], int s) {
+        load_rows<V, 4>(w, down, p.ld_down, s * 16 + q * 4, p.inner, s * 16 + 16 > p.inner);
+    };
+    vec w[4];
+    if constexpr (JOIN) {  // the first weights travel while h is joined
+        if (s0 < s1) load(w, s0);
+        const int len = (s1 - s0) * 16;
+        if (rows * len > 256) join_h<PARTS, 4>(p, list, rows, s0 * 16, len, lane, piece);
+        else join_h<PARTS, 1>(p, list, rows, s0 * 16, len, lane, piece);
+    }
+    const int row = min(FOURS ? lane & 3 : c, rows - 1);  // (rows behind the last: not stored)
+    const float *h = JOIN ? piece + row * (s1 - s0) * 16 - s0 * 16 : p.h + list[row] * p.ld_h;
+    f32x4 acc[V] = {};
+    for (int s = s0; s < s1; s++) {
+        const int k = s * 16 + q * 4;
+        // (Loads a step ahead: 63.6 us for 58.6 at 16 tokens, for the waves that their
+        // registers cost.)
+        if (!JOIN || s > s0) load(w, s);
+        f32x4 a = {};
+        if (JOIN || k < p.inner) a = *(const f32x4 *)(h + k);  // (rows are whole pieces of four)
+        if (!JOIN && s * 16 + 16 > p.inner) {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (k + e >= p.inner) a[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                const float ae = a[e], be = (float)element<V>(w[e], v);
+                if constexpr (FOURS) acc[v] = __builtin_amdgcn_mfma_f32_4x4x1f32(ae, be, acc[v], 0, 0, 0);
+                else acc[v] = __builtin_amdgcn_mfma_f32_16x16x4f32(ae, be, acc[v], 0, 0, 0);
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        if (r >= rows) break;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; v++) part[wave][0][v * 64 + lane] = acc[v][r];
+        __syncthreads();
+        for (int e = tid; e < V * 64; e += NW * 64) {  // (e % 64 == lane)
+            float sum = join_waves(part, 0, e);
+            if constexpr (FOURS) sum += __shfl_xor(sum, 16), sum += __shfl_xor(sum, 32);
+            const int at = FOURS ? r : q * 4 + r;
+            if (at < rows && want < p.cols && (!FOURS || q == 0))
+                p.z[((int64_t)blockIdx.z * p.entries + list[at]) * p.ld_z + n + (e >> 6)] = sum;
+        }
+    }
+}
+
 template <int V, int NW, int PARTS>
 __global__ void __launch_bounds__(NW * 64) k_layer_down(LayerArgs p) {
     __shared__ int list[MAX_ENTRIES];
     __shared__ float part[NW][1][V * 64];
-    constexpr bool JOIN = PARTS > 1;
-    extern __shared__ __attribute__((aligned(16))) float pieces[];  // JOIN: a piece of h for each wave
-    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    extern __shared__ __attribute__((aligned(16))) float pieces[];  // PARTS > 1: a piece of h for each wave
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Mine mine = find_entries(p, blockIdx.y, list);
     if (mine.count == 0) return;
-    typedef typename Halves<V>::vec vec;
-    const int want = ((int)blockIdx.x * 16 + c) * V, n = min(want, p.cols - V);
+    const int want = ((int)blockIdx.x * 16 + (threadIdx.x & 15)) * V, n = min(want, p.cols - V);
     const unsigned char *down = p.down + mine.expert * p.stride_down + (int64_t)n * 2;
     const int steps = (p.inner + 15) / 16, runs = NW * p.parts_z, run = (int)blockIdx.z * NW + wave;
     const int s0 = (int)((int64_t)steps * run / runs), s1 = (int)((int64_t)steps * (run + 1) / runs);
-    float *piece = JOIN ? pieces + wave * p.piece : nullptr;
+    float *piece = PARTS > 1 ? pieces + wave * p.piece : nullptr;
     __syncthreads();
     for (int r0 = 0; r0 < mine.count; r0 += 16) {
-        const int rows = min(16, mine.count - r0), row = min(c, rows - 1);  // (rows behind the last: not stored)
-        const float *h = JOIN ? piece + row * (s1 - s0) * 16 - s0 * 16 : p.h + list[r0 + row] * p.ld_h;
-        f32x4 acc[V] = {};
-        auto load = [&](vec (&w)[4], int s) {
-            load_rows<V, 4>(w, down, p.ld_down, s * 16 + q * 4, p.inner, s * 16 + 16 > p.inner);
-        };
-        vec next[4];
-        if constexpr (JOIN) {  // the first weights travel while h is joined
-            if (s0 < s1) load(next, s0);
-            const int len = (s1 - s0) * 16;
-            if (rows * len > 256) join_h<PARTS, 4>(p, list + r0, rows, s0 * 16, len, lane, piece);
-            else join_h<PARTS, 1>(p, list + r0, rows, s0 * 16, len, lane, piece);
-        }
-        for (int s = s0; s < s1; s++) {
-            const int k = s * 16 + q * 4;
-            vec w[4];
-            if constexpr (JOIN) {
-#pragma unroll
-                for (int e = 0; e < 4; e++) w[e] = next[e];
-                if (s + 1 < s1) load(next, s + 1);
-            } else {  // (one step ahead: 63.6 us for 58.6 at 16 tokens, for the waves that its registers cost)
-                load(w, s);
-            }
-            f32x4 a = {};
-            if (JOIN || k < p.inner) a = *(const f32x4 *)(h + k);  // (rows are whole pieces of four)
-            if (!JOIN && s * 16 + 16 > p.inner) {
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (k + e >= p.inner) a[e] = 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-#pragma unroll
-                for (int v = 0; v < V; v++) {
-                    const float ae = a[e], be = (float)element<V>(w[e], v);
-                    acc[v] = __builtin_amdgcn_mfma_f32_16x16x4f32(ae, be, acc[v], 0, 0, 0);
-                }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            if (r >= rows) break;
-            __syncthreads();
-#pragma unroll
-            for (int v = 0; v < V; v++) part[wave][0][v * 64 + lane] = acc[v][r];
-            __syncthreads();
-            for (int e = tid; e < V * 64; e += NW * 64) {
-                const int at = q * 4 + r;
-                if (at < rows && want < p.cols)
-                    p.z[((int64_t)blockIdx.z * p.entries + list[r0 + at]) * p.ld_z + n + (e >> 6)] = join_waves(part, 0, e);
-            }
-        }
+        const int rows = min(16, mine.count - r0);
+        if (rows <= 4) down_rows<V, NW, PARTS, true>(p, down, list + r0, rows, want, n, s0, s1, piece, part);
+        else down_rows<V, NW, PARTS, false>(p, down, list + r0, rows, want, n, s0, s1, piece, part);
     }
 }
 
