@@ -648,18 +648,18 @@ struct Variant4 {
 
 // The kernel of a shape for the group length and with or without zero points:
 // a sum takes as many matrix instructions as the groups and blocks allow.
-#define TDG_W4_FN(KERNEL, ...)                                             \
-    (q.group % 128 == 0  ? (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, 4, true>   \
-                                    : (const void *)&KERNEL<__VA_ARGS__, 4, false>) \
-     : q.group % 64 == 0 ? (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, 2, true>   \
-                                    : (const void *)&KERNEL<__VA_ARGS__, 2, false>) \
-                         : (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, 1, true>   \
-                                    : (const void *)&KERNEL<__VA_ARGS__, 1, false>))
+// (LEAST: the fewest that a call can ask it for.)
+#define TDG_W4_SPAN(KERNEL, SPAN, ...) \
+    (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, SPAN, true> : (const void *)&KERNEL<__VA_ARGS__, SPAN, false>)
+#define TDG_W4_FN(KERNEL, LEAST, ...)                                      \
+    (q.group % 128 == 0                 ? TDG_W4_SPAN(KERNEL, 4, __VA_ARGS__) \
+     : q.group % 64 == 0 || LEAST == 2  ? TDG_W4_SPAN(KERNEL, 2, __VA_ARGS__) \
+                                        : TDG_W4_SPAN(KERNEL, (LEAST == 2 ? 2 : 1), __VA_ARGS__))
 
 template <int MT, int CT, int NW>
 Variant4 few(const W4Args &p, const Named4 &q) {
     const int64_t z = p.offsets ? 1 : ceil_quot(p.rows, 16 * MT);
-    return {TDG_W4_FN(k_w4_few, MT, CT, NW),
+    return {TDG_W4_FN(k_w4_few, 1, MT, CT, NW),
             grid_of(ceil_quot(q.N, 16 * CT), p.row_groups, z > 65535 ? 65535 : z), NW * 64};
 }
 
@@ -670,13 +670,13 @@ int64_t tiles_of(const W4Args &p, int64_t live, int64_t bm, int64_t bn) {
     return (high > live ? high : live) * ceil_quot(p.N, bn);
 }
 
-template <int MT, int CT, int WAVES>
+template <int MT, int CT, int WAVES, int LEAST = 1>
 Variant4 tiled(W4Args &p, const Named4 &q, int64_t live) {
     typedef W4Tile<MT, CT, WAVES, 4, false> T;
     p.tiles_m = (int)ceil_quot(p.rows, T::BM), p.tiles_n = (int)ceil_quot(q.N, T::BN);
     // (Most tiles: every group can end inside one, and needs a row for it.)
     const int64_t most = p.offsets ? ceil_quot((p.rows / T::BM + live) * p.tiles_n, 8) * 8 : (int64_t)p.tiles_m * p.tiles_n;
-    return {TDG_W4_FN(k_w4_tile, MT, CT, WAVES), dim3(most <= INT32_MAX - 65536 ? (unsigned)most : UINT32_MAX), T::THREADS};
+    return {TDG_W4_FN(k_w4_tile, LEAST, MT, CT, WAVES), dim3(most <= INT32_MAX - 65536 ? (unsigned)most : UINT32_MAX), T::THREADS};
 }
 
 Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
@@ -704,9 +704,11 @@ Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
     }
     // Tiles.  128 x 512, one to a CU, where its rounds of 256 are full (us, against
     // 64 x 256: 4096 x 4096 x 4096, 256 tiles, 121 / 138; 3000 x 11008 x 2048, 528,
-    // 174 / 150; 16 groups of 1024 rows, 4096 x 4096, 1088 588 / 585).
+    // 174 / 150; 16 groups of 1024 rows, 4096 x 4096, 1088 588 / 585).  A scale for
+    // each 32 k asks for more registers than there are (4096 x 8192 x 4096: 471 / 351).
     const int64_t large = tiles_of(p, live, 128, 512);
-    if (large * 100 > ceil_quot(large, 256) * 256 * 85 && p.rows >= 1024 * live) return tiled<8, 4, 8>(p, q, live);
+    if (large * 100 > ceil_quot(large, 256) * 256 * 85 && p.rows >= 1024 * live && q.group % 64 == 0)
+        return tiled<8, 4, 8, 2>(p, q, live);
     // A few rows of each group: 32 x 128, or 64 wide (us, against 64 x 128 / 32 x 64:
     // 32 groups of 2048 x 2048, 600 rows 20.3, 25.2 / 21.4; 1000 rows 25.4, 26.1 /
     // 30.1; 2000 rows -, 32.7 / -; 9 groups of 1537 x 1000, 333 rows 8.6, 9.7 / 7.9).
