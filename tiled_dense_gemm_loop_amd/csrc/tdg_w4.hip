@@ -384,8 +384,11 @@ __global__ void __launch_bounds__(NW * 64) k_w4_few(W4Args p) {
 // accumulators times the scale.  What bounds it: the copies' rate from L2, which
 // tall and wide tiles spare, and the vector instructions that unpack and scale, so
 // that tiles small enough for two or three workgroups to a CU do better than a
-// third buffer (8192 rows, 16 matrices of 4096 x 4096: 64 x 256 tiles 291 us,
-// with three buffers 319 and more).
+// third buffer (8192 rows, 16 matrices of 4096 x 4096, groups of
+// 128: 64 x 256 tiles 291-310 us, 0.9 PFLOP/s, 128 x 256 with three buffers 319; groups
+// of 64 326-338, the matrix cores busy for 44% of the time and vector instructions
+// issued in 75%.  4096 x 8192 x 4096: 225-239 us, 1.2 PFLOP/s, the plain FP16 product's
+// rate).
 template <int MT_, int CT_, int WAVES_, int SPAN_, bool ZEROS_>
 struct W4Tile {
     static constexpr int MT = MT_, CT = CT_, WAVES = WAVES_, SPAN = SPAN_;
@@ -439,7 +442,7 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
 #pragma unroll
     for (int i = 0; i < T::SCALE_COPIES; i++) {
         at_k[i] = min(i * T::AT_ONCE + lane / (16 * T::CT), T::SCALES - 1) * 32 * T::SPAN;
-        const int own = min(lane % (16 * T::CT), last), g = min(at_k[i], p.K - 1) / p.group;
+        const int own = min(lane % (16 * T::CT), last), g = at_k[i] / p.group;
         into[i] = at_k[i] - g * p.group;
         scale[i] = w.scales + g * w.ld_scales + (int64_t)(first + own) * 2;
         if constexpr (T::ZEROS) zero[i] = w.zeros + g * w.ld_zeros + first + own;
@@ -477,13 +480,14 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
         codes += w.ld_codes;
 #pragma unroll
         for (int i = 0; i < T::SCALE_COPIES; i++) {
-            copy_word_to_lds<2>(scale[i], mine + T::CODE_BYTES + i * 256);
-            if constexpr (T::ZEROS) copy_word_to_lds<1>(zero[i], mine + T::CODE_BYTES + T::SCALE_BYTES + i * 256);
-            // On to the group that holds k of the next block (not past the last k's).
+            // (From the end of k on there are no groups: zeros.)
+            const unsigned char *none = (const unsigned char *)tdg_zero16;
+            copy_word_to_lds<2>(at_k[i] < p.K ? scale[i] : none, mine + T::CODE_BYTES + i * 256);
+            if constexpr (T::ZEROS)
+                copy_word_to_lds<1>(at_k[i] < p.K ? zero[i] : none, mine + T::CODE_BYTES + T::SCALE_BYTES + i * 256);
             at_k[i] += BLOCK, into[i] += BLOCK;
-            if (at_k[i] >= p.K) continue;
 #pragma unroll
-            for (int j = 0; j < T::SCALES; j++) {
+            for (int j = 0; j < T::SCALES; j++) {  // on to the group that holds k of the next block
                 const bool on = into[i] >= p.group;
                 into[i] -= on ? p.group : 0;
                 scale[i] += on ? w.ld_scales : 0;
@@ -510,7 +514,8 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
 #pragma unroll
             for (int g = 0; g < T::SCALES; g++) {
                 const uint32_t bits = *(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + ((g * T::CT + t) * 16 + c) * 4);
-                scale[t][g] = b * BLOCK + g * 32 * T::SPAN < p.K ? (float)__builtin_bit_cast(_Float16, (unsigned short)bits) : 0.0f;
+                scale[t][g] = (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
+                asm("" : "+v"(scale[t][g]));  // converted once: not by each of the products that take it
                 f16x2 z1024 = {(_Float16)1032.0f, (_Float16)1032.0f}, z64 = {(_Float16)72.0f, (_Float16)72.0f};
                 if constexpr (T::ZEROS) {
                     const float z = (float)*(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + T::SCALE_BYTES +
@@ -648,18 +653,17 @@ struct Variant4 {
 
 // The kernel of a shape for the group length and with or without zero points:
 // a sum takes as many matrix instructions as the groups and blocks allow.
-// (LEAST: the fewest that a call can ask it for.)
 #define TDG_W4_SPAN(KERNEL, SPAN, ...) \
     (q.zeros ? (const void *)&KERNEL<__VA_ARGS__, SPAN, true> : (const void *)&KERNEL<__VA_ARGS__, SPAN, false>)
-#define TDG_W4_FN(KERNEL, LEAST, ...)                                      \
-    (q.group % 128 == 0                 ? TDG_W4_SPAN(KERNEL, 4, __VA_ARGS__) \
-     : q.group % 64 == 0 || LEAST == 2  ? TDG_W4_SPAN(KERNEL, 2, __VA_ARGS__) \
-                                        : TDG_W4_SPAN(KERNEL, (LEAST == 2 ? 2 : 1), __VA_ARGS__))
+#define TDG_W4_FN(KERNEL, ...)                                \
+    (q.group % 128 == 0  ? TDG_W4_SPAN(KERNEL, 4, __VA_ARGS__) \
+     : q.group % 64 == 0 ? TDG_W4_SPAN(KERNEL, 2, __VA_ARGS__) \
+                         : TDG_W4_SPAN(KERNEL, 1, __VA_ARGS__))
 
 template <int MT, int CT, int NW>
 Variant4 few(const W4Args &p, const Named4 &q) {
     const int64_t z = p.offsets ? 1 : ceil_quot(p.rows, 16 * MT);
-    return {TDG_W4_FN(k_w4_few, 1, MT, CT, NW),
+    return {TDG_W4_FN(k_w4_few, MT, CT, NW),
             grid_of(ceil_quot(q.N, 16 * CT), p.row_groups, z > 65535 ? 65535 : z), NW * 64};
 }
 
@@ -670,13 +674,17 @@ int64_t tiles_of(const W4Args &p, int64_t live, int64_t bm, int64_t bn) {
     return (high > live ? high : live) * ceil_quot(p.N, bn);
 }
 
-template <int MT, int CT, int WAVES, int LEAST = 1>
-Variant4 tiled(W4Args &p, const Named4 &q, int64_t live) {
-    typedef W4Tile<MT, CT, WAVES, 4, false> T;
+template <class T>
+Variant4 tiled(W4Args &p, const Named4 &q, int64_t live, const void *fn) {
     p.tiles_m = (int)ceil_quot(p.rows, T::BM), p.tiles_n = (int)ceil_quot(q.N, T::BN);
     // (Most tiles: every group can end inside one, and needs a row for it.)
     const int64_t most = p.offsets ? ceil_quot((p.rows / T::BM + live) * p.tiles_n, 8) * 8 : (int64_t)p.tiles_m * p.tiles_n;
-    return {TDG_W4_FN(k_w4_tile, LEAST, MT, CT, WAVES), dim3(most <= INT32_MAX - 65536 ? (unsigned)most : UINT32_MAX), T::THREADS};
+    return {fn, dim3(most <= INT32_MAX - 65536 ? (unsigned)most : UINT32_MAX), T::THREADS};
+}
+
+template <int MT, int CT, int WAVES>
+Variant4 tiled(W4Args &p, const Named4 &q, int64_t live) {
+    return tiled<W4Tile<MT, CT, WAVES, 4, false>>(p, q, live, TDG_W4_FN(k_w4_tile, MT, CT, WAVES));
 }
 
 Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
@@ -704,11 +712,12 @@ Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
     }
     // Tiles.  128 x 512, one to a CU, where its rounds of 256 are full (us, against
     // 64 x 256: 4096 x 4096 x 4096, 256 tiles, 121 / 138; 3000 x 11008 x 2048, 528,
-    // 174 / 150; 16 groups of 1024 rows, 4096 x 4096, 1088 588 / 585).  A scale for
-    // each 32 k asks for more registers than there are (4096 x 8192 x 4096: 471 / 351).
+    // 174 / 150; 16 groups of 1024 rows, 4096 x 4096, 1088 588 / 585).  Shorter
+    // groups' scales ask for more registers than there are (4096 x 8192 x 4096, groups
+    // of 64: 302 / 302, of 32: 471 / 351).
     const int64_t large = tiles_of(p, live, 128, 512);
-    if (large * 100 > ceil_quot(large, 256) * 256 * 85 && p.rows >= 1024 * live && q.group % 64 == 0)
-        return tiled<8, 4, 8, 2>(p, q, live);
+    if (large * 100 > ceil_quot(large, 256) * 256 * 85 && p.rows >= 1024 * live && q.group % 128 == 0)
+        return tiled<W4Tile<8, 4, 8, 4, false>>(p, q, live, TDG_W4_SPAN(k_w4_tile, 4, 8, 4, 8));
     // A few rows of each group: 32 x 128, or 64 wide (us, against 64 x 128 / 32 x 64:
     // 32 groups of 2048 x 2048, 600 rows 20.3, 25.2 / 21.4; 1000 rows 25.4, 26.1 /
     // 30.1; 2000 rows -, 32.7 / -; 9 groups of 1537 x 1000, 333 rows 8.6, 9.7 / 7.9).
