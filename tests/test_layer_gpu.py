@@ -95,7 +95,8 @@ def test_layer(lib, T, k, E, cols, inner, dtype):
 # Every way to cut the work: k of the up product in two and four parts beside both
 # shapes of down, k of down in two, more rows than one tile with each.
 CUTS = [(3, 2, 8, 600, 200), (2, 2, 8, 1100, 600), (20, 2, 16, 1600, 520), (20, 2, 16, 1600, 500), (40, 1, 2, 1030, 100),
-        (64, 8, 64, 1100, 130), (1, 1, 1, 4096, 1100), (50, 1, 2, 520, 700), (33, 2, 8, 2050, 300), (2, 2, 4, 1025, 129)]
+        (64, 8, 64, 1100, 130), (1, 1, 1, 4096, 1100), (50, 1, 2, 520, 700), (33, 2, 8, 2050, 300), (2, 2, 4, 1025, 129),
+        (5, 2, 4, 1024, 2048)]  # (the last: as much LDS as any)
 
 
 @pytest.mark.parametrize("T,k,E,cols,inner", CUTS)
@@ -280,6 +281,19 @@ def test_on_other_streams_and_in_graphs(lib):
         eager = lib.tdg_expert_layer(*dev[(i + 1) % 4])
         torch.cuda.synchronize()
         assert torch.equal(y, want[i]) and torch.equal(eager, want[(i + 1) % 4])
+    # and one whose first product is cut, so that the second joins its parts
+    cut = [[t.cuda() for t in problem(rng(17, i), 3, 2, 8, 1030, 200)] for i in range(2)]
+    eager = [lib.tdg_expert_layer(*c) for c in cut]
+    held = [t.clone() for t in cut[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lib.tdg_expert_layer(*held)
+    for i in (1, 0, 1):
+        for h, t in zip(held, cut[i]):
+            h.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager[i])
     # one workspace for calls of several sizes that follow each other
     small = problem(r, 2, 3, 16, 192, 72)
     near(lib.tdg_expert_layer(*(t.cuda() for t in small), workspace=work[1]), *layer64(*small, F16))

@@ -118,7 +118,24 @@ def test_grids_past_one_launch_are_refused():
     n = 1 << 30
     assert call("gemm_f16w4f32", W4, M=1 << 30, N=n, K=32, a=far[0], lda=32, codes=far[1], ld_codes=n, scales=far[2],
                 ld_scales=n, zeros=None, c=1 << 62, ldc=n) == TOO_BIG
-    assert call("tdg_w4_quantize", QUANT, count=65536, w=far[0], codes=far[1], scales=far[2], zeros=far[3]) == TOO_BIG
+    places = dict(w=far[0], codes=far[1], scales=far[2], zeros=far[3])
+    one = dict(count=1, N=1, ldw=1, ld_codes=1, ld_scales=1, ld_zeros=1)
+    for name, args in (("tdg_w4_quantize", QUANT), ("tdg_w4_dequantize", DEQUANT)):
+        assert call(name, args, count=65536, **places) == TOO_BIG
+        assert call(name, args, **{**one, **places}, K=65535 * 128 + 1) == TOO_BIG
+    assert call("tdg_w4_quantize", QUANT, **{**one, **places}, K=65535 * 96 + 1, group=96) == TOO_BIG
+
+
+@no_device_only
+def test_the_limits_that_the_header_states():
+    """The largest counts that quantize and dequantize take."""
+    far = [i << 55 for i in range(1, 8)]
+    places = dict(w=far[0], codes=far[1], scales=far[2], zeros=far[3])
+    one = dict(count=1, N=1, ldw=1, ld_codes=1, ld_scales=1, ld_zeros=1)
+    for name, args in (("tdg_w4_quantize", QUANT), ("tdg_w4_dequantize", DEQUANT)):
+        assert call(name, args, count=65535, **places) == NODEV
+        assert call(name, args, **{**one, **places}, K=65535 * 128) == NODEV
+    assert call("tdg_w4_quantize", QUANT, **{**one, **places}, K=65535 * 96, group=96) == NODEV
 
 
 def test_workspace_sizes():

@@ -71,7 +71,7 @@ __device__ __forceinline__ ScaleZero scale_of(float lo, float hi) {
 __device__ __forceinline__ uint32_t code_of(float w, ScaleZero g) {
     float q = w * g.r;
     q = rintf(fmaf(fmaf(-q, g.s, w), g.r, q));
-    return (uint32_t)(q != q ? g.z : fminf(fmaxf(q + g.z, 0.0f), 15.0f));
+    return (uint32_t)(q != q ? g.z : __builtin_amdgcn_fmed3f(q + g.z, 0.0f, 15.0f));
 }
 
 __device__ __forceinline__ float load_weight(const unsigned char *p) { return (float)*(const _Float16 *)p; }
@@ -89,45 +89,62 @@ __device__ __forceinline__ void store_scale(const QuantArgs &a, int64_t e, int g
         *(unsigned char *)(a.q.zeros + e * a.q.stride_zeros + g * a.q.ld_zeros + n) = (unsigned char)v.z;
 }
 
-// Groups of G = 32, 64 or 128: one pass, a thread has a column of a block and
-// holds a group of it (4096 x 4096, groups of 128: 15 us, 2.8 TB/s; scales and
-// codes in two passes, with two divisions, 54).
+// Groups of G = 32, 64 or 128: one pass.  A workgroup has 64 columns of a block
+// and each of its four waves 32 k of them, a column to a lane; LDS joins the
+// waves' ranges, and puts the words of a column together, so that the codes leave
+// as whole lines (4096 x 4096, groups of 128: 11.5 us; a thread with all 128 k of one
+// column 14.8, of two 19.4; scales and codes in two passes, with two divisions, 54).
 template <int G, bool ZEROS>
 __global__ void __launch_bounds__(256) k_w4_quantize(QuantArgs a) {
-    const int n = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+    constexpr int PIECES = G / 32;             // waves that share a group
+    __shared__ float low[4][64], high[4][64];
+    __shared__ uint32_t words[64][17];         // (a column's 16; 17 spread over the banks)
+    const int tid = threadIdx.x, lane = tid & 63, j = tid >> 6, b = blockIdx.y;
+    const int n0 = blockIdx.x * 64, n = min(n0 + lane, a.N - 1);
     const int64_t e = blockIdx.z;
-    if (n >= a.N) return;
-    const unsigned char *w = a.W + e * a.stride_w + (int64_t)b * BLOCK * a.ldw + (int64_t)n * 2;
-    const int left = a.K - b * BLOCK;
-    u32x4 word[4] = {};
+    const int k0 = b * BLOCK + 32 * j, left = a.K - k0;
+    const unsigned char *w = a.W + e * a.stride_w + (int64_t)k0 * a.ldw + (int64_t)n * 2;
+    _Float16 v[32];
+    if (left >= 32) {
 #pragma unroll
-    for (int g = 0; g < BLOCK / G; g++) {
-        if (g * G >= left) break;
-        _Float16 v[G];
-        if (left >= (g + 1) * G) {
+        for (int k = 0; k < 32; k++) v[k] = *(const _Float16 *)(w + k * a.ldw);
+    } else {
 #pragma unroll
-            for (int k = 0; k < G; k++) v[k] = *(const _Float16 *)(w + (g * G + k) * a.ldw);
-        } else {
+        for (int k = 0; k < 32; k++) v[k] = k < left ? *(const _Float16 *)(w + k * a.ldw) : (_Float16)0.0f;
+    }
+    float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-            for (int k = 0; k < G; k++)
-                v[k] = g * G + k < left ? *(const _Float16 *)(w + (g * G + k) * a.ldw) : (_Float16)0.0f;
-        }
-        float lo = 0.0f, hi = 0.0f;
+    for (int k = 0; k < 32; k++) widen<ZEROS>((float)v[k], lo, hi);
+    if constexpr (PIECES > 1) {
+        low[j][lane] = lo, high[j][lane] = hi;
+        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < G; k++) widen<ZEROS>((float)v[k], lo, hi);
-        const ScaleZero sz = scale_of<ZEROS>(lo, hi);
-        store_scale<ZEROS>(a, e, b * (BLOCK / G) + g, n, sz);
-#pragma unroll
-        for (int k = 0; k < G; k++) {
-            const int at = g * G + k;
-            uint32_t code = code_of((float)v[k], sz);
-            if (at >= left) code = 0;
-            word[at % 32 / 8][at / 32] |= code << nibble_at(at % 8);
+        for (int i = 0; i < PIECES; i++) {
+            const int of = j / PIECES * PIECES + i;
+            lo = fminf(lo, low[of][lane]), hi = fmaxf(hi, high[of][lane]);
         }
     }
-    u32x4 *out = (u32x4 *)(a.q.codes + e * a.q.stride_codes + b * a.q.ld_codes + (int64_t)n * 64);
+    const ScaleZero sz = scale_of<ZEROS>(lo, hi);
+    if (j % PIECES == 0 && left > 0 && n0 + lane < a.N) store_scale<ZEROS>(a, e, k0 / G, n, sz);
 #pragma unroll
-    for (int q = 0; q < 4; q++) out[q] = word[q];
+    for (int q = 0; q < 4; q++) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) word |= code_of((float)v[8 * q + i], sz) << nibble_at(i);
+        if (left < 8 * q + 8) {  // no codes from the end of k on
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (8 * q + i >= left) word &= ~(15u << nibble_at(i));
+        }
+        words[lane][4 * q + j] = word;
+    }
+    __syncthreads();
+    const int col = tid >> 2, q = tid & 3;
+    if (n0 + col >= a.N) return;
+    u32x4 out;
+#pragma unroll
+    for (int i = 0; i < 4; i++) out[i] = words[col][4 * q + i];
+    *(u32x4 *)(a.q.codes + e * a.q.stride_codes + b * a.q.ld_codes + (int64_t)n0 * 64 + tid * 16) = out;
 }
 
 // Scales of groups of any length: a workgroup has 64 columns of one group, its
@@ -438,14 +455,14 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
     const unsigned char *codes = w.codes + (int64_t)first * 64;
     // The lane's next scale: its column, k, and k counted from its group's start.
     int at_k[T::SCALE_COPIES], into[T::SCALE_COPIES];
-    const unsigned char *scale[T::SCALE_COPIES], *zero[T::SCALE_COPIES];
+    const unsigned char *scales[T::SCALE_COPIES], *zeros[T::SCALE_COPIES];
 #pragma unroll
     for (int i = 0; i < T::SCALE_COPIES; i++) {
         at_k[i] = min(i * T::AT_ONCE + lane / (16 * T::CT), T::SCALES - 1) * 32 * T::SPAN;
         const int own = min(lane % (16 * T::CT), last), g = at_k[i] / p.group;
         into[i] = at_k[i] - g * p.group;
-        scale[i] = w.scales + g * w.ld_scales + (int64_t)(first + own) * 2;
-        if constexpr (T::ZEROS) zero[i] = w.zeros + g * w.ld_zeros + first + own;
+        scales[i] = w.scales + g * w.ld_scales + (int64_t)(first + own) * 2;
+        if constexpr (T::ZEROS) zeros[i] = w.zeros + g * w.ld_zeros + first + own;
     }
 
     // (Blocks are copied in order: each moves codes, scales and zeros on.)
@@ -482,16 +499,16 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
         for (int i = 0; i < T::SCALE_COPIES; i++) {
             // (From the end of k on there are no groups: zeros.)
             const unsigned char *none = (const unsigned char *)tdg_zero16;
-            copy_word_to_lds<2>(at_k[i] < p.K ? scale[i] : none, mine + T::CODE_BYTES + i * 256);
+            copy_word_to_lds<2>(at_k[i] < p.K ? scales[i] : none, mine + T::CODE_BYTES + i * 256);
             if constexpr (T::ZEROS)
-                copy_word_to_lds<1>(at_k[i] < p.K ? zero[i] : none, mine + T::CODE_BYTES + T::SCALE_BYTES + i * 256);
+                copy_word_to_lds<1>(at_k[i] < p.K ? zeros[i] : none, mine + T::CODE_BYTES + T::SCALE_BYTES + i * 256);
             at_k[i] += BLOCK, into[i] += BLOCK;
 #pragma unroll
             for (int j = 0; j < T::SCALES; j++) {  // on to the group that holds k of the next block
                 const bool on = into[i] >= p.group;
                 into[i] -= on ? p.group : 0;
-                scale[i] += on ? w.ld_scales : 0;
-                if constexpr (T::ZEROS) zero[i] += on ? w.ld_zeros : 0;
+                scales[i] += on ? w.ld_scales : 0;
+                if constexpr (T::ZEROS) zeros[i] += on ? w.ld_zeros : 0;
             }
         }
     };
@@ -771,13 +788,14 @@ int tdg_w4_quantize(int64_t count, int64_t K, int64_t N, int64_t group, const ui
     const dim3 scale_grid = grid_of(ceil_quot(N, 64), q.groups(), count);
     const dim3 code_grid = grid_of(ceil_quot(N, 256), q.blocks(), count);
     const bool once = group == 32 || group == 64 || group == 128;
-    if ((!once && !grid_ok(scale_grid, 256)) || !grid_ok(code_grid, 256)) return TDG_ERR_UNSUPPORTED;
+    const dim3 once_grid = grid_of(ceil_quot(N, 64), q.blocks(), count);
+    if (once ? !grid_ok(once_grid, 256) : !grid_ok(scale_grid, 256) || !grid_ok(code_grid, 256)) return TDG_ERR_UNSUPPORTED;
     int rc = device_check();
     if (rc != TDG_OK) return rc;
 #define TDG_W4_ONCE(G) (zeros ? (const void *)&k_w4_quantize<G, true> : (const void *)&k_w4_quantize<G, false>)
     if (once)
-        return launch(group == 32 ? TDG_W4_ONCE(32) : group == 64 ? TDG_W4_ONCE(64) : TDG_W4_ONCE(128), code_grid, 256,
-                      &a, stream);
+        return launch(group == 32 ? TDG_W4_ONCE(32) : group == 64 ? TDG_W4_ONCE(64) : TDG_W4_ONCE(128),
+                      once_grid, 256, &a, stream);
 #undef TDG_W4_ONCE
     rc = launch(zeros ? (const void *)&k_w4_scales<true> : (const void *)&k_w4_scales<false>, scale_grid, 256, &a,
                 stream);
