@@ -587,7 +587,8 @@ int gemm_f16w4f32_grouped(int64_t groups, const int32_t *offsets, int64_t M, int
  * more than TDG_LAYER_MAX_TOKENS tokens or TDG_LAYER_MAX_TOP_K choices are
  * TDG_ERR_UNSUPPORTED: sorted rows and grouped products are for those.  The
  * workspace (tdg_expert_layer_workspace) is 16-byte aligned; its contents on
- * return are unspecified. */
+ * return are unspecified, and its size does not grow with the tokens throughout:
+ * one for calls of several sizes is as large as the largest that they need. */
 #define TDG_LAYER_MAX_TOKENS 64
 #define TDG_LAYER_MAX_TOP_K 32
 int tdg_expert_layer_workspace(int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int64_t inner,

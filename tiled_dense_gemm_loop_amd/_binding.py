@@ -1112,7 +1112,8 @@ TDG_LAYER_MAX_TOP_K = 32
 
 
 def tdg_expert_layer_workspace(tokens: int, top_k: int, experts: int, cols: int, inner: int) -> int:
-    """Bytes of workspace that tdg_expert_layer needs."""
+    """Bytes of workspace that tdg_expert_layer needs (not growing with the
+    tokens throughout: for several sizes take the largest)."""
     need = ctypes.c_size_t()
     rc = _fn("tdg_expert_layer_workspace")(tokens, top_k, experts, cols, inner, ctypes.byref(need))
     if rc != TDG_OK:
