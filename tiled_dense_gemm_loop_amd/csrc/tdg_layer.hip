@@ -25,8 +25,6 @@ namespace {
 using namespace tdg;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int MAX_ENTRIES = TDG_LAYER_MAX_TOKENS * TDG_LAYER_MAX_TOP_K;
 
@@ -261,10 +259,9 @@ __device__ __forceinline__ void join_token(const LayerArgs &p, int t, int n) {
 
 // The down product of up to 16 rows of an expert: a workgroup has 16 V columns,
 // lane l loads V of them at k = 4 q .. + 3 of each 16, q = l / 16, and the e-th
-// products take row e of those.  FOURS = 0: v_mfma_f32_16x16x4_f32, a product of 16
-// rows at the four k of the lane groups.  FOURS = 1: four rows on
-// v_mfma_f32_4x4x1_16b_f32, a quarter of its time: 16 blocks of
-// four lanes' columns, each at its own lanes' k, so that a column's sum is spread
+// products take row e of those.  Without FOURS v_mfma_f32_16x16x4_f32, a
+// product of 16 rows at the four k of the lane groups; with it four rows on
+// v_mfma_f32_4x4x1_16b_f32, a quarter of its time: 16 blocks of four lanes' columns, each at its own lanes' k, so that a column's sum is spread
 // over the four lane groups, and added at the end.  Most experts of a few tokens
 // have four rows or fewer, and the time of 16 rows' products shows: it is as long
 // as that of reading the weights (16 tokens, 8 of 64 experts, 2048 x 1024: 47 us

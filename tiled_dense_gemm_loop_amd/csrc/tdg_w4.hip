@@ -45,7 +45,7 @@ struct QuantArgs {
     const unsigned char *W;
     int64_t ldw, stride_w;  // bytes
     Weights4 q;             // written
-    int K, N, group, groups, blocks;
+    int K, N, group;
 };
 
 struct ScaleZero {
@@ -62,7 +62,7 @@ __device__ __forceinline__ ScaleZero scale_of(float lo, float hi) {
     return {s, 1.0f / s, s > 0.0f && z >= 0.0f ? fminf(z, 15.0f) : 0.0f};
 }
 
-// The code of w: the nearest of the 16 values.  The quotient is w / r with one
+// The code of w: the nearest of the 16 values.  The quotient is w * r with one
 // correction.  A quotient of two FP16 numbers that is half a whole number below
 // 16 comes out exactly (the correction's own error is far below half a step),
 // and any other lies at least 2^-13 from such a one: the code is that of the
@@ -649,7 +649,7 @@ struct Named4 {
 QuantArgs quant_args(const Named4 &q, const void *W, int64_t ldw, int64_t stride_w, int64_t es) {
     QuantArgs a;
     a.W = (const unsigned char *)W, a.ldw = ldw * es, a.stride_w = stride_w * es, a.q = q.device();
-    a.K = (int)q.K, a.N = (int)q.N, a.group = (int)q.group, a.groups = (int)q.groups(), a.blocks = (int)q.blocks();
+    a.K = (int)q.K, a.N = (int)q.N, a.group = (int)q.group;
     return a;
 }
 
@@ -714,8 +714,8 @@ Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
     // 16 / 32 / 64 columns: 16 x 4096 x 4096, 256 pieces, 6.6 / 7.2 / -; 24 rows,
     // 512, 9.7 / 7.5 / 8.7; 64 rows, 1024, 15.0 / 12.2 / 9.2; 1 x 16384 x 4096,
     // 1024, - / 10.6 / 10.2); then two row tiles (128 rows, 2048: 15.7 with one,
-    // 13.7 with two, 32 x 64 tiles from LDS 16.1; 192 rows, 3072: 21.0, 24.8,
-    // 18.8; 32 x 16384 x 4096, 2048: 16.9, 15.0, 21).  Groups of rows: up to 8 to a
+    // 13.7 with two, 32 x 64 tiles from LDS 16.1; 192 rows: 21.0, 24.8, 18.8; 32
+    // x 16384 x 4096, 2048: 16.9, 15.0, 21).  Groups of rows: up to 8 to a
     // group (32 groups of 2048 x 2048, 200 rows: 17.9, tiles 19.2; 400: 22.6, 19.6).
     const bool short_groups = p.rows <= 8 * live;
     if (far || p.blocks == 0 || (p.offsets ? short_groups : p.rows <= 32 || pieces <= 2048)) {
