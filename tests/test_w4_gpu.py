@@ -460,7 +460,7 @@ def test_grouped_one_matrix_for_all_groups(lib):
 
 # (rows, matrices or 0 for the plain product, N, K): 128 x 512, 64 x 256, 64 x 128,
 # 32 x 128 and 32 x 64 tiles and the kernels of few rows, by the rule that picks them.
-TILES = [(1030, 0, 13000, 130), (1100, 0, 6000, 155), (700, 0, 3000, 256), (70, 0, 8200, 300), (130, 0, 3900, 200),
+TILES = [(1000, 0, 3500, 130), (450, 0, 3900, 257), (1030, 0, 13000, 130), (1100, 0, 6000, 155), (700, 0, 3000, 256), (70, 0, 8200, 300), (130, 0, 3900, 200),
          (40, 0, 4100, 129), (24, 0, 4100, 384), (9, 0, 300, 8200), (2100, 2, 6600, 70), (2000, 6, 3300, 257),
          (1000, 5, 2000, 128), (700, 40, 800, 200), (300, 20, 300, 391), (150, 30, 500, 140)]
 

@@ -284,6 +284,7 @@ __device__ __forceinline__ void down_rows(const LayerArgs &p, const unsigned cha
         const int len = (s1 - s0) * 16;
         if (rows * len > 256) join_h<PARTS, 4>(p, list, rows, s0 * 16, len, lane, piece);
         else join_h<PARTS, 1>(p, list, rows, s0 * 16, len, lane, piece);
+        __builtin_amdgcn_wave_barrier();  // (the wave's own piece: no other wave reads it)
     }
     const int row = min(FOURS ? lane & 3 : c, rows - 1);  // (rows behind the last: not stored)
     const float *h = JOIN ? piece + row * (s1 - s0) * 16 - s0 * 16 : p.h + list[row] * p.ld_h;

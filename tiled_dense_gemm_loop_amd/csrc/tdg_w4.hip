@@ -525,9 +525,12 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
         const unsigned char *at = smem + (b & 1) * T::STAGE, *mine = at + T::A_BYTES + wave * T::WAVE_BYTES;
         f16x8 v[T::CT][4];
         float scale[T::CT][T::SCALES];
+        u32x4 words[T::CT];
+#pragma unroll
+        for (int t = 0; t < T::CT; t++) words[t] = lds_read16(mine + t * 1024 + c * 64 + ((q ^ (c >> 2)) << 4));
 #pragma unroll
         for (int t = 0; t < T::CT; t++) {
-            const u32x4 word = lds_read16(mine + t * 1024 + c * 64 + ((q ^ (c >> 2)) << 4));
+            const u32x4 word = words[t];
 #pragma unroll
             for (int g = 0; g < T::SCALES; g++) {
                 const uint32_t bits = *(const TDG_LDS uint32_t *)(mine + T::CODE_BYTES + ((g * T::CT + t) * 16 + c) * 4);
@@ -576,8 +579,9 @@ __device__ __forceinline__ void w4_tile(const W4Args &p, const Weights4 &w, int 
         }
 }
 
+// (Registers for four waves to a SIMD: two workgroups of eight waves to a CU.)
 template <int MT, int CT, int WAVES, int SPAN, bool ZEROS>
-__global__ void __launch_bounds__(WAVES * 64) k_w4_tile(W4Args p) {
+__global__ void __launch_bounds__(WAVES * 64, MT == 8 ? 2 : 4) k_w4_tile(W4Args p) {
     typedef W4Tile<MT, CT, WAVES, SPAN, ZEROS> T;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * T::STAGE];
     poison_lds<2 * T::STAGE, T::THREADS>(p.flags, smem);
