@@ -221,6 +221,30 @@ def test_dequantize_gives_back_what_quantize_rounded(lib):
     assert ((back.cpu().double() - w.double()).abs() <= step * (0.5 + 8 * 2.0 ** -11 + 7 * 2.0 ** -11)).all()
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("wide,apart", [(0, 0), (2, 0), (1, 0), (2, 1), (14, 64)])
+def test_stacks_of_many_workgroups(lib, wide, apart, dtype):
+    """More workgroups than one round of places, and a last one that is not full; rows and
+    matrices that start at whole lines, at multiples of 4 bytes, at odd elements."""
+    count, K, N, group = 5, 290, 2034, 64
+    ws = [Weights(rng(31, e), K, N, group, True) for e in range(count)]
+    ld = N + wide
+    stride = K * ld + apart
+    flat = torch.full((count * stride,), -7.0, dtype=dtype, device="cuda")
+    out = flat.as_strided((count, K, N), (stride, ld, 1))
+    lib.tdg_w4_dequantize(*stacked(ws), K=K, group=group, out=out)
+    for e in range(count):
+        assert torch.equal(out[e].cpu(), ws[e].value.to(dtype))
+    assert int((flat == -7.0).sum()) >= count * (K * wide + apart)
+    rest = flat.clone()
+    rest.as_strided((count, K, N), (stride, ld, 1)).fill_(-7.0)
+    assert (rest == -7.0).all()
+    if dtype == F16:
+        got = lib.tdg_w4_quantize(out, group, True)
+        for e in range(count):
+            check_quantized([t[e] for t in got], ws[e].value.to(F16), group, True)
+
+
 # ------------------------------------------------------------------ the product
 
 PRODUCTS = [(1, 1, 1, 32), (1, 16, 32, 32), (1, 17, 33, 64), (2, 100, 128, 128), (3, 64, 129, 32), (15, 33, 500, 96),

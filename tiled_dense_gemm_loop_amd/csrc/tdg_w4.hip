@@ -46,7 +46,25 @@ struct QuantArgs {
     int64_t ldw, stride_w;  // bytes
     Weights4 q;             // written
     int K, N, group;
+    int run;  // neighbours that one XCD takes
 };
+
+struct Place {
+    int x, y, z;
+};
+
+// The workgroup's place in its grid.  Workgroups are dealt round-robin to the 8
+// XCDs; here each takes `run` neighbours of a row, so that a line that two of
+// them share is read, or put together, in one L2.
+__device__ __forceinline__ Place place_in_runs(uint32_t run) {
+    if (run == 1) return {(int)blockIdx.x, (int)blockIdx.y, (int)blockIdx.z};
+    const uint32_t total = gridDim.x * gridDim.y * gridDim.z, round = 8 * run;
+    uint32_t id = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    const uint32_t in = id % round;
+    if (id - in + round <= total) id += (in & 7) * run + (in >> 3) - in;  // (the last round stays as it is)
+    const uint32_t row = id / gridDim.x, z = row / gridDim.y;
+    return {(int)(id - row * gridDim.x), (int)(row - z * gridDim.y), (int)z};
+}
 
 struct ScaleZero {
     float s, r, z;  // r: 1 / s
@@ -94,14 +112,17 @@ __device__ __forceinline__ void store_scale(const QuantArgs &a, int64_t e, int g
 // waves' ranges, and puts the words of a column together, so that the codes leave
 // as whole lines (4096 x 4096, groups of 128: 11.5 us; a thread with all 128 k of one
 // column 14.8, of two 19.4; scales and codes in two passes, with two divisions, 54).
+// Rows that start inside lines: runs of 8 places (8 of 1000 x 4095, groups of 64:
+// 21.2 us, 24.4 without; rows of whole lines 11.8, and 11.4 without).
 template <int G, bool ZEROS>
 __global__ void __launch_bounds__(256) k_w4_quantize(QuantArgs a) {
     constexpr int PIECES = G / 32;             // waves that share a group
     __shared__ float low[4][64], high[4][64];
     __shared__ uint32_t words[64][17];         // (a column's 16; 17 spread over the banks)
-    const int tid = threadIdx.x, lane = tid & 63, j = tid >> 6, b = blockIdx.y;
-    const int n0 = blockIdx.x * 64, n = min(n0 + lane, a.N - 1);
-    const int64_t e = blockIdx.z;
+    const Place at = place_in_runs(a.run);
+    const int tid = threadIdx.x, lane = tid & 63, j = tid >> 6, b = at.y;
+    const int n0 = at.x * 64, n = min(n0 + lane, a.N - 1);
+    const int64_t e = at.z;
     const int k0 = b * BLOCK + 32 * j, left = a.K - k0;
     const unsigned char *w = a.W + e * a.stride_w + (int64_t)k0 * a.ldw + (int64_t)n * 2;
     _Float16 v[32];
@@ -199,45 +220,76 @@ __global__ void __launch_bounds__(256) k_w4_codes(QuantArgs a) {
     for (int q = 0; q < 4; q++) out[q] = word[q];
 }
 
-// Weights from codes: a thread has V neighbouring columns of a block (the last
-// ones end with the matrix, and write again what their neighbours write).
+// Weights from codes: a workgroup has 128 columns of a block, whose codes come
+// as whole lines and turn in LDS, so that a thread has V columns by 64 / V k and
+// a row's pieces are stored next to each other: 16 bytes to a lane, or 4 where
+// rows of FP16 start at odd elements (V = 8 / 4 / 2: 4096 x 4096 8.0 / 8.1 / 8.8 us,
+// in FP32 17.5 / 15.3 / 17.2; 8 of 1000 x 4095 20.0 / 17.5 / 15.1; a thread with all
+// 128 k of two columns 11.2 and 16.2).  Places in runs of 8: 9.4 without.
 template <typename T, bool ZEROS, int V>
 __global__ void __launch_bounds__(256) k_w4_values(QuantArgs a) {
+    constexpr int ACROSS = 128 / V, WORDS = 8 / V;  // threads to a row; words of 8 k to a thread's column
     typedef T vec __attribute__((ext_vector_type(V)));
     typedef vec vec_ua __attribute__((aligned(sizeof(T))));
-    const int want = (blockIdx.x * 256 + threadIdx.x) * V, n = min(want, a.N - V), b = blockIdx.y;
-    const int64_t e = blockIdx.z;
-    if (want >= a.N) return;
-    unsigned char *w = (unsigned char *)a.W + e * a.stride_w + (int64_t)b * BLOCK * a.ldw + (int64_t)n * sizeof(T);
-    const u32x4 *in = (const u32x4 *)(a.q.codes + e * a.q.stride_codes + b * a.q.ld_codes + (int64_t)n * 64);
-    u32x4 word[V][4];
+    typedef _Float16 halves __attribute__((ext_vector_type(V)));
+    typedef halves halves_ua __attribute__((aligned(2)));
+    typedef unsigned char bytes __attribute__((ext_vector_type(V)));
+    typedef bytes bytes_ua __attribute__((aligned(1)));
+    __shared__ __attribute__((aligned(16))) uint32_t words[16][128 + 4];  // (4: the writes' banks)
+    const Place at = place_in_runs(a.run);
+    const int tid = threadIdx.x, n0 = at.x * 128, b = at.y;
+    const int64_t e = at.z;
+    const unsigned char *codes = a.q.codes + e * a.q.stride_codes + b * a.q.ld_codes;
+    u32x4 in[2];
 #pragma unroll
-    for (int v = 0; v < V; v++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) word[v][q] = in[v * 4 + q];
-    const int left = a.K - b * BLOCK;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        if (32 * j >= left) break;
-        const int g = (b * BLOCK + 32 * j) / a.group;
-        float s[V], z[V];
+    for (int i = 0; i < 2; i++)
+        in[i] = *(const u32x4 *)(codes + (int64_t)min(n0 + 64 * i + (tid >> 2), a.N - 1) * 64 + (tid & 3) * 16);
+    // The thread's columns from n on, k from k0 on: all in one group.
+    const int c = tid % ACROSS * V, n = n0 + c, first = tid / ACROSS * WORDS, have = min(a.N - n, V);
+    const int k0 = b * BLOCK + first * 8, left = a.K - k0, g = min(k0, a.K - 1) / a.group;
+    const unsigned char *scales = a.q.scales + e * a.q.stride_scales + g * a.q.ld_scales + (int64_t)n * 2;
+    const unsigned char *zeros = a.q.zeros + e * a.q.stride_zeros + g * a.q.ld_zeros + n;
+    halves s = {};
+    bytes z = {};
+    if (have == V) {
+        s = *(const halves_ua *)scales;
+        if constexpr (ZEROS) z = *(const bytes_ua *)zeros;
+    } else {
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            s[v] = load_weight(a.q.scales + e * a.q.stride_scales + g * a.q.ld_scales + (int64_t)(n + v) * 2);
-            z[v] = ZEROS ? (float)a.q.zeros[e * a.q.stride_zeros + g * a.q.ld_zeros + n + v] : 8.0f;
+            if (v >= have) continue;
+            s[v] = *(const _Float16 *)(scales + v * 2);
+            if constexpr (ZEROS) z[v] = zeros[v];
         }
+    }
 #pragma unroll
-        for (int q = 0; q < 4; q++)
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int k = 32 * j + 8 * q + i;
-                if (k >= left) break;
-                vec out;
+        for (int j = 0; j < 4; j++) words[(tid & 3) * 4 + j][64 * i + (tid >> 2)] = in[i][j];
+    __syncthreads();
+    if (have <= 0) return;
+    unsigned char *w = (unsigned char *)a.W + e * a.stride_w + (int64_t)k0 * a.ldw + (int64_t)n * sizeof(T);
+#pragma unroll
+    for (int u = 0; u < WORDS; u++) {
+        uint32_t word[V];
+#pragma unroll
+        for (int v = 0; v < V; v++) word[v] = words[((first + u) & 3) * 4 + ((first + u) >> 2)][c + v];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (u * 8 + i >= left) return;
+            vec out;
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                out[v] = (T)(((float)(word[v] >> nibble_at(i) & 15) - (ZEROS ? (float)z[v] : 8.0f)) * (float)s[v]);
+            unsigned char *to = w + (u * 8 + i) * a.ldw;
+            if (have == V) {
+                *(vec_ua *)to = out;
+            } else {
 #pragma unroll
                 for (int v = 0; v < V; v++)
-                    out[v] = (T)(((float)(word[v][q][j] >> nibble_at(i) & 15) - z[v]) * s[v]);
-                *(vec_ua *)(w + k * a.ldw) = out;
+                    if (v < have) *(T *)(to + v * sizeof(T)) = out[v];
             }
+        }
     }
 }
 
@@ -792,6 +844,8 @@ int tdg_w4_quantize(int64_t count, int64_t K, int64_t N, int64_t group, const ui
     const dim3 scale_grid = grid_of(ceil_quot(N, 64), q.groups(), count);
     const dim3 code_grid = grid_of(ceil_quot(N, 256), q.blocks(), count);
     const bool once = group == 32 || group == 64 || group == 128;
+    const bool lines = aligned_to(W, 128) && ldw % 64 == 0 && (count == 1 || stride_w % 64 == 0);
+    a.run = lines ? 1 : 8;
     const dim3 once_grid = grid_of(ceil_quot(N, 64), q.blocks(), count);
     if (once ? !grid_ok(once_grid, 256) : !grid_ok(scale_grid, 256) || !grid_ok(code_grid, 256)) return TDG_ERR_UNSUPPORTED;
     int rc = device_check();
@@ -822,15 +876,15 @@ int tdg_w4_dequantize(int out_elem, int64_t count, int64_t K, int64_t N, int64_t
         return TDG_ERR_INVALID_ARG;
     if (count == 0 || K == 0 || N == 0) return TDG_OK;
     QuantArgs a = quant_args(q, W, ldw, stride_w, es);
-    const int V = N > 1 ? 2 : 1;
-    const dim3 grid = grid_of(ceil_quot(N, 256 * V), q.blocks(), count);
+    const dim3 grid = grid_of(ceil_quot(N, 128), q.blocks(), count);
     if (!grid_ok(grid, 256)) return TDG_ERR_UNSUPPORTED;
     const int rc = device_check();
     if (rc != TDG_OK) return rc;
-#define TDG_W4_VALUES(T)                                                                                        \
-    (V == 2 ? (zeros ? (const void *)&k_w4_values<T, true, 2> : (const void *)&k_w4_values<T, false, 2>)        \
-            : (zeros ? (const void *)&k_w4_values<T, true, 1> : (const void *)&k_w4_values<T, false, 1>))
-    const void *fn = half ? TDG_W4_VALUES(_Float16) : TDG_W4_VALUES(float);
+    a.run = 8;
+    // FP16 rows that all start at multiples of 4 bytes.
+    const bool even = aligned_to(W, 4) && ldw % 2 == 0 && (count == 1 || stride_w % 2 == 0);
+#define TDG_W4_VALUES(T, V) (zeros ? (const void *)&k_w4_values<T, true, V> : (const void *)&k_w4_values<T, false, V>)
+    const void *fn = !half ? TDG_W4_VALUES(float, 4) : even ? TDG_W4_VALUES(_Float16, 8) : TDG_W4_VALUES(_Float16, 2);
 #undef TDG_W4_VALUES
     return launch(fn, grid, 256, &a, stream);
 }
