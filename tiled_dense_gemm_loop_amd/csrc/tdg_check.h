@@ -74,4 +74,11 @@ inline bool stops_each(int64_t rows, int64_t cols, int64_t ld, int64_t count, in
 
 inline int64_t ceil_quot(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A dimension of a grid for `n` pieces of work.  What it does not hold, its
+// workgroups take one after the other, `step` apart: next_start is the start
+// behind `at`, or `end` where there is none.  No sum passes `end`, which may lie
+// less than a step below 2^31.  (The kernels call it too.)
+inline int64_t grid_dim(int64_t n) { return n < 65535 ? n : 65535; }
+constexpr int next_start(int at, int end, int step) { return end - at > step ? at + step : end; }
+
 }  // namespace tdg

@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(NW * 64) k_w4_few(W4Args p) {
     int col[CT];
 #pragma unroll
     for (int t = 0; t < CT; t++) col[t] = min((int)blockIdx.x * 16 * CT + t * 16 + c, p.N - 1);
-    for (int m0 = lo + (int)blockIdx.z * 16 * MT; m0 < hi; m0 += (int)gridDim.z * 16 * MT) {
+    const int step = (int)gridDim.z * 16 * MT;
+    for (int m0 = lo + (int)blockIdx.z * 16 * MT; m0 < hi; m0 = next_start(m0, hi, step)) {
         const unsigned char *row[MT];  // a lane behind the last row takes that one: its sums are not stored
 #pragma unroll
         for (int i = 0; i < MT; i++) row[i] = p.A + (int64_t)min(m0 + i * 16 + c, hi - 1) * p.lda + q * 16;
@@ -735,9 +736,8 @@ struct Variant4 {
 
 template <int MT, int CT, int NW>
 Variant4 few(const W4Args &p, const Named4 &q) {
-    const int64_t z = p.offsets ? 1 : ceil_quot(p.rows, 16 * MT);
-    return {TDG_W4_FN(k_w4_few, MT, CT, NW),
-            grid_of(ceil_quot(q.N, 16 * CT), p.row_groups, z > 65535 ? 65535 : z), NW * 64};
+    const int64_t z = p.offsets ? 1 : grid_dim(ceil_quot(p.rows, 16 * MT));
+    return {TDG_W4_FN(k_w4_few, MT, CT, NW), grid_of(ceil_quot(q.N, 16 * CT), p.row_groups, z), NW * 64};
 }
 
 // Tiles of bm x bn that a product is expected to have: half a row tile for each
