@@ -109,7 +109,15 @@ __device__ __forceinline__ void load_rows(typename Halves<V>::vec (&w)[N], const
     }
 }
 
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) * u.  Below -87 exp(-g) nears FP32's largest value, and from -88.8 on the
+// quotient would be 0: there 1 + exp(-g) is exp(-g) to the last bit, and g * exp(g)
+// * u is formed with a root of exp(g) on each side, so that it stays until it is
+// itself too small for FP32.
+__device__ __forceinline__ float gated(float g, float u) {
+    const bool low = g < -87.0f;
+    const float e = expf(low ? 0.5f * g : -g);
+    return low ? g * e * (u * e) : g / (1.0f + e) * u;
+}
 
 // Sums the waves' parts of one accumulator row, in order.
 template <int NW, int SIDES, int N>
