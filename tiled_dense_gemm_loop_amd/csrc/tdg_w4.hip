@@ -19,6 +19,7 @@
 
 #include "tdg_check.h"
 #include "tdg_internal.h"
+#include "tdg_w4_plan.h"
 
 namespace {
 
@@ -740,13 +741,6 @@ Variant4 few(const W4Args &p, const Named4 &q) {
     return {TDG_W4_FN(k_w4_few, MT, CT, NW), grid_of(ceil_quot(q.N, 16 * CT), p.row_groups, z), NW * 64};
 }
 
-// Tiles of bm x bn that a product is expected to have: half a row tile for each
-// group that can have rows, beside those that the rows fill.
-int64_t tiles_of(const W4Args &p, int64_t live, int64_t bm, int64_t bn) {
-    const int64_t high = p.offsets ? p.rows / bm + live / 2 : ceil_quot(p.rows, bm);
-    return (high > live ? high : live) * ceil_quot(p.N, bn);
-}
-
 template <class T>
 Variant4 tiled(W4Args &p, const Named4 &q, int64_t live, const void *fn) {
     p.tiles_m = (int)ceil_quot(p.rows, T::BM), p.tiles_n = (int)ceil_quot(q.N, T::BN);
@@ -761,46 +755,21 @@ Variant4 tiled(W4Args &p, const Named4 &q, int64_t live) {
 }
 
 Variant4 choose(W4Args &p, const Named4 &q, int64_t lda) {
-    const int64_t live = p.offsets ? (p.row_groups < p.rows ? p.row_groups : p.rows) : 1;
-    // Pieces of 16 rows by 16 columns.
-    const int64_t pieces = (p.offsets ? live : ceil_quot(p.rows, 16)) * ceil_quot(q.N, 16);
-    // The DMA's lanes reach a tile's rows with 32-bit byte offsets.
-    const bool far = lda > (int64_t)UINT32_MAX / 2 / 128 - 256;
-    // Few rows: as many columns to a workgroup as leave one or two to a CU (us,
-    // 16 / 32 / 64 columns: 16 x 4096 x 4096, 256 pieces, 6.6 / 7.2 / -; 24 rows,
-    // 512, 9.7 / 7.5 / 8.7; 64 rows, 1024, 15.0 / 12.2 / 9.2; 1 x 16384 x 4096,
-    // 1024, - / 10.6 / 10.2); then two row tiles (128 rows, 2048: 15.7 with one,
-    // 13.7 with two, 32 x 64 tiles from LDS 16.1; 192 rows: 21.0, 24.8, 18.8; 32
-    // x 16384 x 4096, 2048: 16.9, 15.0, 21).  Groups of rows: up to 8 to a
-    // group (32 groups of 2048 x 2048, 200 rows: 17.9, tiles 19.2; 400: 22.6, 19.6).
-    const bool short_groups = p.rows <= 8 * live;
-    if (far || p.blocks == 0 || (p.offsets ? short_groups : p.rows <= 32 || pieces <= 2048)) {
-        // 16 waves where k is long or so few rows that their loads do not count
-        // (us, 8 / 16 waves: 1 x 4096 x 4096 4.9 / 4.3, 1 x 512 x 8192 6.7 / 5.4, 16 x
-        // 4096 x 4096 6.6 / 6.9).
-        if (pieces <= 384) return (p.rows <= 4 || p.blocks >= 64) && !p.offsets ? few<1, 1, 16>(p, q) : few<1, 1, 8>(p, q);
-        if (pieces <= 640) return few<1, 2, 8>(p, q);
-        if (pieces <= 1280 || p.rows <= 16 || (p.offsets && short_groups)) return few<1, 4, 8>(p, q);
-        return few<2, 4, 8>(p, q);
-    }
-    // Tiles.  128 x 512, one to a CU, where its rounds of 256 are full (us, against
-    // 64 x 256: 4096 x 4096 x 4096, 256 tiles, 121 / 138; 3000 x 11008 x 2048, 528,
-    // 174 / 150; 16 groups of 1024 rows, 4096 x 4096, 1088 588 / 585).  Shorter
-    // groups' scales ask for more registers than there are (4096 x 8192 x 4096, groups
-    // of 64: 302 / 302, of 32: 471 / 351).
-    const int64_t large = tiles_of(p, live, 128, 512);
-    if (large * 100 > ceil_quot(large, 256) * 256 * 85 && p.rows >= 1024 * live && q.group % 128 == 0)
+    const W4Size size = {p.rows, p.offsets ? p.row_groups : 0, q.N, q.K, q.group, lda};
+    const int64_t live = size.live();
+    switch (w4_kernel(size)) {
+    case W4_FEW_1_1_16: return few<1, 1, 16>(p, q);
+    case W4_FEW_1_1_8: return few<1, 1, 8>(p, q);
+    case W4_FEW_1_2_8: return few<1, 2, 8>(p, q);
+    case W4_FEW_1_4_8: return few<1, 4, 8>(p, q);
+    case W4_FEW_2_4_8: return few<2, 4, 8>(p, q);
+    case W4_TILE_128_512:  // (groups of whole blocks alone)
         return tiled<W4Tile<8, 4, 8, 4, false>>(p, q, live, TDG_W4_SPAN(k_w4_tile, 4, 8, 4, 8));
-    // A few rows of each group: 32 x 128, or 64 wide (us, against 64 x 128 / 32 x 64:
-    // 32 groups of 2048 x 2048, 600 rows 20.3, 25.2 / 21.4; 1000 rows 25.4, 26.1 /
-    // 30.1; 2000 rows -, 32.7 / -; 9 groups of 1537 x 1000, 333 rows 8.6, 9.7 / 7.9).
-    if (p.rows <= 40 * live) return tiles_of(p, live, 32, 128) >= 256 ? tiled<2, 2, 4>(p, q, live) : tiled<2, 1, 4>(p, q, live);
-    // 64 x 256, two to a CU (us, against 64 x 128: 2048 x 4096 x 4096, 512 tiles, 73
-    // / 80; 1536 rows, 384, 64 / 60; 1024 rows, 256, 44 / 42); 64 x 128, three to a
-    // CU, against 32 x 64 (512 rows, 256 tiles: 29 / 30; 192 rows, 96: 26 / 19).
-    if (tiles_of(p, live, 64, 256) > 416) return tiled<4, 2, 8>(p, q, live);
-    if (tiles_of(p, live, 64, 128) >= 256) return tiled<4, 1, 8>(p, q, live);
-    return tiled<2, 1, 4>(p, q, live);
+    case W4_TILE_64_256: return tiled<4, 2, 8>(p, q, live);
+    case W4_TILE_64_128: return tiled<4, 1, 8>(p, q, live);
+    case W4_TILE_32_128: return tiled<2, 2, 4>(p, q, live);
+    default: return tiled<2, 1, 4>(p, q, live);
+    }
 }
 
 int run_product(int64_t row_groups, const int32_t *offsets, int64_t M, const Named4 &q, const void *A, int64_t lda,
