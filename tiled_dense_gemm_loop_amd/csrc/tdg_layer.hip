@@ -19,6 +19,7 @@
 
 #include "tdg_check.h"
 #include "tdg_internal.h"
+#include "tdg_layer_plan.h"
 
 namespace {
 
@@ -369,47 +370,6 @@ bool sizes_ok(int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int6
            size_ok(cols) && cols <= kMaxSize / 2 && size_ok(inner) && inner <= kMaxSize / 2;
 }
 
-int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
-
-int64_t at_most(int64_t n, int64_t most) { return n < most ? n : most; }
-
-// How the work is cut; a function of the sizes alone, as the workspace is.
-struct Plan {
-    int64_t slots, up_x, parts, down_x, parts_z, piece;
-    bool thin_up, thin_down, narrow;  // matrices below 8 columns; 64 instead of 128 columns of down to a workgroup
-    uint64_t z_at, bytes;
-};
-
-Plan make_plan(int64_t tokens, int64_t top_k, int64_t experts, int64_t cols, int64_t inner) {
-    Plan p;
-    const int64_t entries = tokens * top_k;
-    p.slots = entries < experts ? entries : experts;
-    // down: 128 columns and eight waves, k in two parts below 512 workgroups; 64
-    // columns and sixteen waves below 192 (us, 128 whole / 128 in two / 64 whole /
-    // 64 in two: 16 tokens, 1024 workgroups of 128, 50.7 / 51.4 / 56 / 65; 33
-    // tokens of 8 experts, 256, 22.3 / 20.2 / 23.3 / -; one token, 128, 10.9 / 9.3 /
-    // 8.5 / 9.7; 2 experts of 4096 x 4096, 64, - / 27 / 28 / 17).
-    p.thin_down = cols < 8;
-    const int64_t wide = ceil_quot(cols, 128) * p.slots;
-    p.narrow = !p.thin_down && wide < 192;
-    p.down_x = ceil_quot(cols, p.thin_down ? 16 : p.narrow ? 64 : 128);
-    p.parts_z = p.thin_down ? 1 : at_most(wide < 96 || (wide >= 192 && wide < 512) ? 2 : 1, inner / 256);
-    if (p.parts_z < 1) p.parts_z = 1;
-    // A CU takes about 35 GB/s from L2, so the weights need most CUs: k is cut in
-    // two or four where there are few workgroups (us, 1 / 2 / 4 parts: one token, 8
-    // experts of 2048 x 2 768, 48 workgroups, 17.3 / 12.5 / 11.4; two tokens, 96, 21
-    // / 18.7 / 21; 33 tokens, 8 experts of 4095 x 2 1001, 64, - / 33.8 / 32.9), if LDS
-    // holds what down then joins.
-    p.thin_up = inner < 8;
-    p.up_x = ceil_quot(inner, p.thin_up ? 16 : 128);
-    const int64_t wgs = p.up_x * p.slots, waves = p.narrow ? 16 : 8;
-    p.piece = ceil_quot(ceil_quot(inner, 16), waves * p.parts_z) * 16 * at_most(entries, 16);
-    p.parts = wgs > 96 || cols < 512 || p.piece * waves * 4 > 40 * 1024 ? 1 : wgs > 64 || cols < 1024 ? 2 : 4;
-    p.z_at = (uint64_t)(entries * up4(inner) * 4 * (p.parts > 1 ? 2 * p.parts : 1));
-    p.bytes = p.z_at + (uint64_t)(p.parts_z * entries * up4(cols) * 4);
-    return p;
-}
-
 int launch(const void *fn, dim3 grid, int threads, size_t lds, LayerArgs *args, void *stream) {
     void *kargs[] = {args};
     if (hipLaunchKernel(fn, grid, dim3((unsigned)threads), kargs, lds, (hipStream_t)stream) != hipSuccess)
@@ -426,7 +386,7 @@ int tdg_expert_layer_workspace(int64_t tokens, int64_t top_k, int64_t experts, i
                                size_t *bytes) {
     if (!bytes || !sizes_ok(tokens, top_k, experts, cols, inner)) return TDG_ERR_INVALID_ARG;
     if (tokens > TDG_LAYER_MAX_TOKENS || top_k > TDG_LAYER_MAX_TOP_K) return TDG_ERR_UNSUPPORTED;
-    *bytes = (size_t)make_plan(tokens, top_k, experts, cols, inner).bytes;
+    *bytes = (size_t)layer_plan(tokens, top_k, experts, cols, inner).bytes;
     return TDG_OK;
 }
 
@@ -463,7 +423,7 @@ int tdg_expert_layer(int out_elem, int64_t tokens, int64_t top_k, int64_t expert
     for (int i = 0; i < 5; i++)
         if (overlaps(workspace, need, in[i], in_len[i])) return TDG_ERR_INVALID_ARG;
 
-    const Plan plan = make_plan(tokens, top_k, experts, cols, inner);
+    const LayerPlan plan = layer_plan(tokens, top_k, experts, cols, inner);
     LayerArgs p;
     p.x = (const unsigned char *)x, p.up = (const unsigned char *)up, p.down = (const unsigned char *)down;
     p.ids = ids, p.weights = weights, p.y = (unsigned char *)y;
@@ -482,12 +442,9 @@ int tdg_expert_layer(int out_elem, int64_t tokens, int64_t top_k, int64_t expert
     int rc = device_check();
     if (rc != TDG_OK) return rc;
     if (inner > 0) {
-        // Two row tiles where many experts have more than one (us, one / two: 64
-        // tokens, 2 of 8 experts, 146 / 99; 8 of 64 experts 107.8 / 104.5; 33 tokens, 2
-        // of 8, 32.9 / 36.6).
-        const void *fn = plan.thin_up  ? (const void *)&k_layer_up<2, 1, 8>
-                         : p.entries > 10 * plan.slots ? (const void *)&k_layer_up<2, 8, 8>
-                                       : (const void *)&k_layer_up<1, 8, 8>;
+        const void *fn = plan.thin_up     ? (const void *)&k_layer_up<2, 1, 8>
+                         : plan.two_tiles ? (const void *)&k_layer_up<2, 8, 8>
+                                          : (const void *)&k_layer_up<1, 8, 8>;
         rc = launch(fn, dim3((unsigned)plan.up_x, (unsigned)plan.slots, (unsigned)plan.parts), 512, 0, &p, stream);
         if (rc != TDG_OK) return rc;
     }
