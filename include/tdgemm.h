@@ -546,7 +546,9 @@ int gemm_f16f32_lora(int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t
  *   dequantize  W = (code - zero) * scale, rounded once: FP16 or FP32
  *               (out_elem).
  * Both take up to 65535 matrices, blocks of 128 k and (quantize, groups other
- * than 32, 64 and 128) groups of k; more are TDG_ERR_UNSUPPORTED.
+ * than 32, 64 and 128) groups of k, and less than 2^24 of matrices times blocks (or
+ * those groups) times ceil(N / 64), dequantize ceil(N / 128); more are
+ * TDG_ERR_UNSUPPORTED.
  *
  * The products, FP16 rows -> FP32:
  *   gemm_f16w4f32          C[m][n] = sum over groups G of scale[G][n] * sum over

@@ -164,3 +164,31 @@ def test_host_tensors_and_wrong_types_are_refused():
                lambda: tdg.tdg_expert_layer(h.float(), ids, None, h[None], h[None])):
         with pytest.raises(TypeError):
             fn()
+
+
+# (what, group, the most columns of 65535 matrices of one block, and of 16 of 4095)
+MOST_COLUMNS = [("tdg_w4_quantize", QUANT, 64, 64 * 256, 64 * 256), ("tdg_w4_quantize", QUANT, 96, 64 * 256, 64 * 192),
+                ("tdg_w4_dequantize", DEQUANT, 64, 128 * 256, 128 * 256)]
+
+
+def _columns(args, count, K, N, group):
+    """The arguments for `count` dense matrices of K x N, each array far from the others."""
+    blocks, groups = -(-K // 128), -(-K // group)
+    return dict(args, count=count, K=K, N=N, group=group, w=1 << 55, ldw=N, stride_w=K * N, codes=2 << 55, ld_codes=N,
+                stride_codes=blocks * N, scales=3 << 55, ld_scales=N, stride_scales=groups * N, zeros=4 << 55,
+                ld_zeros=N, stride_zeros=groups * N)
+
+
+@pytest.mark.parametrize("name,args,group,one,many", MOST_COLUMNS)
+def test_more_columns_than_a_launch_holds_are_refused(name, args, group, one, many):
+    K = 128 if group == 64 else 96
+    assert call(name, _columns(args, 65535, K, one + 1, group)) == TOO_BIG
+    assert call(name, _columns(args, 16, 4095 * 128, many + 1, group)) == TOO_BIG
+
+
+@no_device_only
+@pytest.mark.parametrize("name,args,group,one,many", MOST_COLUMNS)
+def test_as_many_columns_as_a_launch_holds_are_taken(name, args, group, one, many):
+    K = 128 if group == 64 else 96
+    assert call(name, _columns(args, 65535, K, one, group)) == NODEV
+    assert call(name, _columns(args, 16, 4095 * 128, many, group)) == NODEV
