@@ -40,7 +40,7 @@ struct LayerArgs {
     int64_t ldx, ld_up, stride_up, ld_down, stride_down, ldy;     // bytes
     int64_t ld_ids, ld_weights;                                   // elements
     int64_t ld_h, ld_z;                                           // elements, multiples of 4
-    int tokens, top_k, experts, cols, inner, entries;
+    int top_k, experts, cols, inner, entries;
     int parts, parts_z;  // workgroups that share k: grid.z of the up and of the down product
     int piece;           // elements of h that a wave of down joins in LDS
 };
@@ -432,7 +432,7 @@ int tdg_expert_layer(int out_elem, int64_t tokens, int64_t top_k, int64_t expert
     p.h = (float *)workspace, p.z = (float *)((unsigned char *)workspace + plan.z_at);
     p.ldx = ldx * 2, p.ld_up = ld_up * 2, p.stride_up = stride_up * 2, p.ld_down = ld_down * 2;
     p.stride_down = stride_down * 2, p.ldy = ldy * es, p.ld_ids = ld_ids, p.ld_weights = ld_weights;
-    p.tokens = (int)tokens, p.top_k = (int)top_k, p.experts = (int)experts, p.cols = (int)cols;
+    p.top_k = (int)top_k, p.experts = (int)experts, p.cols = (int)cols;
     p.inner = (int)inner;
     p.parts = (int)plan.parts, p.parts_z = (int)plan.parts_z, p.piece = (int)plan.piece;
     const int64_t join_x = ceil_quot(cols, 256), most = (int64_t)UINT32_MAX / 1024;
